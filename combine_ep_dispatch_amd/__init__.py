@@ -16,20 +16,25 @@ Typical use (all tensors on one GPU, bf16 payloads as torch.bfloat16)::
     ep_dispatch(cfg, lay, x, recv)
     ...
     ep_combine(cfg, lay, expert_out, probs, y)
+
+The expert layer around them: ep_route (logits -> topk_ids, probs) before the
+layout, ep_expert_gemm / ep_swiglu / ep_expert_gemm (or ep_expert_gemm_nvfp4)
+between dispatch and combine, each with its backward calls.
 """
 
 from __future__ import annotations
 
 import ctypes
 import dataclasses
-from typing import NamedTuple, Optional
+from typing import NamedTuple, Optional, Sequence
 
 import torch
 
 from . import _lib
 from ._lib import (EP_FLAG_BAD_ID, EP_FLAG_DROPPED, EP_FLAG_INTERNAL, EP_FLAG_MAP_OVERFLOW,  # noqa: F401
                    EP_NOALLOC_SCRATCH_BYTES, EP_ZERO_PAD_ROWS, EP_LAYOUT_LOOKBACK, EP_LAYOUT_DIRECT,
-                   EP_LAYOUT_BARRIER, EP_LAYOUT_COUNT, EpCfg, EpLayout)
+                   EP_LAYOUT_BARRIER, EP_LAYOUT_COUNT, EP_GRAD_BF16, EP_GRAD_F32, EP_GRAD_F32_ADD,
+                   EP_SCORE_SIGMOID, EP_SCORE_SOFTMAX, EP_TYPE_BF16, EP_TYPE_F32, EpCfg, EpLayout, EpRoute)
 
 __all__ = [
     "EpConfig", "Layout", "QueryResult", "ep_query", "workspace_for", "ep_dispatch_layout",
@@ -38,6 +43,8 @@ __all__ = [
     "ep_dispatch", "ep_dispatch_nvfp4", "ep_dispatch_fp8", "ep_combine", "ep_dispatch_bwd", "ep_combine_bwd",
     "ep_combine_bwd_probs", "ep_indices_to_multihot", "ep_multihot_to_indices", "assert_no_overflow", "EpError", "abi_version", "EP_ZERO_PAD_ROWS", "EP_LAYOUT_LOOKBACK", "EP_LAYOUT_DIRECT", "EP_LAYOUT_BARRIER", "EP_LAYOUT_COUNT", "EP_FLAG_DROPPED",
     "EP_FLAG_BAD_ID", "EP_FLAG_INTERNAL",
+    "RouteConfig", "ep_route", "ep_route_bwd", "ep_swiglu", "ep_swiglu_bwd", "ep_expert_gemm",
+    "ep_expert_gemm_bwd_x", "ep_expert_gemm_bwd_w", "ep_expert_gemm_nvfp4",
 ]
 
 
@@ -397,6 +404,169 @@ def ep_multihot_to_indices(cfg: EpConfig, routing_map: torch.Tensor, dense_probs
         ctypes.byref(c), routing_map.data_ptr(), None if dense_probs is None else dense_probs.data_ptr(),
         topk_ids.data_ptr(), None if probs is None else probs.data_ptr(),
         None if flags is None else flags.data_ptr(), _stream(stream, dev)), "ep_multihot_to_indices")
+
+
+@dataclasses.dataclass
+class RouteConfig:
+    """How ep_route chooses and weights experts (ep_route_t in include/epx.h)."""
+
+    score: str = "softmax"  # or "sigmoid"
+    normalize: bool = True
+    num_groups: int = 1
+    top_groups: int = 1
+    scale: float = 1.0
+
+    def to_c(self, logits_dtype) -> EpRoute:
+        scores = {"softmax": EP_SCORE_SOFTMAX, "sigmoid": EP_SCORE_SIGMOID}
+        if self.score not in scores:
+            raise ValueError(f"score must be one of {sorted(scores)}, got {self.score!r}")
+        types = {torch.float32: EP_TYPE_F32, torch.bfloat16: EP_TYPE_BF16}
+        if logits_dtype not in types:
+            raise ValueError(f"logits must be torch.float32 or torch.bfloat16, got {logits_dtype}")
+        return EpRoute(scores[self.score], int(self.normalize), self.num_groups, self.top_groups, self.scale,
+                       types[logits_dtype], 0, 0)
+
+
+def _call(name: str, dev, stream, *args) -> None:
+    """Call `name` with `dev` current (the library launches on the current
+    device) and the stream last."""
+    if dev.index == torch.cuda.current_device():
+        status = getattr(_lib.lib(), name)(*args, _stream(stream, dev))
+    else:
+        with torch.cuda.device(dev):
+            status = getattr(_lib.lib(), name)(*args, _stream(stream, dev))
+    _check(status, name)
+
+
+def _ptr(t: Optional[torch.Tensor]):
+    return None if t is None else t.data_ptr()
+
+
+def ep_route(cfg: EpConfig, route: RouteConfig, logits: torch.Tensor, topk_ids: torch.Tensor, probs: torch.Tensor,
+             bias: Optional[torch.Tensor] = None, token_mask: Optional[torch.Tensor] = None, stream=None) -> None:
+    """logits [T, E] (float32 or bfloat16) -> topk_ids int32 [T, K] and probs
+    float32 [T, K]; bias float32 [E] shifts the choice, token_mask uint8 [T]
+    leaves tokens out."""
+    dev, T, E, K = logits.device, cfg.num_tokens, cfg.num_experts, cfg.top_k
+    r = route.to_c(logits.dtype)
+    _tensor(logits, "logits", logits.dtype, T * E)
+    _tensor(topk_ids, "topk_ids", torch.int32, T * K, dev)
+    _tensor(probs, "probs", torch.float32, T * K, dev)
+    if bias is not None:
+        _tensor(bias, "bias", torch.float32, E, dev)
+    if token_mask is not None:
+        _tensor(token_mask, "token_mask", torch.uint8, T, dev)
+    _call("ep_route", dev, stream, ctypes.byref(cfg.to_c()), ctypes.byref(r), logits.data_ptr(), _ptr(bias),
+          _ptr(token_mask), topk_ids.data_ptr(), probs.data_ptr())
+
+
+def ep_route_bwd(cfg: EpConfig, route: RouteConfig, logits: torch.Tensor, topk_ids: torch.Tensor,
+                 grad_probs: torch.Tensor, grad_logits: torch.Tensor, stream=None) -> None:
+    """grad_logits [T, E] (type of logits) from grad_probs float32 [T, K], the choice held fixed."""
+    dev, T, E, K = logits.device, cfg.num_tokens, cfg.num_experts, cfg.top_k
+    r = route.to_c(logits.dtype)
+    _tensor(logits, "logits", logits.dtype, T * E)
+    _tensor(topk_ids, "topk_ids", torch.int32, T * K, dev)
+    _tensor(grad_probs, "grad_probs", torch.float32, T * K, dev)
+    _tensor(grad_logits, "grad_logits", logits.dtype, T * E, dev)
+    _call("ep_route_bwd", dev, stream, ctypes.byref(cfg.to_c()), ctypes.byref(r), logits.data_ptr(),
+          topk_ids.data_ptr(), grad_probs.data_ptr(), grad_logits.data_ptr())
+
+
+def _columns(t: torch.Tensor, name: str, rows: int, dtype=torch.bfloat16, device=None) -> int:
+    """The row width of a [rows, width] buffer of the receive side."""
+    if t is None or t.dim() != 2 or t.shape[0] != rows:
+        raise ValueError(f"{name} must be [{rows}, columns], got {None if t is None else list(t.shape)}")
+    _tensor(t, name, dtype, rows * t.shape[1], device)
+    return t.shape[1]
+
+
+def _weights(cfg: EpConfig, t: torch.Tensor, name: str, dtype, shape: Sequence[int], device) -> None:
+    want = [cfg.num_experts + cfg.shared_expert, *shape]
+    _tensor(t, name, dtype, t.numel() if t is not None else 0, device)
+    if list(t.shape) != want:
+        raise ValueError(f"{name} must be {want}, got {list(t.shape)}")
+
+
+def ep_swiglu(cfg: EpConfig, layout: Layout, h: torch.Tensor, probs: Optional[torch.Tensor], act: torch.Tensor,
+              stream=None) -> None:
+    """act[r] = w * silu(gate) * up on the kept rows: h bf16 [R, 2*inter] (gate,
+    then up), probs float32 [T, K] or None (weight 1), act bf16 [R, inter]."""
+    dev, R = h.device, cfg.recv_rows
+    inter = _columns(act, "act", R, device=dev)
+    _tensor(h, "h", torch.bfloat16, R * 2 * inter)
+    if probs is not None:
+        _tensor(probs, "probs", torch.float32, cfg.num_tokens * cfg.top_k, dev)
+    layout.check(cfg, dev)
+    _call("ep_swiglu", dev, stream, ctypes.byref(cfg.to_c()), ctypes.byref(layout.to_c()), inter, h.data_ptr(),
+          _ptr(probs), act.data_ptr())
+
+
+def ep_swiglu_bwd(cfg: EpConfig, layout: Layout, h: torch.Tensor, probs: Optional[torch.Tensor],
+                  grad_act: torch.Tensor, grad_h: torch.Tensor, grad_probs: Optional[torch.Tensor] = None,
+                  stream=None) -> None:
+    """grad_h bf16 [R, 2*inter] and grad_probs float32 [T, K] (or None) from grad_act bf16 [R, inter]."""
+    dev, R = h.device, cfg.recv_rows
+    inter = _columns(grad_act, "grad_act", R, device=dev)
+    _tensor(h, "h", torch.bfloat16, R * 2 * inter)
+    _tensor(grad_h, "grad_h", torch.bfloat16, R * 2 * inter, dev)
+    for t, name in ((probs, "probs"), (grad_probs, "grad_probs")):
+        if t is not None:
+            _tensor(t, name, torch.float32, cfg.num_tokens * cfg.top_k, dev)
+    layout.check(cfg, dev)
+    _call("ep_swiglu_bwd", dev, stream, ctypes.byref(cfg.to_c()), ctypes.byref(layout.to_c()), inter, h.data_ptr(),
+          _ptr(probs), grad_act.data_ptr(), grad_h.data_ptr(), _ptr(grad_probs))
+
+
+def ep_expert_gemm(cfg: EpConfig, layout: Layout, x: torch.Tensor, w: torch.Tensor, y: torch.Tensor,
+                   stream=None) -> None:
+    """y[r] = w[expert of r] @ x[r]: x bf16 [R, in], w bf16 [E (+1 shared, last), out, in], y bf16 [R, out]."""
+    dev, R = x.device, cfg.recv_rows
+    n_in, n_out = _columns(x, "x", R), _columns(y, "y", R, device=dev)
+    _weights(cfg, w, "w", torch.bfloat16, (n_out, n_in), dev)
+    layout.check(cfg, dev)
+    _call("ep_expert_gemm", dev, stream, ctypes.byref(cfg.to_c()), ctypes.byref(layout.to_c()), n_in, n_out,
+          x.data_ptr(), w.data_ptr(), y.data_ptr())
+
+
+def ep_expert_gemm_bwd_x(cfg: EpConfig, layout: Layout, grad_y: torch.Tensor, w: torch.Tensor, grad_x: torch.Tensor,
+                         stream=None) -> None:
+    """grad_x[r] = grad_y[r] @ w[expert of r]: grad_y bf16 [R, out], grad_x bf16 [R, in]."""
+    dev, R = grad_y.device, cfg.recv_rows
+    n_in, n_out = _columns(grad_x, "grad_x", R, device=dev), _columns(grad_y, "grad_y", R)
+    _weights(cfg, w, "w", torch.bfloat16, (n_out, n_in), dev)
+    layout.check(cfg, dev)
+    _call("ep_expert_gemm_bwd_x", dev, stream, ctypes.byref(cfg.to_c()), ctypes.byref(layout.to_c()), n_in, n_out,
+          grad_y.data_ptr(), w.data_ptr(), grad_x.data_ptr())
+
+
+def ep_expert_gemm_bwd_w(cfg: EpConfig, layout: Layout, grad_y: torch.Tensor, x: torch.Tensor, grad_w: torch.Tensor,
+                         accumulate: bool = False, stream=None) -> None:
+    """grad_w[e] = sum over e's rows of grad_y[r]^T x[r]: grad_w bf16 or float32
+    [E (+1), out, in]; accumulate (float32 only) adds to what it holds."""
+    dev, R = grad_y.device, cfg.recv_rows
+    kinds = {torch.bfloat16: EP_GRAD_BF16, torch.float32: EP_GRAD_F32_ADD if accumulate else EP_GRAD_F32}
+    if grad_w.dtype not in kinds or (accumulate and grad_w.dtype != torch.float32):
+        raise ValueError(f"grad_w must be torch.float32{'' if accumulate else ' or torch.bfloat16'}, got {grad_w.dtype}")
+    n_in, n_out = _columns(x, "x", R, device=dev), _columns(grad_y, "grad_y", R)
+    _weights(cfg, grad_w, "grad_w", grad_w.dtype, (n_out, n_in), dev)
+    layout.check(cfg, dev)
+    _call("ep_expert_gemm_bwd_w", dev, stream, ctypes.byref(cfg.to_c()), ctypes.byref(layout.to_c()), n_in, n_out,
+          grad_y.data_ptr(), x.data_ptr(), grad_w.data_ptr(), kinds[grad_w.dtype])
+
+
+def ep_expert_gemm_nvfp4(cfg: EpConfig, layout: Layout, x: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor,
+                         rowscale: torch.Tensor, y: torch.Tensor, stream=None) -> None:
+    """ep_expert_gemm over 4-bit weights in the dispatch's NVFP4 row format: codes
+    uint8 [E (+1), out, in/2], scales uint8 (E4M3) [E (+1), out, in/16], rowscale bf16 [E (+1), out]."""
+    dev, R = x.device, cfg.recv_rows
+    n_in, n_out = _columns(x, "x", R), _columns(y, "y", R, device=dev)
+    _weights(cfg, codes, "codes", torch.uint8, (n_out, n_in // 2), dev)
+    _weights(cfg, scales, "scales", torch.uint8, (n_out, n_in // 16), dev)
+    _weights(cfg, rowscale, "rowscale", torch.bfloat16, (n_out,), dev)
+    layout.check(cfg, dev)
+    _call("ep_expert_gemm_nvfp4", dev, stream, ctypes.byref(cfg.to_c()), ctypes.byref(layout.to_c()), n_in, n_out,
+          x.data_ptr(), codes.data_ptr(), scales.data_ptr(), rowscale.data_ptr(), y.data_ptr())
 
 
 def assert_no_overflow(layout: Layout, capacity: Optional[int] = None) -> None:

@@ -27,13 +27,22 @@ EP_FLAG_BAD_ID = 2
 EP_FLAG_INTERNAL = 4
 EP_FLAG_MAP_OVERFLOW = 8
 EP_MAX_GROUPS = 2048
+EP_SCORE_SOFTMAX = 0
+EP_SCORE_SIGMOID = 1
+EP_TYPE_F32 = 0
+EP_TYPE_BF16 = 1
+EP_GRAD_BF16 = 0
+EP_GRAD_F32 = 1
+EP_GRAD_F32_ADD = 2
 
 # Every symbol include/epx.h declares.
 SYMBOLS = ("ep_query", "ep_dispatch_layout", "ep_dispatch", "ep_dispatch_nvfp4", "ep_dispatch_fp8",
            "ep_combine", "ep_dispatch_bwd", "ep_combine_bwd", "ep_combine_bwd_probs",
            "ep_indices_to_multihot", "ep_multihot_to_indices", "ep_dispatch_layout_noalloc",
            "ep_combine_nvfp4", "ep_dispatch_with_layout", "ep_dispatch_nvfp4_with_layout",
-           "ep_dispatch_fp8_with_layout", "ep_strerror", "ep_abi_version")
+           "ep_dispatch_fp8_with_layout", "ep_route", "ep_route_bwd", "ep_swiglu", "ep_swiglu_bwd",
+           "ep_expert_gemm", "ep_expert_gemm_bwd_x", "ep_expert_gemm_bwd_w", "ep_expert_gemm_nvfp4",
+           "ep_strerror", "ep_abi_version")
 
 
 class EpCfg(ctypes.Structure):
@@ -54,6 +63,14 @@ class EpLayout(ctypes.Structure):
     _fields_ = [(name, ctypes.c_void_p) for name in
                 ("counts", "seg_base", "row_offsets", "scales_offsets", "token_row", "expert_ids",
                  "src_info", "flags")]
+
+
+class EpRoute(ctypes.Structure):
+    """Mirror of ep_route_t."""
+
+    _fields_ = [("score", ctypes.c_int32), ("normalize", ctypes.c_int32), ("num_groups", ctypes.c_int32),
+                ("top_groups", ctypes.c_int32), ("scale", ctypes.c_float), ("logits_type", ctypes.c_int32),
+                ("reserved0", ctypes.c_int32), ("reserved1", ctypes.c_int32)]
 
 
 _lib = None
@@ -85,7 +102,16 @@ def lib():
         L.ep_dispatch_with_layout.argtypes = [cfg_p, P, P, I64, lay_p, P, P, P]
         L.ep_dispatch_nvfp4_with_layout.argtypes = [cfg_p, P, P, I64, lay_p, P, P, P, P, P]
         L.ep_dispatch_fp8_with_layout.argtypes = [cfg_p, P, P, I64, lay_p, P, P, P, P]
-        for name in SYMBOLS[:16]:
+        I32, route_p = ctypes.c_int32, ctypes.POINTER(EpRoute)
+        L.ep_route.argtypes = [cfg_p, route_p, P, P, P, P, P, P]
+        L.ep_route_bwd.argtypes = [cfg_p, route_p, P, P, P, P, P]
+        L.ep_swiglu.argtypes = [cfg_p, lay_p, I32, P, P, P, P]
+        L.ep_swiglu_bwd.argtypes = [cfg_p, lay_p, I32, P, P, P, P, P, P]
+        L.ep_expert_gemm.argtypes = [cfg_p, lay_p, I32, I32, P, P, P, P]
+        L.ep_expert_gemm_bwd_x.argtypes = [cfg_p, lay_p, I32, I32, P, P, P, P]
+        L.ep_expert_gemm_bwd_w.argtypes = [cfg_p, lay_p, I32, I32, P, P, P, I32, P]
+        L.ep_expert_gemm_nvfp4.argtypes = [cfg_p, lay_p, I32, I32, P, P, P, P, P, P]
+        for name in SYMBOLS[:-2]:
             getattr(L, name).restype = I
         L.ep_strerror.argtypes = [I]
         L.ep_strerror.restype = ctypes.c_char_p

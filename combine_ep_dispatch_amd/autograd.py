@@ -18,6 +18,14 @@ gets a layout of its own, and each forward node keeps the layout it ran
 with, so routing the next batch before this one's backward is safe.  The
 routing is not differentiable; probs is, through the router-probability
 gradient.
+
+The expert layer around the two, on the same layout:
+
+    topk_ids, probs = d.gate(logits, RouteConfig(...))   # differentiable in logits
+    recv = d.dispatch(x, topk_ids)
+    h = d.linear(recv, w1)                   # [R, 2 * inter], differentiable in both
+    act = d.swiglu(h, probs)                 # weights applied to the rows; differentiable in both
+    y = d.combine(d.linear(act, w2), None)
 """
 
 from __future__ import annotations
@@ -26,8 +34,9 @@ from typing import Optional
 
 import torch
 
-from . import (EpConfig, Layout, ep_combine, ep_combine_bwd, ep_combine_bwd_probs, ep_dispatch,
-               ep_dispatch_bwd, ep_dispatch_layout, ep_dispatch_with_layout, ep_query, workspace_for)
+from . import (EpConfig, Layout, RouteConfig, ep_combine, ep_combine_bwd, ep_combine_bwd_probs, ep_dispatch,
+               ep_dispatch_bwd, ep_dispatch_layout, ep_dispatch_with_layout, ep_expert_gemm, ep_expert_gemm_bwd_w,
+               ep_expert_gemm_bwd_x, ep_query, ep_route, ep_route_bwd, ep_swiglu, ep_swiglu_bwd, workspace_for)
 
 __all__ = ["EpDispatcher"]
 
@@ -79,6 +88,74 @@ class _Combine(torch.autograd.Function):
         return g_out, g_probs, None, None
 
 
+class _Gate(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, logits, bias, token_mask, cfg, route):
+        logits = logits.contiguous()
+        ids = torch.empty(cfg.num_tokens, cfg.top_k, dtype=torch.int32, device=logits.device)
+        probs = torch.empty(cfg.num_tokens, cfg.top_k, dtype=torch.float32, device=logits.device)
+        ep_route(cfg, route, logits, ids, probs, bias=bias, token_mask=token_mask)
+        ctx.cfg, ctx.route = cfg, route
+        ctx.save_for_backward(logits, ids)
+        ctx.mark_non_differentiable(ids)
+        return ids, probs
+
+    @staticmethod
+    def backward(ctx, _, grad_probs):
+        logits, ids = ctx.saved_tensors
+        grad = torch.empty_like(logits)
+        ep_route_bwd(ctx.cfg, ctx.route, logits, ids, grad_probs.float().contiguous(), grad)
+        return grad, None, None, None, None
+
+
+class _Linear(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, w, cfg, layout):
+        x, w = x.contiguous(), w.contiguous()
+        y = torch.zeros(cfg.recv_rows, w.shape[1], dtype=torch.bfloat16, device=x.device)
+        ep_expert_gemm(cfg, layout, x, w, y)
+        ctx.cfg, ctx.layout = cfg, layout
+        ctx.save_for_backward(x, w)
+        return y
+
+    @staticmethod
+    def backward(ctx, grad_y):
+        x, w = ctx.saved_tensors
+        gy = grad_y.to(torch.bfloat16).contiguous()
+        gx = gw = None
+        if ctx.needs_input_grad[0]:
+            gx = torch.zeros_like(x)
+            ep_expert_gemm_bwd_x(ctx.cfg, ctx.layout, gy, w, gx)
+        if ctx.needs_input_grad[1]:
+            gw = torch.empty_like(w)
+            ep_expert_gemm_bwd_w(ctx.cfg, ctx.layout, gy, x, gw)
+        return gx, gw, None, None
+
+
+class _Swiglu(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, h, probs, cfg, layout):
+        h = h.contiguous()
+        p = None if probs is None else probs.contiguous().float()
+        act = torch.zeros(h.shape[0], h.shape[1] // 2, dtype=torch.bfloat16, device=h.device)
+        ep_swiglu(cfg, layout, h, p, act)
+        ctx.cfg, ctx.layout = cfg, layout
+        ctx.has_probs = probs is not None
+        ctx.save_for_backward(h, p if p is not None else torch.empty(0, device=h.device))
+        return act
+
+    @staticmethod
+    def backward(ctx, grad_act):
+        h, p = ctx.saved_tensors
+        ga = grad_act.to(torch.bfloat16).contiguous()
+        gh = torch.zeros_like(h)
+        gp = None
+        if ctx.has_probs and ctx.needs_input_grad[1]:
+            gp = torch.empty(ctx.cfg.num_tokens, ctx.cfg.top_k, dtype=torch.float32, device=h.device)
+        ep_swiglu_bwd(ctx.cfg, ctx.layout, h, p if ctx.has_probs else None, ga, gh, gp)
+        return gh, gp, None, None
+
+
 class EpDispatcher:
     """Dispatch / combine with autograd for one configuration on one device."""
 
@@ -114,6 +191,22 @@ class EpDispatcher:
     def combine(self, expert_out: torch.Tensor, probs: Optional[torch.Tensor]) -> torch.Tensor:
         """[R, H] bf16 expert outputs -> [T, H] bf16, weighted by probs [T, K] (or 1)."""
         return _Combine.apply(expert_out, probs, self.cfg, self.layout)
+
+    def gate(self, logits: torch.Tensor, route: RouteConfig, bias: Optional[torch.Tensor] = None,
+             token_mask: Optional[torch.Tensor] = None):
+        """[T, E] logits (float32 or bfloat16) -> topk_ids int32 [T, K] and probs
+        float32 [T, K], differentiable in the logits."""
+        return _Gate.apply(logits, bias, token_mask, self.cfg, route)
+
+    def linear(self, rows: torch.Tensor, w: torch.Tensor) -> torch.Tensor:
+        """[R, in] bf16 receive rows times their experts' weights bf16
+        [E (+1 shared), out, in] -> [R, out]; rows no slot owns are zero."""
+        return _Linear.apply(rows, w, self.cfg, self.layout)
+
+    def swiglu(self, h: torch.Tensor, probs: Optional[torch.Tensor]) -> torch.Tensor:
+        """[R, 2*inter] bf16 (gate, then up) -> [R, inter], each row times its
+        slot's probs [T, K] (or 1); rows no slot owns are zero."""
+        return _Swiglu.apply(h, probs, self.cfg, self.layout)
 
     def tokens_per_expert(self) -> torch.Tensor:
         """Routed rows per group [S, G] (the shared group included)."""

@@ -1,6 +1,7 @@
 // C ABI of epx (declared in include/epx.h): host-side validation, sizing and
 // kernel launches.  No call allocates, frees or synchronizes; every kernel
 // goes onto the caller's stream.
+#include <math.h>
 #include <string.h>
 
 #include <mutex>
@@ -313,6 +314,69 @@ int layout_launch(const Shape& d, const int32_t* topk_ids, void* ws, const ep_la
     }
     if (fused) *fused = a.x != nullptr;
     return status_of(launch_layout(a, static_cast<hipStream_t>(stream)));
+}
+
+// ep_route_t against the configuration.
+int check_route(const Shape& d, const ep_route_t* r) {
+    if (r == nullptr) return EP_EINVAL;
+    if (r->score != EP_SCORE_SOFTMAX && r->score != EP_SCORE_SIGMOID) return EP_EINVAL;
+    if (r->normalize != 0 && r->normalize != 1) return EP_EINVAL;
+    if (r->num_groups < 1 || r->num_groups > EP_MAX_ROUTE_GROUPS || d.E % r->num_groups != 0) return EP_EINVAL;
+    if (r->top_groups < 1 || r->top_groups > r->num_groups) return EP_EINVAL;
+    if (!isfinite(r->scale)) return EP_EINVAL;
+    if (r->logits_type != EP_TYPE_F32 && r->logits_type != EP_TYPE_BF16) return EP_EINVAL;
+    if (r->reserved0 != 0 || r->reserved1 != 0) return EP_EINVAL;
+    if (d.E > EP_MAX_GROUPS) return EP_EINVAL;
+    return EP_OK;
+}
+
+TopkArgs topk_args(const Shape& d, const ep_route_t* r, const void* logits) {
+    TopkArgs a = {};
+    a.logits = logits;
+    a.T = d.T;
+    a.E = d.E;
+    a.K = d.K;
+    a.sigmoid = r->score == EP_SCORE_SIGMOID;
+    a.normalize = r->normalize;
+    a.groups = r->num_groups;
+    a.top_groups = r->top_groups;
+    a.bf16 = r->logits_type == EP_TYPE_BF16;
+    a.scale = r->scale;
+    return a;
+}
+
+// The experts' products: the layout arrays they read, and their dimensions.
+int check_expert(const Shape& d, const ep_layout_t* L, int32_t in_dim, int32_t out_dim, int32_t in_multiple) {
+    int rc;
+    if ((rc = check_rows(d)) != EP_OK) return rc;
+    if (in_dim < in_multiple || in_dim > EP_MAX_EXPERT_DIM || in_dim % in_multiple != 0) return EP_EINVAL;
+    if (out_dim < 8 || out_dim > EP_MAX_EXPERT_DIM || out_dim % 8 != 0) return EP_EINVAL;
+    if (L == nullptr || bad_buffer(L->counts, (int64_t)d.NG * 4, 4) ||
+        bad_buffer(L->row_offsets, (int64_t)d.S * (d.G + 1) * 4, 4) ||
+        bad_buffer(L->seg_base, (int64_t)(d.S + 1) * 4, 4))
+        return EP_EINVAL;
+    return EP_OK;
+}
+
+ExpertArgs expert_args(const Shape& d, const ep_layout_t* L, int32_t in_dim, int32_t out_dim, void* out) {
+    ExpertArgs a = {};
+    a.out = out;
+    a.counts = L->counts;
+    a.seg_base = L->seg_base;
+    a.row_offsets = L->row_offsets;
+    a.in = in_dim;
+    a.on = out_dim;
+    a.E = d.E;
+    a.S = d.S;
+    a.G = d.G;
+    a.NG = d.NG;
+    a.E_loc = d.E_loc;
+    a.C = d.C;
+    a.shared = d.shared;
+    a.src_seg = d.src;
+    a.R = d.R;
+    a.slots = std::min<int64_t>((int64_t)d.T * d.Kp, d.R);
+    return a;
 }
 
 constexpr int64_t kScratchBytes = EP_NOALLOC_SCRATCH_BYTES;
@@ -635,6 +699,150 @@ int ep_multihot_to_indices(const ep_cfg_t* cfg, const uint8_t* routing_map, cons
     a.K = d.K;
     a.E = d.E;
     return status_of(launch_multihot_to_indices(a, static_cast<hipStream_t>(stream)));
+}
+
+int ep_route(const ep_cfg_t* cfg, const ep_route_t* route, const void* logits, const float* bias,
+             const uint8_t* token_mask, int32_t* topk_ids, float* probs, void* stream) {
+    Shape d;
+    int rc = derive(cfg, &d);
+    if (rc != EP_OK) return rc;
+    if ((rc = check_route(d, route)) != EP_OK) return rc;
+    if (grid_too_big(d, 64)) return EP_EINVAL;
+    if (bad_buffer(logits, (int64_t)d.T * d.E * 2, 16) || misaligned(bias, 4) ||
+        bad_buffer(topk_ids, (int64_t)d.T * d.K * 4, 4) || bad_buffer(probs, (int64_t)d.T * d.K * 4, 4))
+        return EP_EINVAL;
+    if ((rc = check_device()) != EP_OK) return rc;
+    TopkArgs a = topk_args(d, route, logits);
+    a.bias = bias;
+    a.mask = token_mask;
+    a.ids = topk_ids;
+    a.probs = probs;
+    return status_of(launch_route(a, static_cast<hipStream_t>(stream)));
+}
+
+int ep_route_bwd(const ep_cfg_t* cfg, const ep_route_t* route, const void* logits, const int32_t* topk_ids,
+                 const float* grad_probs, void* grad_logits, void* stream) {
+    Shape d;
+    int rc = derive(cfg, &d);
+    if (rc != EP_OK) return rc;
+    if ((rc = check_route(d, route)) != EP_OK) return rc;
+    if (grid_too_big(d, 64)) return EP_EINVAL;
+    if (bad_buffer(logits, (int64_t)d.T * d.E * 2, 16) || bad_buffer(grad_logits, (int64_t)d.T * d.E * 2, 16) ||
+        bad_buffer(topk_ids, (int64_t)d.T * d.K * 4, 4) || bad_buffer(grad_probs, (int64_t)d.T * d.K * 4, 4))
+        return EP_EINVAL;
+    if ((rc = check_device()) != EP_OK) return rc;
+    TopkArgs a = topk_args(d, route, logits);
+    a.ids = const_cast<int32_t*>(topk_ids);
+    a.grad_probs = grad_probs;
+    a.grad_logits = grad_logits;
+    return status_of(launch_route_bwd(a, static_cast<hipStream_t>(stream)));
+}
+
+int ep_swiglu(const ep_cfg_t* cfg, const ep_layout_t* layout, int32_t inter, const uint16_t* h, const float* probs,
+              uint16_t* act, void* stream) {
+    Shape d;
+    int rc = derive(cfg, &d);
+    if (rc != EP_OK) return rc;
+    if ((rc = check_rows(d)) != EP_OK) return rc;
+    if (inter < 8 || inter > EP_MAX_EXPERT_DIM || inter % 8 != 0) return EP_EINVAL;
+    if ((rc = check_layout_for_payload(d, layout)) != EP_OK) return rc;
+    if (bad_buffer(h, d.R * inter * 4, 16) || bad_buffer(act, d.R * inter * 2, 16) || misaligned(probs, 4))
+        return EP_EINVAL;
+    if ((rc = check_device()) != EP_OK) return rc;
+    hipStream_t st = static_cast<hipStream_t>(stream);
+    SwigluArgs a = {h, probs, nullptr, act, nullptr, layout->token_row, d.T, d.K, d.Kp, inter, d.R};
+    if ((rc = status_of(launch_swiglu(a, st))) != EP_OK) return rc;
+    return zero_pad(d, layout, act, (int64_t)inter * 2, st);
+}
+
+int ep_swiglu_bwd(const ep_cfg_t* cfg, const ep_layout_t* layout, int32_t inter, const uint16_t* h, const float* probs,
+                  const uint16_t* grad_act, uint16_t* grad_h, float* grad_probs, void* stream) {
+    Shape d;
+    int rc = derive(cfg, &d);
+    if (rc != EP_OK) return rc;
+    if ((rc = check_rows(d)) != EP_OK) return rc;
+    if (inter < 8 || inter > EP_MAX_EXPERT_DIM || inter % 8 != 0) return EP_EINVAL;
+    if ((rc = check_layout_for_payload(d, layout)) != EP_OK) return rc;
+    if (bad_buffer(h, d.R * inter * 4, 16) || bad_buffer(grad_act, d.R * inter * 2, 16) ||
+        bad_buffer(grad_h, d.R * inter * 4, 16) || misaligned(probs, 4) || misaligned(grad_probs, 4))
+        return EP_EINVAL;
+    if ((rc = check_device()) != EP_OK) return rc;
+    hipStream_t st = static_cast<hipStream_t>(stream);
+    SwigluArgs a = {h, probs, grad_act, grad_h, grad_probs, layout->token_row, d.T, d.K, d.Kp, inter, d.R};
+    if ((rc = status_of(launch_swiglu_bwd(a, st))) != EP_OK) return rc;
+    return zero_pad(d, layout, grad_h, (int64_t)inter * 4, st);
+}
+
+int ep_expert_gemm(const ep_cfg_t* cfg, const ep_layout_t* layout, int32_t in_dim, int32_t out_dim, const uint16_t* x,
+                   const uint16_t* w, uint16_t* y, void* stream) {
+    Shape d;
+    int rc = derive(cfg, &d);
+    if (rc != EP_OK) return rc;
+    if ((rc = check_expert(d, layout, in_dim, out_dim, 8)) != EP_OK) return rc;
+    if (bad_buffer(x, d.R * in_dim * 2, 16) || bad_buffer(w, 16, 16) || bad_buffer(y, d.R * out_dim * 2, 16))
+        return EP_EINVAL;
+    if ((rc = check_device()) != EP_OK) return rc;
+    hipStream_t st = static_cast<hipStream_t>(stream);
+    ExpertArgs a = expert_args(d, layout, in_dim, out_dim, y);
+    a.x = x;
+    a.w = w;
+    if ((rc = status_of(launch_expert_gemm(a, st))) != EP_OK) return rc;
+    return zero_pad(d, layout, y, (int64_t)out_dim * 2, st);
+}
+
+int ep_expert_gemm_bwd_x(const ep_cfg_t* cfg, const ep_layout_t* layout, int32_t in_dim, int32_t out_dim,
+                         const uint16_t* grad_y, const uint16_t* w, uint16_t* grad_x, void* stream) {
+    Shape d;
+    int rc = derive(cfg, &d);
+    if (rc != EP_OK) return rc;
+    if ((rc = check_expert(d, layout, in_dim, out_dim, 8)) != EP_OK) return rc;
+    if (bad_buffer(grad_y, d.R * out_dim * 2, 16) || bad_buffer(w, 16, 16) || bad_buffer(grad_x, d.R * in_dim * 2, 16))
+        return EP_EINVAL;
+    if ((rc = check_device()) != EP_OK) return rc;
+    hipStream_t st = static_cast<hipStream_t>(stream);
+    ExpertArgs a = expert_args(d, layout, in_dim, out_dim, grad_x);
+    a.gy = grad_y;
+    a.w = w;
+    if ((rc = status_of(launch_expert_gemm_bwd_x(a, st))) != EP_OK) return rc;
+    return zero_pad(d, layout, grad_x, (int64_t)in_dim * 2, st);
+}
+
+int ep_expert_gemm_bwd_w(const ep_cfg_t* cfg, const ep_layout_t* layout, int32_t in_dim, int32_t out_dim,
+                         const uint16_t* grad_y, const uint16_t* x, void* grad_w, int32_t grad_type, void* stream) {
+    Shape d;
+    int rc = derive(cfg, &d);
+    if (rc != EP_OK) return rc;
+    if ((rc = check_expert(d, layout, in_dim, out_dim, 8)) != EP_OK) return rc;
+    if (grad_type != EP_GRAD_BF16 && grad_type != EP_GRAD_F32 && grad_type != EP_GRAD_F32_ADD) return EP_EINVAL;
+    if (bad_buffer(grad_y, d.R * out_dim * 2, 16) || bad_buffer(x, d.R * in_dim * 2, 16) || bad_buffer(grad_w, 16, 16))
+        return EP_EINVAL;
+    if ((rc = check_device()) != EP_OK) return rc;
+    ExpertArgs a = expert_args(d, layout, in_dim, out_dim, grad_w);
+    a.gy = grad_y;
+    a.x = x;
+    a.grad_type = grad_type;
+    return status_of(launch_expert_gemm_bwd_w(a, static_cast<hipStream_t>(stream)));
+}
+
+int ep_expert_gemm_nvfp4(const ep_cfg_t* cfg, const ep_layout_t* layout, int32_t in_dim, int32_t out_dim,
+                         const uint16_t* x, const uint8_t* codes, const uint8_t* scales, const uint16_t* rowscale,
+                         uint16_t* y, void* stream) {
+    Shape d;
+    int rc = derive(cfg, &d);
+    if (rc != EP_OK) return rc;
+    if ((rc = check_expert(d, layout, in_dim, out_dim, 16)) != EP_OK) return rc;
+    if (bad_buffer(x, d.R * in_dim * 2, 16) || bad_buffer(codes, 16, 16) || bad_buffer(scales, 16, 16) ||
+        bad_buffer(rowscale, 2, 2) || bad_buffer(y, d.R * out_dim * 2, 16))
+        return EP_EINVAL;
+    if ((rc = check_device()) != EP_OK) return rc;
+    hipStream_t st = static_cast<hipStream_t>(stream);
+    ExpertArgs a = expert_args(d, layout, in_dim, out_dim, y);
+    a.x = x;
+    a.codes = codes;
+    a.scales = scales;
+    a.rowscale = rowscale;
+    if ((rc = status_of(launch_expert_gemm_nvfp4(a, st))) != EP_OK) return rc;
+    return zero_pad(d, layout, y, (int64_t)out_dim * 2, st);
 }
 
 }  // extern "C"

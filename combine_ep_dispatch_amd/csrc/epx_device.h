@@ -369,6 +369,56 @@ struct RouteArgs {
 hipError_t launch_indices_to_multihot(const RouteArgs& a, hipStream_t stream);
 hipError_t launch_multihot_to_indices(const RouteArgs& a, hipStream_t stream);
 
+struct TopkArgs {         // ep_route and its backward
+    const void* logits;   // [T, E] fp32 or bf16
+    const float* bias;    // [E] or nullptr
+    const uint8_t* mask;  // [T] or nullptr
+    int32_t* ids;         // [T, K] (read only by the backward pass)
+    float* probs;         // [T, K]
+    const float* grad_probs;
+    void* grad_logits;    // [T, E], type of logits
+    int32_t T, E, K;
+    int32_t sigmoid, normalize, groups, top_groups, bf16;
+    float scale;
+};
+hipError_t launch_route(const TopkArgs& a, hipStream_t stream);
+hipError_t launch_route_bwd(const TopkArgs& a, hipStream_t stream);
+
+struct SwigluArgs {
+    const uint16_t* h;          // [R, 2I]
+    const float* probs;         // [T, K] or nullptr: weight 1
+    const uint16_t* grad_act;   // backward: [R, I]
+    uint16_t* out;              // act [R, I], or grad_h [R, 2I]
+    float* grad_probs;          // [T, K] or nullptr
+    const int32_t* token_row;   // [T, K']
+    int32_t T, K, Kp, I;
+    int64_t R;                  // receive rows; a token_row entry outside [0, R) is skipped
+};
+hipError_t launch_swiglu(const SwigluArgs& a, hipStream_t stream);
+hipError_t launch_swiglu_bwd(const SwigluArgs& a, hipStream_t stream);
+
+struct ExpertArgs {             // the experts' products
+    const uint16_t* x;          // [R, in]  (forward, weights' gradient)
+    const uint16_t* gy;         // [R, out] (both gradients)
+    const uint16_t* w;          // [E + shared, out, in]
+    const uint8_t* codes;       // 4-bit weights: [E + shared, out, in/2]
+    const uint8_t* scales;      // [E + shared, out, in/16]
+    const uint16_t* rowscale;   // [E + shared, out]
+    void* out;                  // y [R, out], grad_x [R, in] or grad_w [E + shared, out, in]
+    const int32_t* counts;      // [S*G]
+    const int32_t* seg_base;    // [S + 1]
+    const int32_t* row_offsets; // [S*(G + 1)]
+    int32_t in, on;             // in_dim, out_dim
+    int32_t E, S, G, NG, E_loc, C, shared, src_seg;
+    int32_t grad_type;          // EP_GRAD_*
+    int64_t R;                  // rows of x, gy, y, grad_x
+    int64_t slots;              // T*K': most rows that all groups hold together
+};
+hipError_t launch_expert_gemm(const ExpertArgs& a, hipStream_t stream);
+hipError_t launch_expert_gemm_bwd_x(const ExpertArgs& a, hipStream_t stream);
+hipError_t launch_expert_gemm_bwd_w(const ExpertArgs& a, hipStream_t stream);
+hipError_t launch_expert_gemm_nvfp4(const ExpertArgs& a, hipStream_t stream);
+
 // Zero the payload bytes of every pad row ([count, align_up(count)) of each
 // group, below capacity).  row_bytes = bytes of one row of `base`.
 hipError_t launch_zero_pad_rows(void* base, int64_t row_bytes, const ep_layout_t& L, int32_t S,

@@ -1,0 +1,92 @@
+// What the experts' product kernels share: which rows belong to which
+// expert, and the tiles of a launch.
+#pragma once
+
+#include "epx_device.h"
+
+namespace epx {
+
+// A group's rows in the receive buffers, whatever the layout holds: [first,
+// first + rows) lies inside [0, R).
+struct GroupRows {
+    int64_t first;
+    int32_t rows;
+};
+
+__device__ __forceinline__ GroupRows group_rows(const ExpertArgs& a, int32_t g) {
+    const int32_t s = g / a.G, gl = g - s * a.G;
+    const int64_t off = a.row_offsets[s * (a.G + 1) + gl];
+    int64_t n = a.counts[g];
+    if (a.C > 0) n = min(n, (int64_t)a.C - off);  // rows past the capacity were dropped
+    const int64_t first = (int64_t)a.seg_base[s] + off;
+    n = first < 0 || first > a.R ? 0 : min(n, a.R - first);
+    return {first, n > 0 ? (int32_t)n : 0};
+}
+
+// The expert whose weights group g uses; the shared expert is the last.
+__device__ __forceinline__ int32_t group_expert(const ExpertArgs& a, int32_t g) {
+    const int32_t s = g / a.G, gl = g - s * a.G;
+    return gl < a.shared ? a.E : s * a.E_loc + gl - a.shared;
+}
+
+// Most row tiles of BM rows that the groups can need: every group with rows
+// has at most one part tile.
+inline int64_t max_row_tiles(const ExpertArgs& a, int bm) {
+    const int64_t groups = a.slots < a.E + a.shared ? a.slots : a.E + a.shared;
+    return a.slots / bm + groups;
+}
+
+struct RowTile {
+    int32_t expert;  // -1: no such tile
+    int32_t rows;    // rows of the tile, 1..BM
+    int64_t first;   // its first receive row
+};
+
+// Number of row tiles of all groups, and the tile-th of them (groups in
+// order).  Every thread of the workgroup (THREADS of them) takes part; lds
+// holds THREADS / 64 + 5 words.  Each thread counts the tiles of a run of
+// groups; an exclusive sum over the threads gives the run that holds the tile.
+// pick(total) maps the number of tiles to the one wanted (>= total: none).
+template <int THREADS, int BM, typename Pick>
+__device__ __forceinline__ RowTile find_row_tile(const ExpertArgs& a, int32_t* lds, Pick pick, int32_t& other) {
+    constexpr int kWaves = THREADS / kWave;
+    const int tid = threadIdx.x, lane = tid & (kWave - 1), w = tid / kWave;
+    const int per = (a.NG + THREADS - 1) / THREADS;
+    const int g0 = tid * per, g1 = min(g0 + per, a.NG);
+    int32_t mine = 0;
+    for (int g = g0; g < g1; ++g) mine += (group_rows(a, g).rows + BM - 1) / BM;
+    const int32_t upto = wave_inclusive_sum(mine);
+    if (lane == kWave - 1) lds[w] = upto;
+    if (tid == 0) lds[kWaves] = -1;
+    __syncthreads();
+    int32_t base = 0, total = 0;
+#pragma unroll
+    for (int i = 0; i < kWaves; ++i) {
+        if (i < w) base += lds[i];
+        total += lds[i];
+    }
+    const int32_t want = pick(total, other);
+    int32_t before = base + upto - mine;
+    if (want >= before && want < before + mine) {
+        for (int g = g0; g < g1; ++g) {
+            const GroupRows r = group_rows(a, g);
+            const int32_t n = (r.rows + BM - 1) / BM;
+            if (want < before + n) {
+                const int32_t skip = (want - before) * BM;
+                lds[kWaves] = group_expert(a, g);
+                lds[kWaves + 1] = min(BM, r.rows - skip);
+                lds[kWaves + 2] = (int32_t)(r.first + skip);
+                break;
+            }
+            before += n;
+        }
+    }
+    __syncthreads();
+    RowTile t;
+    t.expert = uniform(lds[kWaves]);
+    t.rows = uniform(lds[kWaves + 1]);
+    t.first = uniform(lds[kWaves + 2]);
+    return t;
+}
+
+}  // namespace epx

@@ -412,6 +412,167 @@ int ep_multihot_to_indices(const ep_cfg_t* cfg, const uint8_t* routing_map, cons
 int ep_dispatch_layout_noalloc(const ep_cfg_t* cfg, const int32_t* topk_ids, const ep_layout_t* layout,
                                void* stream);
 
+/* ------------------------------------------------------------------------
+ * The expert layer: what runs between the router's logits and ep_combine.
+ *   logits --ep_route--> topk_ids, probs --ep_dispatch_layout / ep_dispatch-->
+ *   recv --ep_expert_gemm--> h --ep_swiglu (weights applied)--> act
+ *   --ep_expert_gemm--> out --ep_combine (probs NULL)--> y
+ * (or ep_swiglu with probs NULL and ep_combine with probs).  Rows that no
+ * kept slot owns (pad rows, rows past a segment's used rows, rows of dropped
+ * slots) are never read and, unless EP_ZERO_PAD_ROWS is set, never written.
+ * ------------------------------------------------------------------------ */
+
+/* ep_route_t.score */
+#define EP_SCORE_SOFTMAX 0  /* s = softmax of the token's logits over all experts */
+#define EP_SCORE_SIGMOID 1  /* s = 1 / (1 + exp(-logit)), each expert by itself   */
+/* ep_route_t.logits_type */
+#define EP_TYPE_F32 0
+#define EP_TYPE_BF16 1
+/* Largest num_groups of ep_route_t. */
+#define EP_MAX_ROUTE_GROUPS 64
+
+/* How ep_route chooses and weights a token's experts. */
+typedef struct ep_route_t {
+    int32_t score;        /* EP_SCORE_*                                             */
+    int32_t normalize;    /* 1: the chosen scores are divided by their sum + 1e-20  */
+    int32_t num_groups;   /* >= 1, divides num_experts: experts [g*E/num_groups,
+                             (g+1)*E/num_groups) form group g; <= EP_MAX_ROUTE_GROUPS */
+    int32_t top_groups;   /* 1 <= top_groups <= num_groups: experts are chosen from
+                             this many groups                                       */
+    float scale;          /* finite; multiplies every weight                        */
+    int32_t logits_type;  /* EP_TYPE_*: type of logits (and of their gradient)      */
+    int32_t reserved0;    /* must be 0                                              */
+    int32_t reserved1;    /* must be 0                                              */
+} ep_route_t;
+
+/*
+ * Router: the experts and weights of every token ([TD] moe_router_dtype: fp32
+ * routing weights; [FA] topk_idx with -1 for unused slots, topk_weights).
+ *   logits      [T, E] of route->logits_type
+ *   bias        float [E] or NULL: added to the scores for the choice only
+ *   token_mask  uint8 [T] or NULL: tokens with 0 get no experts
+ *   topk_ids    int32 [T, K]   the chosen experts, best first; what
+ *                              ep_dispatch_layout takes
+ *   probs       float [T, K]   their weights; what ep_combine / ep_swiglu take
+ * key = s + bias where there is a bias, the logit itself where there is none
+ * (the scores grow with it).  A group's key is the sum of its two largest
+ * keys with a bias (its only key in a group of one) and its largest key
+ * without; the top_groups groups with the largest keys stay.  The K experts
+ * of the largest keys among them are chosen; ties go to the lower index, of
+ * groups and of experts.  Keys with a bias are ordered as 64-bit floating
+ * point orders them: two experts are told apart where fp32 scores would round
+ * to the same value.
+ *   probs[t,k] = scale * s[id_k] / (sum_j s[id_j] + 1e-20)   normalize = 1
+ *              = scale * s[id_k]                             normalize = 0
+ * in fp32, from the scores without the bias.
+ * An expert with a logit of -infinity or NaN is never chosen; a token with
+ * fewer than K experts to choose from has id -1 and weight 0 in its last
+ * slots.  Softmax sums over every expert of the token (a NaN or +infinity
+ * among its logits makes its weights NaN; the ids stay valid).  bias is finite.
+ * Only T, E, K (and their validity) of cfg are used.
+ */
+int ep_route(const ep_cfg_t* cfg, const ep_route_t* route, const void* logits, const float* bias,
+             const uint8_t* token_mask, int32_t* topk_ids, float* probs, void* stream);
+
+/*
+ * Router backward: the gradient of ep_route's weights with respect to the
+ * logits, the choice held fixed (the bias gets none).
+ *   logits      [T, E] of route->logits_type, as in the forward call
+ *   topk_ids    int32 [T, K]   ep_route's; -1 and ids outside [0, E) count as
+ *                              unused slots (grad_probs is not read into them)
+ *   grad_probs  float [T, K]
+ *   grad_logits [T, E] of route->logits_type, all written; 0 for a token
+ *               without experts
+ * With q_k = s[id_k], Q = sum q + 1e-20 and the weights' gradient g:
+ *   gq_k = scale * (g_k - sum_j g_j q_j / Q) / Q (normalize), scale * g_k (not)
+ *   sigmoid: grad_logits[id_k] = gq_k q_k (1 - q_k), 0 elsewhere
+ *   softmax: grad_logits[e] = s_e (sum_{k: id_k = e} gq_k - sum_j gq_j q_j)
+ * in fp32, rounded once to the logits' type.
+ */
+int ep_route_bwd(const ep_cfg_t* cfg, const ep_route_t* route, const void* logits, const int32_t* topk_ids,
+                 const float* grad_probs, void* grad_logits, void* stream);
+
+/*
+ * Gated activation on the receive rows, with the routing weights applied to
+ * the sorted rows ([FA] HybridEPDispatch.forward hands the experts their rows'
+ * probabilities): for every kept slot, row r = token_row[t,k],
+ *   act[r, i] = bf16_rne( w * (silu(h[r, i]) * h[r, inter + i]) )
+ * silu(a) = a / (1 + exp(-a)), in fp32; w = probs[t,k] for routed slots (1
+ * when probs is NULL) and 1 for the shared slot.
+ *   h    bf16 [R, 2*inter]  (gate, then up; inter >= 8, a multiple of 8)
+ *   probs float [T, K] or NULL;  act  bf16 [R, inter]
+ */
+int ep_swiglu(const ep_cfg_t* cfg, const ep_layout_t* layout, int32_t inter, const uint16_t* h,
+              const float* probs, uint16_t* act, void* stream);
+
+/*
+ * Backward of ep_swiglu: for every kept slot, with a, b the row's two halves,
+ * s = 1 / (1 + exp(-a)) and g the row of grad_act, in fp32,
+ *   grad_h[r, i]         = bf16_rne( w g b s (1 + a (1 - s)) )
+ *   grad_h[r, inter + i] = bf16_rne( w g a s )
+ *   grad_probs[t, k]     = sum_i g a s b      (k < K; 0 for masked, invalid and
+ *                          dropped slots), summed in a fixed order
+ *   grad_probs float [T, K], or NULL to leave it out.
+ * grad_h may not overlap h or grad_act.
+ */
+int ep_swiglu_bwd(const ep_cfg_t* cfg, const ep_layout_t* layout, int32_t inter, const uint16_t* h,
+                  const float* probs, const uint16_t* grad_act, uint16_t* grad_h, float* grad_probs,
+                  void* stream);
+
+/* Largest in_dim and out_dim of the experts' products. */
+#define EP_MAX_EXPERT_DIM (1 << 20)
+
+/*
+ * The experts' product: every kept row times its own expert's weights,
+ *   y[r, n] = bf16_rne( sum_h x[r, h] w[e(r), n, h] )   (fp32 accumulation)
+ *   x  bf16 [R, in_dim];  w  bf16 [E + shared_expert, out_dim, in_dim], the
+ *   shared expert last;  y  bf16 [R, out_dim].
+ * in_dim and out_dim: multiples of 8 in [8, EP_MAX_EXPERT_DIM] (cfg->hidden
+ * takes no part).  Uses layout->counts, row_offsets and seg_base, not the
+ * ids: rows of one group belong to one expert.
+ */
+int ep_expert_gemm(const ep_cfg_t* cfg, const ep_layout_t* layout, int32_t in_dim, int32_t out_dim,
+                   const uint16_t* x, const uint16_t* w, uint16_t* y, void* stream);
+
+/*
+ * The input's gradient of ep_expert_gemm:
+ *   grad_x[r, h] = bf16_rne( sum_n grad_y[r, n] w[e(r), n, h] )
+ */
+int ep_expert_gemm_bwd_x(const ep_cfg_t* cfg, const ep_layout_t* layout, int32_t in_dim, int32_t out_dim,
+                         const uint16_t* grad_y, const uint16_t* w, uint16_t* grad_x, void* stream);
+
+/* How ep_expert_gemm_bwd_w leaves the weights' gradient. */
+#define EP_GRAD_BF16 0     /* grad_w bf16, overwritten                           */
+#define EP_GRAD_F32 1      /* grad_w float, overwritten                          */
+#define EP_GRAD_F32_ADD 2  /* grad_w float, added to (gradients over several batches) */
+
+/*
+ * The weights' gradient of ep_expert_gemm:
+ *   grad_w[e, n, h] = sum_{r of expert e} grad_y[r, n] x[r, h]   (fp32 accumulation)
+ * for all E + shared_expert experts; one without rows gets zeros (EP_GRAD_F32_ADD:
+ * stays as it is).  The order of the sum is fixed: results repeat bit for bit.
+ */
+int ep_expert_gemm_bwd_w(const ep_cfg_t* cfg, const ep_layout_t* layout, int32_t in_dim, int32_t out_dim,
+                         const uint16_t* grad_y, const uint16_t* x, void* grad_w, int32_t grad_type, void* stream);
+
+/*
+ * The experts' product over 4-bit weights, in the dispatch's NVFP4 row format
+ * ([MX]): w[e, n, h] = e2m1(code) * e4m3(scales[e, n, h/16]) * float(rowscale[e, n]),
+ *   y[r, n] = bf16_rne( float(rowscale[e, n]) * sum_h x[r, h] * e2m1 * e4m3 )
+ * (the product of a code and its block scale is exact; fp32 accumulation).
+ *   x        bf16  [R, in_dim]
+ *   codes    uint8 [E + shared, out_dim, in_dim/2]   element 2j in the low nibble
+ *   scales   uint8 [E + shared, out_dim, in_dim/16]  E4M3, sign bit decoded; the NaN
+ *                                                    codes 0x7F / 0xFF are outside the contract
+ *   rowscale bf16  [E + shared, out_dim]
+ *   y        bf16  [R, out_dim]
+ * in_dim: a multiple of 16, out_dim of 8, both at most EP_MAX_EXPERT_DIM; codes
+ * and scales 16-byte aligned.
+ */
+int ep_expert_gemm_nvfp4(const ep_cfg_t* cfg, const ep_layout_t* layout, int32_t in_dim, int32_t out_dim,
+                         const uint16_t* x, const uint8_t* codes, const uint8_t* scales,
+                         const uint16_t* rowscale, uint16_t* y, void* stream);
+
 /* Static description of a status code. */
 const char* ep_strerror(int status);
 
