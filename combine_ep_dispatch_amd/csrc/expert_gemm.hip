@@ -1,164 +1,283 @@
-// The experts' products: every receive row times its expert's weights, and
-// both gradients.
-//   forward      y[r, n]  = sum_h x[r, h] w[e, n, h]
-//   4-bit        the same, w[e, n, h] = e2m1 * e4m3 * rowscale[e, n]
-//   input's      gx[r, h] = sum_n gy[r, n] w[e, n, h]
-//   weights'     gw[e, n, h] = sum_r gy[r, n] x[r, h]
-// Each is a product of an F operand (features: the output's contiguous
-// dimension, the rows of the matrix instruction's result) and an N operand
-// over a summed dimension L.  Tiles of 64 x 64 results are built from 32
-// values of L at a time, staged in LDS with L contiguous.
+// The experts' products with bf16 weights: every receive row times its
+// expert's weights, and both gradients.
+//   forward   y[r, n]     = sum_h x[r, h] w[e, n, h]
+//   input's   gx[r, h]    = sum_n gy[r, n] w[e, n, h]
+//   weights'  gw[e, n, h] = sum_r gy[r, n] x[r, h]
+// Each is a product of a feature operand F (the output's contiguous dimension,
+// and the rows of the matrix instruction's result, so that a lane stores
+// consecutive values) and a row operand N, summed over a dimension L that is
+// contiguous in an operand (rows) or its rows (columns).
+//
+// Tiles of 256 features by 256 or 128 rows, 8 waves of 128 x 64 or 64 x 64
+// results in registers; steps of 64 values of L, double-buffered in LDS and
+// copied there by the loads themselves, one barrier a step.
+#include <type_traits>
+
 #include "expert_device.h"
 
 namespace epx {
 namespace {
 
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef short s16x8 __attribute__((ext_vector_type(8)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
-typedef uint32_t v4u __attribute__((ext_vector_type(4)));
+typedef uint32_t v2u __attribute__((ext_vector_type(2)));
 
-constexpr int kGemmThreads = 256;
-constexpr int kTile = 64;   // results of a tile, each way
-constexpr int kStep = 32;   // values of L a step
-constexpr int kPitch = 40;  // LDS row pitch in bf16
+#define EPX_LDS __attribute__((address_space(3)))
 
-// Operand rows m0.. (of `rows`), L contiguous: element (m, l) at p[m * ld + l].
-__device__ __forceinline__ void stage_rows(uint16_t* lds, const uint16_t* p, int64_t ld, int32_t m0, int32_t rows,
-                                           int32_t l0, int32_t len) {
-    const int m = threadIdx.x / 4, c = threadIdx.x % 4 * 8;
-    v4u v = {0, 0, 0, 0};
-    if (m0 + m < rows && l0 + c < len) v = *reinterpret_cast<const v4u*>(p + (int64_t)(m0 + m) * ld + l0 + c);
-    *reinterpret_cast<v4u*>(lds + m * kPitch + c) = v;
+constexpr int kWideThreads = 512;
+constexpr int kStepL = 64;                 // values of L a step
+constexpr int kFeatures = 256;             // features of a tile
+[[maybe_unused]] constexpr int kBufferWord3 = 0x00020000;   // buffer descriptor word 3: 32-bit data, raw addressing
+constexpr int kOutside = 0x7FFFFFF0;       // an offset past every descriptor's end: loads zeros
+
+// 16 bytes a lane from offset voff + soff of a buffer to LDS: lane l's at
+// lds + 16 l.  (The compiler's host pass has no such builtin: it silently
+// drops the kernels that use it.)
+__device__ __forceinline__ void load_to_lds(const void* base, int32_t records, uint16_t* lds, int32_t voff, int32_t soff) {
+#ifdef __HIP_DEVICE_COMPILE__
+    const __amdgpu_buffer_rsrc_t rs =
+        __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), (short)0, records, kBufferWord3);
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (EPX_LDS void*)lds, 16, voff, soff, 0, 0);
+#endif
 }
 
-// Operand columns m0.. (of `cols`), L the rows: element (m, l) at p[l * ld + m].
-__device__ __forceinline__ void stage_cols(uint16_t* lds, const uint16_t* p, int64_t ld, int32_t m0, int32_t cols,
-                                           int32_t l0, int32_t len) {
-    const int l = threadIdx.x / 8, c = threadIdx.x % 8 * 8;
-    v4u v = {0, 0, 0, 0};
-    if (l0 + l < len && m0 + c < cols) v = *reinterpret_cast<const v4u*>(p + (int64_t)(l0 + l) * ld + m0 + c);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) lds[(c + j) * kPitch + l] = (uint16_t)(v[j / 2] >> (j % 2 * 16));
-}
+// One operand's step of BM x kStepL values, copied to LDS by the loads
+// themselves (16 bytes a lane, 1 KiB a wave and load, to consecutive LDS
+// addresses; the lanes pick their global addresses so that the LDS tile comes
+// out swizzled).  Loads past the operand's end write zeros.
+//
+// Rows: L contiguous.  LDS row m holds its 8 chunks of 16 bytes at c ^ (m & 7).
+template <int BM>
+struct RowsOperand {
+    static constexpr int kLoads = BM / 64;  // of each wave
+    const uint16_t* base;
+    int32_t len, records;
+    int32_t voff[kLoads];
+    int32_t chunk;
 
-// 4-bit rows: half a block (8 codes) a thread, times the block's scale.
-__device__ __forceinline__ void stage_nvfp4(uint16_t* lds, const uint8_t* codes, const uint8_t* scales, int64_t in,
-                                            int32_t m0, int32_t rows, int32_t l0, int32_t len) {
-    const int m = threadIdx.x / 4, c = threadIdx.x % 4 * 8;
-    v4u o = {0, 0, 0, 0};
-    if (m0 + m < rows && l0 + c < len) {
-        const uint32_t q = *reinterpret_cast<const uint32_t*>(codes + (int64_t)(m0 + m) * (in / 2) + (l0 + c) / 2);
-        const float s = e4m3_decode_signed(scales[(int64_t)(m0 + m) * (in / 16) + (l0 + c) / 16]);
+    // rows: valid rows from base on; ld: their pitch; len: values of L
+    __device__ __forceinline__ void init(const uint16_t* p, int32_t rows, int32_t ld, int32_t l) {
+        const int lane = threadIdx.x & (kWave - 1), w = uniform((int32_t)(threadIdx.x / kWave));
+        base = p;
+        len = l;
+        records = rows * ld * 2;
+        chunk = (lane % 8) ^ (lane / 8);
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-            o[j] = pack_bf16x2(e2m1_decode((q >> (8 * j)) & 15) * s, e2m1_decode((q >> (8 * j + 4)) & 15) * s);
+        for (int j = 0; j < kLoads; ++j) voff[j] = ((w * kLoads + j) * 8 + lane / 8) * ld * 2 + chunk * 16;
     }
-    *reinterpret_cast<v4u*>(lds + m * kPitch + c) = o;
-}
+    __device__ __forceinline__ void load(uint16_t* lds, int32_t l0) const {
+        const int w = uniform((int32_t)(threadIdx.x / kWave));
+        const bool in = l0 + chunk * 8 < len;
+#pragma unroll
+        for (int j = 0; j < kLoads; ++j)
+            load_to_lds(base, records, lds + (w * kLoads + j) * 512, in ? voff[j] : kOutside, l0 * 2);
+    }
+    // Fragment of 16 rows from m0 on, values [32 kk, 32 kk + 32) of L.
+    static __device__ __forceinline__ bf16x8 fragment(const uint16_t* lds, int m0, int kk) {
+        const int lane = threadIdx.x & (kWave - 1), i = lane % 16, q = lane / 16;
+        return *reinterpret_cast<const bf16x8*>(lds + (m0 + i) * 64 + ((kk * 4 + q) ^ (i & 7)) * 8);
+    }
+};
 
-enum Product { kForward, kNvfp4, kInputGrad, kWeightGrad };
+// Columns: L strided.  LDS row l holds its BM values in 32-byte pairs of
+// chunks at p ^ swizzle(l), so that the transposing reads of 4 rows by 16
+// lanes, and of two such groups, fall on different banks.
+template <int BM>
+struct ColsOperand {
+    static constexpr int kLoads = BM / 64;
+    static constexpr int kPerRow = BM / 8;          // lanes of one LDS row
+    static constexpr int kRows = kWave / kPerRow;   // LDS rows of one load
+    const uint16_t* base;
+    int32_t ld, len, cut;
+    int32_t voff[kLoads];
 
-template <Product P>
-__global__ __launch_bounds__(kGemmThreads) void k_expert_simple(ExpertArgs a, int32_t ftiles, int32_t ntiles) {
-    __shared__ uint16_t lf[kTile * kPitch], ln[kTile * kPitch];
-    __shared__ int32_t ls[16];
-    const int lane = threadIdx.x & (kWave - 1), w = threadIdx.x / kWave;
-    const int32_t F = P == kForward || P == kNvfp4 ? a.on : a.in;
-    int32_t expert, f0, n0 = 0, nrows, len;
+    // cols: valid columns from p on; ld: row pitch; l: rows
+    __device__ __forceinline__ void init(const uint16_t* p, int32_t cols, int32_t pitch, int32_t l, int32_t m0) {
+        const int lane = threadIdx.x & (kWave - 1), w = uniform((int32_t)(threadIdx.x / kWave));
+        base = p;
+        ld = pitch;
+        len = l;
+        cut = m0 * 2;
+#pragma unroll
+        for (int j = 0; j < kLoads; ++j) {
+            const int r = (w * kLoads + j) * kRows + lane / kPerRow, c = lane % kPerRow;
+            const int col = (((c / 2) ^ swizzle(r)) * 2 + c % 2) * 8;
+            voff[j] = col < cols ? r * ld * 2 + col * 2 : kOutside;
+        }
+    }
+    static __device__ __forceinline__ int swizzle(int l) { return (l & 3) | ((l >> 1) & 4); }
+    __device__ __forceinline__ void load(uint16_t* lds, int32_t l0) const {
+        const int w = uniform((int32_t)(threadIdx.x / kWave));
+        const int32_t records = min(len - l0, kStepL) * ld * 2 - cut;
+#pragma unroll
+        for (int j = 0; j < kLoads; ++j)
+            load_to_lds(base + (int64_t)l0 * ld, records, lds + (w * kLoads + j) * 512, voff[j], 0);
+    }
+    static __device__ __forceinline__ bf16x8 fragment(const uint16_t* lds, int m0, int kk) {
+        const int lane = threadIdx.x & (kWave - 1), i = lane % 16, q = lane / 16;
+        const int l = kk * 32 + q * 8 + i / 4;
+        [[maybe_unused]] const uint16_t* p = lds + l * BM + ((m0 / 16) ^ ((i / 4) | (q & 1) * 4)) * 16 + i % 4 * 4;
+        s16x4 lo = {}, hi = {};
+#ifdef __HIP_DEVICE_COMPILE__
+        lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((EPX_LDS s16x4*)p);
+        hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((EPX_LDS s16x4*)(p + 4 * BM));
+#endif
+        return __builtin_bit_cast(bf16x8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+    }
+};
+
+enum Product { kForward, kInputGrad, kWeightGrad };
+
+template <Product P, int NT>
+__global__ __launch_bounds__(kWideThreads) void k_expert_wide(ExpertArgs a, int32_t ftiles, int32_t ntiles) {
+    using FOp = typename std::conditional<P == kForward, RowsOperand<kFeatures>, ColsOperand<kFeatures>>::type;
+    using NOp = typename std::conditional<P == kWeightGrad, ColsOperand<NT>, RowsOperand<NT>>::type;
+    constexpr int kWavesN = NT / 64, kWavesF = 8 / kWavesN;  // a wave's tile: 64 rows
+    constexpr int kF = kFeatures / kWavesF / 16, kN = 4;     // its fragments
+    constexpr int kBuffer = (kFeatures + NT) * kStepL;
+    __shared__ __align__(1024) uint16_t lds[2 * kBuffer];
+    __shared__ int32_t scan[16];
+    const int lane = threadIdx.x & (kWave - 1), w = uniform((int32_t)(threadIdx.x / kWave));
+    const int wf = w / kWavesN * (kFeatures / kWavesF), wn = w % kWavesN * 64;
+    const int32_t F = P == kForward ? a.on : a.in;
+
+    // Workgroups are handed to the 8 XCDs in turn: XCD x takes the x-th
+    // eighth of the tiles, in blocks of 4 row tiles by all feature tiles, so
+    // that the workgroups that run together on it share operands in its L2.
+    auto pick = [&](int32_t rt, int32_t& f) {
+        const int32_t total = rt * ftiles, per = (total + 7) / 8;
+        const int32_t b = (int32_t)(blockIdx.x / 8), at = (int32_t)(blockIdx.x % 8) * per + b;
+        f = 0;
+        if (b >= per || at >= total) return INT32_MAX;
+        const int32_t block = at / (4 * ftiles), r0 = block * 4, height = min(4, rt - r0);
+        const int32_t in = at - block * 4 * ftiles;
+        f = in / height;
+        return r0 + in % height;
+    };
+    int32_t expert, f0, rows, len;
     int64_t first = 0;
-    if (P == kWeightGrad) {
-        // one tile of one expert's gradient; a group that has no part in it
-        // (a segment's shared group) is left out
-        const int32_t f = blockIdx.x % ftiles, n = blockIdx.x / ftiles % ntiles;
-        expert = blockIdx.x / ftiles / ntiles;
-        f0 = f * kTile;
-        n0 = n * kTile;
+    FOp fo;
+    NOp no;
+    if constexpr (P == kWeightGrad) {
+        int32_t f;
+        const int32_t n = pick((a.E + a.shared) * ntiles, f);
+        if (n == INT32_MAX) return;
+        expert = n / ntiles;
+        const int32_t n0 = (n - expert * ntiles) * NT;
+        f0 = f * kFeatures;
         const int32_t g = expert < a.E ? expert / a.E_loc * a.G + a.shared + expert % a.E_loc : a.src_seg * a.G;
         const GroupRows r = group_rows(a, g);
-        first = r.first;
         len = r.rows;
-        nrows = a.on;
+        rows = min(NT, a.on - n0);
+        first = (int64_t)expert * a.on + n0;
+        fo.init(a.x + r.first * a.in + f0, a.in - f0, a.in, len, f0);
+        no.init(a.gy + r.first * a.on + n0, rows, a.on, len, n0);
     } else {
         int32_t f;
-        const RowTile t = find_row_tile<kGemmThreads, kTile>(
-            a, ls,
-            [&](int32_t, int32_t& ft) {
-                ft = blockIdx.x % ftiles;
-                return (int32_t)(blockIdx.x / ftiles);
-            },
-            f);
+        const RowTile t = find_row_tile<kWideThreads, NT>(a, scan, pick, f);
         if (t.expert < 0) return;
         expert = t.expert;
+        rows = t.rows;
         first = t.first;
-        nrows = t.rows;
-        f0 = f * kTile;
-        len = P == kInputGrad ? a.on : a.in;
-    }
-    f32x4 acc[4] = {};
-    for (int32_t l0 = 0; l0 < len; l0 += kStep) {
-        __syncthreads();
-        if (P == kForward) stage_rows(lf, a.w + (int64_t)expert * a.on * a.in, a.in, f0, a.on, l0, len);
-        if (P == kNvfp4)
-            stage_nvfp4(lf, a.codes + (int64_t)expert * a.on * (a.in / 2), a.scales + (int64_t)expert * a.on * (a.in / 16),
-                        a.in, f0, a.on, l0, len);
-        if (P == kInputGrad) stage_cols(lf, a.w + (int64_t)expert * a.on * a.in, a.in, f0, a.in, l0, len);
-        if (P == kWeightGrad) stage_cols(lf, a.x + first * a.in, a.in, f0, a.in, l0, len);
-        if (P == kForward || P == kNvfp4) stage_rows(ln, a.x + first * a.in, a.in, 0, nrows, l0, len);
-        if (P == kInputGrad) stage_rows(ln, a.gy + first * a.on, a.on, 0, nrows, l0, len);
-        if (P == kWeightGrad) stage_cols(ln, a.gy + first * a.on, a.on, n0, a.on, l0, len);
-        __syncthreads();
-        const bf16x8 fa = *reinterpret_cast<const bf16x8*>(lf + (w * 16 + lane % 16) * kPitch + lane / 16 * 8);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const bf16x8 fb = *reinterpret_cast<const bf16x8*>(ln + (i * 16 + lane % 16) * kPitch + lane / 16 * 8);
-            acc[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fa, fb, acc[i], 0, 0, 0);
+        f0 = f * kFeatures;
+        const uint16_t* we = a.w + (int64_t)expert * a.on * a.in;
+        if constexpr (P == kForward) {
+            len = a.in;
+            fo.init(we + (int64_t)f0 * a.in, min(kFeatures, a.on - f0), a.in, len);
+            no.init(a.x + first * a.in, rows, a.in, len);
+        } else {
+            len = a.on;
+            fo.init(we + f0, a.in - f0, a.in, len, f0);
+            no.init(a.gy + first * a.on, rows, a.on, len);
         }
     }
-    // acc[i][j]: feature f0 + 16 w + 4 (lane / 16) + j, row 16 i + lane % 16
-    const int32_t f = f0 + w * 16 + lane / 16 * 4;
-    if (f >= F) return;
-    float rs[4] = {1.0f, 1.0f, 1.0f, 1.0f};
-    if (P == kNvfp4)
+
+    f32x4 acc[kF][kN] = {};
+    auto step = [&](const uint16_t* lf, const uint16_t* ln) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) rs[j] = bf16_lo(a.rowscale[(int64_t)expert * a.on + f + j]);
+        for (int kk = 0; kk < 2; ++kk) {
+            bf16x8 fb[kN], fa[kF];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int32_t n = n0 + i * 16 + lane % 16;
-        if (n >= nrows) continue;
-        const int64_t at = (P == kWeightGrad ? (int64_t)expert * a.on + n : first + n) * F + f;
-        float v[4];
+            for (int n = 0; n < kN; ++n) fb[n] = NOp::fragment(ln, wn + n * 16, kk);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) v[j] = P == kNvfp4 ? acc[i][j] * rs[j] : acc[i][j];
-        if (P == kWeightGrad && a.grad_type != EP_GRAD_BF16) {
-            f32x4* o = reinterpret_cast<f32x4*>(static_cast<float*>(a.out) + at);
-            f32x4 s = {v[0], v[1], v[2], v[3]};
-            if (a.grad_type == EP_GRAD_F32_ADD) s += *o;
-            *o = s;
-        } else {
-            uint32_t* o = reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(a.out) + at);
-            o[0] = pack_bf16x2(v[0], v[1]);
-            o[1] = pack_bf16x2(v[2], v[3]);
+            for (int f = 0; f < kF; ++f) fa[f] = FOp::fragment(lf, wf + f * 16, kk);
+#pragma unroll
+            for (int f = 0; f < kF; ++f)
+#pragma unroll
+                for (int n = 0; n < kN; ++n)
+                    acc[f][n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fa[f], fb[n], acc[f][n], 0, 0, 0);
+        }
+    };
+    uint16_t* cur = lds;
+    uint16_t* next = lds + kBuffer;
+    if (len > 0) {
+        fo.load(cur, 0);
+        no.load(cur + kFeatures * kStepL, 0);
+    }
+    for (int32_t l0 = 0; l0 < len; l0 += kStepL) {
+        // This step's loads have landed (LDS loads count as vector memory
+        // operations), and every wave is done with the other buffer.
+        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+        __syncthreads();
+        if (l0 + kStepL < len) {
+            fo.load(next, l0 + kStepL);
+            no.load(next + kFeatures * kStepL, l0 + kStepL);
+        }
+        step(cur, cur + kFeatures * kStepL);
+        uint16_t* t = cur;
+        cur = next;
+        next = t;
+    }
+
+    // acc[f][n][j]: feature f0 + wf + 16 f + 4 (lane / 16) + j, row wn + 16 n + lane % 16
+#pragma unroll
+    for (int n = 0; n < kN; ++n) {
+        const int32_t row = wn + n * 16 + lane % 16;
+        if (row >= rows) continue;
+#pragma unroll
+        for (int f = 0; f < kF; ++f) {
+            const int32_t fe = f0 + wf + f * 16 + lane / 16 * 4;
+            if (fe >= F) continue;
+            const int64_t at = (first + row) * F + fe;
+            const f32x4 v = acc[f][n];
+            if (P == kWeightGrad && a.grad_type != EP_GRAD_BF16) {
+                f32x4* o = reinterpret_cast<f32x4*>(static_cast<float*>(a.out) + at);
+                *o = a.grad_type == EP_GRAD_F32_ADD ? *o + v : v;
+            } else {
+                const v2u o = {pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
+                *reinterpret_cast<v2u*>(static_cast<uint16_t*>(a.out) + at) = o;
+            }
         }
     }
 }
 
-template <Product P>
-hipError_t product(const ExpertArgs& a, hipStream_t stream) {
-    const int32_t F = P == kForward || P == kNvfp4 ? a.on : a.in;
-    const int32_t ftiles = (F + kTile - 1) / kTile, ntiles = (a.on + kTile - 1) / kTile;
-    const int64_t blocks =
-        P == kWeightGrad ? (int64_t)ftiles * ntiles * (a.E + a.shared) : max_row_tiles(a, kTile) * ftiles;
-    if (blocks == 0) return hipSuccess;
-    if (blocks * kGemmThreads > 0xFFFFFFFFll) return hipErrorInvalidValue;
-    hipLaunchKernelGGL(k_expert_simple<P>, dim3((unsigned)blocks), dim3(kGemmThreads), 0, stream, a, ftiles, ntiles);
+template <Product P, int NT>
+hipError_t wide(const ExpertArgs& a, hipStream_t stream) {
+    const int32_t F = P == kForward ? a.on : a.in;
+    const int32_t ftiles = (F + kFeatures - 1) / kFeatures, ntiles = (a.on + NT - 1) / NT;
+    const int64_t tiles = (P == kWeightGrad ? (int64_t)ntiles * (a.E + a.shared) : max_row_tiles(a, NT)) * ftiles;
+    if (tiles == 0) return hipSuccess;
+    const int64_t blocks = (tiles + 7) / 8 * 8;
+    if (blocks * kWideThreads > 0xFFFFFFFFll) return hipErrorInvalidValue;
+    hipLaunchKernelGGL((k_expert_wide<P, NT>), dim3((unsigned)blocks), dim3(kWideThreads), 0, stream, a, ftiles, ntiles);
     return hipGetLastError();
+}
+
+// Row tiles of 256 where the groups hold that many rows on average.
+template <Product P>
+hipError_t by_rows(const ExpertArgs& a, hipStream_t stream) {
+    const int64_t groups = a.slots < a.E + a.shared ? a.slots : a.E + a.shared;
+    return a.slots >= 256 * groups ? wide<P, 256>(a, stream) : wide<P, 128>(a, stream);
 }
 
 }  // namespace
 
-hipError_t launch_expert_gemm(const ExpertArgs& a, hipStream_t stream) { return product<kForward>(a, stream); }
-hipError_t launch_expert_gemm_nvfp4(const ExpertArgs& a, hipStream_t stream) { return product<kNvfp4>(a, stream); }
-hipError_t launch_expert_gemm_bwd_x(const ExpertArgs& a, hipStream_t stream) { return product<kInputGrad>(a, stream); }
-hipError_t launch_expert_gemm_bwd_w(const ExpertArgs& a, hipStream_t stream) { return product<kWeightGrad>(a, stream); }
+hipError_t launch_expert_gemm(const ExpertArgs& a, hipStream_t stream) { return by_rows<kForward>(a, stream); }
+hipError_t launch_expert_gemm_bwd_x(const ExpertArgs& a, hipStream_t stream) { return by_rows<kInputGrad>(a, stream); }
+hipError_t launch_expert_gemm_bwd_w(const ExpertArgs& a, hipStream_t stream) {
+    return wide<kWeightGrad, 256>(a, stream);
+}
 
 }  // namespace epx
