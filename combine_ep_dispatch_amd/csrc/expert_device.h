@@ -6,6 +6,27 @@
 
 namespace epx {
 
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t v2u __attribute__((ext_vector_type(2)));
+typedef uint32_t v4u __attribute__((ext_vector_type(4)));
+
+#define EPX_LDS __attribute__((address_space(3)))
+
+[[maybe_unused]] constexpr int kBufferWord3 = 0x00020000;  // buffer descriptor word 3: 32-bit data, raw addressing
+constexpr int kOutside = 0x7FFFFFF0;                       // an offset past every descriptor's end: loads zeros
+
+// 16 bytes a lane from offset voff + soff of a buffer to LDS: lane l's at
+// lds + 16 l.  (The compiler's host pass has no such builtin: it silently
+// drops the kernels that use it.)
+__device__ __forceinline__ void load_to_lds(const void* base, int32_t records, uint16_t* lds, int32_t voff, int32_t soff) {
+#ifdef __HIP_DEVICE_COMPILE__
+    const __amdgpu_buffer_rsrc_t rs =
+        __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), (short)0, records, kBufferWord3);
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (EPX_LDS void*)lds, 16, voff, soff, 0, 0);
+#endif
+}
+
 // A group's rows in the receive buffers, whatever the layout holds: [first,
 // first + rows) lies inside [0, R).
 struct GroupRows {
@@ -42,11 +63,10 @@ struct RowTile {
     int64_t first;   // its first receive row
 };
 
-// Number of row tiles of all groups, and the tile-th of them (groups in
-// order).  Every thread of the workgroup (THREADS of them) takes part; lds
-// holds THREADS / 64 + 5 words.  Each thread counts the tiles of a run of
+// The row tile that pick(number of row tiles, other) asks for, groups in
+// order.  Every thread of the workgroup (THREADS of them) takes part; lds
+// holds THREADS / 64 + 3 words.  Each thread counts the tiles of a run of
 // groups; an exclusive sum over the threads gives the run that holds the tile.
-// pick(total) maps the number of tiles to the one wanted (>= total: none).
 template <int THREADS, int BM, typename Pick>
 __device__ __forceinline__ RowTile find_row_tile(const ExpertArgs& a, int32_t* lds, Pick pick, int32_t& other) {
     constexpr int kWaves = THREADS / kWave;
@@ -65,7 +85,7 @@ __device__ __forceinline__ RowTile find_row_tile(const ExpertArgs& a, int32_t* l
         if (i < w) base += lds[i];
         total += lds[i];
     }
-    const int32_t want = pick(total, other);
+    const int32_t want = pick(uniform(total), other);
     int32_t before = base + upto - mine;
     if (want >= before && want < before + mine) {
         for (int g = g0; g < g1; ++g) {
@@ -87,6 +107,24 @@ __device__ __forceinline__ RowTile find_row_tile(const ExpertArgs& a, int32_t* l
     t.rows = uniform(lds[kWaves + 1]);
     t.first = uniform(lds[kWaves + 2]);
     return t;
+}
+
+constexpr int32_t kNoTile = INT32_MAX;
+
+// The tile of this workgroup among row_tiles x ftiles: its row tile (kNoTile:
+// none) and, in f, its feature tile.  Workgroups are handed to the 8 XCDs in
+// turn: XCD x takes the x-th eighth of the tiles, in blocks of 4 row tiles by
+// all feature tiles, so that the workgroups that run together on it share
+// operands in its L2.
+__device__ __forceinline__ int32_t xcd_tile(int32_t row_tiles, int32_t ftiles, int32_t& f) {
+    const int32_t total = row_tiles * ftiles, per = (total + 7) / 8;
+    const int32_t b = (int32_t)(blockIdx.x / 8), at = (int32_t)(blockIdx.x % 8) * per + b;
+    f = 0;
+    if (b >= per || at >= total) return kNoTile;
+    const int32_t block = at / (4 * ftiles), r0 = block * 4, height = min(4, row_tiles - r0);
+    const int32_t in = at - block * 4 * ftiles;
+    f = uniform(in / height);
+    return uniform(r0 + in % height);
 }
 
 }  // namespace epx

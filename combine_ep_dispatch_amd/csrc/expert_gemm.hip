@@ -18,30 +18,13 @@
 namespace epx {
 namespace {
 
-typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef short s16x8 __attribute__((ext_vector_type(8)));
-typedef float f32x4 __attribute__((ext_vector_type(4)));
-typedef uint32_t v2u __attribute__((ext_vector_type(2)));
 
-#define EPX_LDS __attribute__((address_space(3)))
 
 constexpr int kWideThreads = 512;
 constexpr int kStepL = 64;                 // values of L a step
 constexpr int kFeatures = 256;             // features of a tile
-[[maybe_unused]] constexpr int kBufferWord3 = 0x00020000;   // buffer descriptor word 3: 32-bit data, raw addressing
-constexpr int kOutside = 0x7FFFFFF0;       // an offset past every descriptor's end: loads zeros
-
-// 16 bytes a lane from offset voff + soff of a buffer to LDS: lane l's at
-// lds + 16 l.  (The compiler's host pass has no such builtin: it silently
-// drops the kernels that use it.)
-__device__ __forceinline__ void load_to_lds(const void* base, int32_t records, uint16_t* lds, int32_t voff, int32_t soff) {
-#ifdef __HIP_DEVICE_COMPILE__
-    const __amdgpu_buffer_rsrc_t rs =
-        __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), (short)0, records, kBufferWord3);
-    __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (EPX_LDS void*)lds, 16, voff, soff, 0, 0);
-#endif
-}
 
 // One operand's step of BM x kStepL values, copied to LDS by the loads
 // themselves (16 bytes a lane, 1 KiB a wave and load, to consecutive LDS
@@ -143,19 +126,7 @@ __global__ __launch_bounds__(kWideThreads) void k_expert_wide(ExpertArgs a, int3
     const int wf = w / kWavesN * (kFeatures / kWavesF), wn = w % kWavesN * 64;
     const int32_t F = P == kForward ? a.on : a.in;
 
-    // Workgroups are handed to the 8 XCDs in turn: XCD x takes the x-th
-    // eighth of the tiles, in blocks of 4 row tiles by all feature tiles, so
-    // that the workgroups that run together on it share operands in its L2.
-    auto pick = [&](int32_t rt, int32_t& f) {
-        const int32_t total = rt * ftiles, per = (total + 7) / 8;
-        const int32_t b = (int32_t)(blockIdx.x / 8), at = (int32_t)(blockIdx.x % 8) * per + b;
-        f = 0;
-        if (b >= per || at >= total) return INT32_MAX;
-        const int32_t block = at / (4 * ftiles), r0 = block * 4, height = min(4, rt - r0);
-        const int32_t in = at - block * 4 * ftiles;
-        f = in / height;
-        return r0 + in % height;
-    };
+    auto pick = [&](int32_t rt, int32_t& f) { return xcd_tile(rt, ftiles, f); };
     int32_t expert, f0, rows, len;
     int64_t first = 0;
     FOp fo;
@@ -163,7 +134,7 @@ __global__ __launch_bounds__(kWideThreads) void k_expert_wide(ExpertArgs a, int3
     if constexpr (P == kWeightGrad) {
         int32_t f;
         const int32_t n = pick((a.E + a.shared) * ntiles, f);
-        if (n == INT32_MAX) return;
+        if (n == kNoTile) return;
         expert = n / ntiles;
         const int32_t n0 = (n - expert * ntiles) * NT;
         f0 = f * kFeatures;
