@@ -9,7 +9,7 @@
 // contiguous in an operand (rows) or its rows (columns).
 //
 // Tiles of 256 features by 256 or 128 rows, 8 waves of 128 x 64 or 64 x 64
-// results in registers; steps of 64 values of L, double-buffered in LDS and
+// results in registers; steps of 64 values of L, two or three of them in LDS,
 // copied there by the loads themselves, one barrier a step.
 #include <type_traits>
 
@@ -23,7 +23,7 @@ typedef short s16x8 __attribute__((ext_vector_type(8)));
 
 
 constexpr int kWideThreads = 512;
-constexpr int kStepL = 64;                 // values of L a step
+constexpr int kStepL = 64;                 // values of L a step: whole 128-byte lines of rows
 constexpr int kFeatures = 256;             // features of a tile
 
 // One operand's step of BM x kStepL values, copied to LDS by the loads
@@ -31,36 +31,37 @@ constexpr int kFeatures = 256;             // features of a tile
 // addresses; the lanes pick their global addresses so that the LDS tile comes
 // out swizzled).  Loads past the operand's end write zeros.
 //
-// Rows: L contiguous.  LDS row m holds its 8 chunks of 16 bytes at c ^ (m & 7).
+// Rows: L contiguous.  LDS row m (128 bytes) holds its 8 chunks of 16 bytes at
+// c ^ (m / 2 % 8): the 16 rows of a fragment's quarter fall on all banks.
 template <int BM>
 struct RowsOperand {
-    static constexpr int kLoads = BM / 64;  // of each wave
+    static constexpr int kLoads = BM / 64;  // of each wave and step
     const uint16_t* base;
-    int32_t len, records;
-    int32_t voff[kLoads];
-    int32_t chunk;
+    int32_t ld, len, records;
+    int32_t voff[kLoads], chunk[2];
 
-    // rows: valid rows from base on; ld: their pitch; len: values of L
-    __device__ __forceinline__ void init(const uint16_t* p, int32_t rows, int32_t ld, int32_t l) {
+    // rows: valid rows from base on; pitch: theirs; l: values of L
+    __device__ __forceinline__ void init(const uint16_t* p, int32_t rows, int32_t pitch, int32_t l) {
         const int lane = threadIdx.x & (kWave - 1), w = uniform((int32_t)(threadIdx.x / kWave));
         base = p;
+        ld = pitch;
         len = l;
-        records = rows * ld * 2;
-        chunk = (lane % 8) ^ (lane / 8);
-#pragma unroll
-        for (int j = 0; j < kLoads; ++j) voff[j] = ((w * kLoads + j) * 8 + lane / 8) * ld * 2 + chunk * 16;
-    }
-    __device__ __forceinline__ void load(uint16_t* lds, int32_t l0) const {
-        const int w = uniform((int32_t)(threadIdx.x / kWave));
-        const bool in = l0 + chunk * 8 < len;
+        records = uniform(rows * ld * 2);
+        chunk[0] = (lane % 8) ^ (lane / 16);
+        chunk[1] = chunk[0] ^ 4;
 #pragma unroll
         for (int j = 0; j < kLoads; ++j)
-            load_to_lds(base, records, lds + (w * kLoads + j) * 512, in ? voff[j] : kOutside, l0 * 2);
+            voff[j] = ((w * kLoads + j) * 8 + lane / 8) * ld * 2 + chunk[(w * kLoads + j) % 2] * 16;
     }
-    // Fragment of 16 rows from m0 on, values [32 kk, 32 kk + 32) of L.
+    __device__ __forceinline__ void load(uint16_t* lds, int32_t l0, int j) const {
+        const int w = uniform((int32_t)(threadIdx.x / kWave));
+        load_to_lds(base, records, lds + (w * kLoads + j) * 512,
+                    l0 + chunk[(w * kLoads + j) % 2] * 8 < len ? voff[j] + l0 * 2 : kOutside);
+    }
+    // Fragment of 16 rows from m0 on, values [32 kk, 32 kk + 32) of the step.
     static __device__ __forceinline__ bf16x8 fragment(const uint16_t* lds, int m0, int kk) {
         const int lane = threadIdx.x & (kWave - 1), i = lane % 16, q = lane / 16;
-        return *reinterpret_cast<const bf16x8*>(lds + (m0 + i) * 64 + ((kk * 4 + q) ^ (i & 7)) * 8);
+        return *reinterpret_cast<const bf16x8*>(lds + (m0 + i) * kStepL + ((kk * 4 + q) ^ (i / 2)) * 8);
     }
 };
 
@@ -70,13 +71,13 @@ struct RowsOperand {
 template <int BM>
 struct ColsOperand {
     static constexpr int kLoads = BM / 64;
-    static constexpr int kPerRow = BM / 8;          // lanes of one LDS row
-    static constexpr int kRows = kWave / kPerRow;   // LDS rows of one load
+    static constexpr int kPerRow = BM / 8;         // lanes of one LDS row
+    static constexpr int kRows = kWave / kPerRow;  // LDS rows of one load
     const uint16_t* base;
     int32_t ld, len, cut;
     int32_t voff[kLoads];
 
-    // cols: valid columns from p on; ld: row pitch; l: rows
+    // p: column m0 of the operand; cols: valid columns from p on; pitch: of rows; l: rows
     __device__ __forceinline__ void init(const uint16_t* p, int32_t cols, int32_t pitch, int32_t l, int32_t m0) {
         const int lane = threadIdx.x & (kWave - 1), w = uniform((int32_t)(threadIdx.x / kWave));
         base = p;
@@ -91,12 +92,14 @@ struct ColsOperand {
         }
     }
     static __device__ __forceinline__ int swizzle(int l) { return (l & 3) | ((l >> 1) & 4); }
-    __device__ __forceinline__ void load(uint16_t* lds, int32_t l0) const {
+    // Bytes of the rows of a step, from base's column on.
+    __device__ __forceinline__ int32_t records(int32_t l0) const {
+        const int32_t rows = min(len - l0, kStepL);
+        return uniform(rows > 0 ? rows * ld * 2 - cut : 0);
+    }
+    __device__ __forceinline__ void load(uint16_t* lds, int32_t l0, int j) const {
         const int w = uniform((int32_t)(threadIdx.x / kWave));
-        const int32_t records = min(len - l0, kStepL) * ld * 2 - cut;
-#pragma unroll
-        for (int j = 0; j < kLoads; ++j)
-            load_to_lds(base + (int64_t)l0 * ld, records, lds + (w * kLoads + j) * 512, voff[j], 0);
+        load_to_lds(base + (int64_t)l0 * ld, records(l0), lds + (w * kLoads + j) * 512, voff[j]);
     }
     static __device__ __forceinline__ bf16x8 fragment(const uint16_t* lds, int m0, int kk) {
         const int lane = threadIdx.x & (kWave - 1), i = lane % 16, q = lane / 16;
@@ -119,8 +122,9 @@ __global__ __launch_bounds__(kWideThreads) void k_expert_wide(ExpertArgs a, int3
     using NOp = typename std::conditional<P == kWeightGrad, ColsOperand<NT>, RowsOperand<NT>>::type;
     constexpr int kWavesN = NT / 64, kWavesF = 8 / kWavesN;  // a wave's tile: 64 rows
     constexpr int kF = kFeatures / kWavesF / 16, kN = 4;     // its fragments
+    constexpr int kBuffers = NT == 256 ? 2 : 3;  // what 160 KiB hold
     constexpr int kBuffer = (kFeatures + NT) * kStepL;
-    __shared__ __align__(1024) uint16_t lds[2 * kBuffer];
+    __shared__ __align__(1024) uint16_t lds[kBuffers * kBuffer];
     __shared__ int32_t scan[16];
     const int lane = threadIdx.x & (kWave - 1), w = uniform((int32_t)(threadIdx.x / kWave));
     const int wf = w / kWavesN * (kFeatures / kWavesF), wn = w % kWavesN * 64;
@@ -166,7 +170,28 @@ __global__ __launch_bounds__(kWideThreads) void k_expert_wide(ExpertArgs a, int3
     }
 
     f32x4 acc[kF][kN] = {};
-    auto step = [&](const uint16_t* lf, const uint16_t* ln) {
+    constexpr int kLoads = FOp::kLoads + NOp::kLoads;
+    auto load = [&](int32_t s) {
+        uint16_t* to = lds + s % kBuffers * kBuffer;
+#pragma unroll
+        for (int j = 0; j < FOp::kLoads; ++j) fo.load(to, s * kStepL, j);
+#pragma unroll
+        for (int j = 0; j < NOp::kLoads; ++j) no.load(to + kFeatures * kStepL, s * kStepL, j);
+    };
+    const int32_t steps = (len + kStepL - 1) / kStepL;
+    const bool busy = wn < rows;  // a wave past the tile's last row only loads
+    for (int s = 0; s < kBuffers - 1; ++s) load(s);
+    for (int32_t s = 0; s < steps; ++s) {
+        // This step's loads have landed when only the later steps' are
+        // outstanding: loads return in order, and past the end they still
+        // count, and write zeros.  Behind the barrier every wave's have, and
+        // every wave is done with the last step's buffer, which is filled next.
+        asm volatile("s_waitcnt vmcnt(%0)" ::"n"((kBuffers - 2) * kLoads) : "memory");
+        lds_barrier();
+        load(s + kBuffers - 1);
+        if (!busy) continue;
+        const uint16_t* lf = lds + s % kBuffers * kBuffer;
+        const uint16_t* ln = lf + kFeatures * kStepL;
 #pragma unroll
         for (int kk = 0; kk < 2; ++kk) {
             bf16x8 fb[kN], fa[kF];
@@ -180,27 +205,9 @@ __global__ __launch_bounds__(kWideThreads) void k_expert_wide(ExpertArgs a, int3
                 for (int n = 0; n < kN; ++n)
                     acc[f][n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fa[f], fb[n], acc[f][n], 0, 0, 0);
         }
-    };
-    uint16_t* cur = lds;
-    uint16_t* next = lds + kBuffer;
-    if (len > 0) {
-        fo.load(cur, 0);
-        no.load(cur + kFeatures * kStepL, 0);
     }
-    for (int32_t l0 = 0; l0 < len; l0 += kStepL) {
-        // This step's loads have landed (LDS loads count as vector memory
-        // operations), and every wave is done with the other buffer.
-        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-        __syncthreads();
-        if (l0 + kStepL < len) {
-            fo.load(next, l0 + kStepL);
-            no.load(next + kFeatures * kStepL, l0 + kStepL);
-        }
-        step(cur, cur + kFeatures * kStepL);
-        uint16_t* t = cur;
-        cur = next;
-        next = t;
-    }
+    // No load may land in LDS that belongs to another workgroup by then.
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
 
     // acc[f][n][j]: feature f0 + wf + 16 f + 4 (lane / 16) + j, row wn + 16 n + lane % 16
 #pragma unroll

@@ -104,7 +104,7 @@ __global__ __launch_bounds__(kFewThreads) void k_nvfp4_few(ExpertArgs a, int32_t
         const int32_t voff = l + lane * 8 < in ? (l + lane * 8) * 2 : kOutside;
         for (int r = wn; r < t.rows; r += kWN)
             if (KC == 512 || lane < 32)
-                load_to_lds(a.x + (t.first + r) * in, in * 2, reinterpret_cast<uint16_t*>(to + r * kPitch), voff, 0);
+                load_to_lds(a.x + (t.first + r) * in, in * 2, reinterpret_cast<uint16_t*>(to + r * kPitch), voff);
     };
     f32x4 acc[NR / 16] = {};
     auto compute = [&](const Chunk& ch, int32_t c) {
