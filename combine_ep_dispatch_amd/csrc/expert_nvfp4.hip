@@ -1,11 +1,18 @@
 // The experts' product over 4-bit weights: y[r, n] = rowscale[e, n] *
 // sum_h x[r, h] e2m1(code) e4m3(scale).
+//
+// Tiles of features by rows; the codes, their block scales and the rows of L
+// values at a time go to LDS by the loads themselves, several steps ahead;
+// each wave turns the codes of its own features into bf16 operands of the
+// matrix instruction (a code times its block scale has at most 2 + 4
+// significant bits: exact in bf16) and multiplies them with all rows of the
+// tile.  Lane (i, q) of a wave takes feature i and the quarter q of the step's
+// values, so that it holds whole blocks; which value of a step is which does
+// not matter to the sum as long as the rows are read in the same order.
 #include "expert_device.h"
 
 namespace epx {
 namespace {
-
-constexpr int kFewThreads = 256;
 
 // E4M3 byte `at` (0..3) of a word.
 __device__ __forceinline__ float e4m3_of(uint32_t word, int at) {
@@ -17,7 +24,7 @@ __device__ __forceinline__ float e4m3_of(uint32_t word, int at) {
     }
 }
 
-// e2m1(code) * e4m3(scale) of 8 codes: at most 2 by 4 significant bits, exact in bf16.
+// e2m1(code) * scale of 8 codes.
 __device__ __forceinline__ bf16x8 weights8(uint32_t codes, float scale) {
     v4u o;
     f32x2_t p;
@@ -32,167 +39,153 @@ __device__ __forceinline__ bf16x8 weights8(uint32_t codes, float scale) {
     return __builtin_bit_cast(bf16x8, o);
 }
 
-// Few rows: the weights stream from memory into registers, 16 features a
-// wave; lane (i, q) holds feature i and, of every chunk of KC values of the
-// summed dimension, the KC / 4 from q * KC / 4 on, so that its loads are 16
-// consecutive bytes and its block scales are whole.  The matrix instruction
-// does not care which value is which as long as both operands agree: the
-// rows, staged in LDS, are read in the same order.
-// WK waves share the summed dimension, 4 / WK the features.  WORDS: every
-// feature's scales start at a word (in_dim is a multiple of 64).
-//
-// Two chunks of weights are in flight in registers and the rows' chunks go
-// round three LDS buffers, so that one barrier a chunk is enough: a wave
-// stages chunk c + 2, into the buffer of chunk c - 1, only after the barrier
-// of chunk c, which every wave reaches after computing chunk c - 1.
-template <int NR, int KC, int WK, bool WORDS>
-__global__ __launch_bounds__(kFewThreads) void k_nvfp4_few(ExpertArgs a, int32_t ftiles) {
-    static_assert(KC == 512 || KC == 256, "a row's chunk is one load of a wave or half of one");
-    constexpr int kWN = 4 / WK;
-    constexpr int kLane = KC / 4;        // values of a lane and chunk
-    constexpr int kCodes = kLane / 32;   // its 16-byte code loads
-    constexpr int kScales = kLane / 64;  // its 4-byte scale words
-    constexpr int kPitch = KC * 2 + 16;  // LDS bytes of a row's chunk: 16 rows fall on different banks
-    constexpr int kBuffer = WK * NR * kPitch;
-    __shared__ __align__(16) uint8_t lds[3 * kBuffer];
-    __shared__ __align__(16) int32_t scan[16];
+// NT rows and WAVES * FW features a tile, L values a step, BUFS steps in LDS.
+// WORDS: every feature's scales start at a word (in_dim is a multiple of 64)
+// and travel as words; otherwise each scale is loaded as a byte, into a word.
+template <int NT, int FW, int WAVES, int L, int BUFS, bool WORDS>
+__global__ __launch_bounds__(WAVES * kWave) void k_nvfp4(ExpertArgs a, int32_t ftiles) {
+    static_assert(FW * L == 4096, "a wave's scales are 64 words, its codes two loads");
+    constexpr int kThreads = WAVES * kWave;
+    constexpr int kFeatures = WAVES * FW;
+    constexpr int kLane = L / 4;                        // values of a lane and step
+    constexpr int kCodeRow = L / 2, kCodeChunks = kCodeRow / 16;
+    constexpr int kScaleBytes = WORDS ? 256 : 1024;     // of a wave
+    constexpr int kScaleLoads = kScaleBytes / 256;
+    constexpr int kRowBytes = L * 2, kRowChunks = kRowBytes / 16;
+    constexpr int kRowLoads = NT * kRowBytes / 1024 / WAVES;
+    constexpr int kLoads = 2 + kScaleLoads + kRowLoads;  // of a wave and step
+    constexpr int kCodes = kFeatures * kCodeRow, kScales = WAVES * kScaleBytes;
+    constexpr int kBuffer = kCodes + kScales + NT * kRowBytes;
+    static_assert(kRowLoads >= 1 && (BUFS - 2) * kLoads < 64, "");
+    __shared__ __align__(1024) uint8_t lds[BUFS * kBuffer];
+    __shared__ int32_t scan[16];
     const int lane = threadIdx.x & (kWave - 1), w = uniform((int32_t)(threadIdx.x / kWave));
-    const int i = lane % 16, q = lane / 16, wn = w % kWN, wk = w / kWN;
+    const int i = lane % 16, q = lane / 16;
     int32_t f;
-    const RowTile t = find_row_tile<kFewThreads, NR>(
+    const RowTile t = find_row_tile<kThreads, NT>(
         a, scan, [&](int32_t rt, int32_t& ft) { return xcd_tile(rt, ftiles, ft); }, f);
     if (t.expert < 0) return;
-    const int32_t in = a.in, f0 = uniform((f * kWN + wn) * 16);
+    const int32_t in = a.in, f0 = uniform(f * kFeatures + w * FW);
     const int64_t row0 = (int64_t)t.expert * a.on + f0;
-    const int32_t frows = max(min(16, a.on - f0), 0);  // 0: this wave only helps with the staging
+    const int32_t frows = max(min(FW, a.on - f0), 0);  // 0: this wave only helps with the rows
     const int32_t cpitch = in / 2, spitch = in / 16;
-    const __amdgpu_buffer_rsrc_t rc = __builtin_amdgcn_make_buffer_rsrc(
-        const_cast<uint8_t*>(a.codes + row0 * cpitch), (short)0, uniform(frows * cpitch), kBufferWord3);
-    const __amdgpu_buffer_rsrc_t rsc = __builtin_amdgcn_make_buffer_rsrc(
-        const_cast<uint8_t*>(a.scales + row0 * spitch), (short)0, uniform(frows * spitch), kBufferWord3);
-    const int32_t voff_c = i * cpitch + q * (kLane / 2), voff_s = i * spitch + q * (kLane / 16);
+    const uint8_t* const codes = a.codes + row0 * cpitch;
+    const uint8_t* const scales = a.scales + row0 * spitch;
+    const uint16_t* const x = a.x + t.first * in;
 
-    struct Chunk {
-        v4u codes[kCodes];
-        uint32_t scales[kScales];
+    // Step s of this wave's features and of its share of the rows.  LDS rows
+    // are swizzled so that 16 lanes reading 16 rows fall on all banks: chunk c
+    // of a feature's codes lies at c ^ (feature / 2 or / 4), chunk c of a row
+    // at c ^ (row % 16).
+    auto load = [&](int32_t s) {
+        uint8_t* const to = lds + s % BUFS * kBuffer;
+        const int32_t l0 = s * L;
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            const int r = j * (64 / kCodeChunks) + lane / kCodeChunks;
+            const int c = (lane % kCodeChunks) ^ (L == 256 ? r / 2 % 8 : r / 4 % 4);
+            load_to_lds<16>(codes, frows * cpitch, to + w * (FW * kCodeRow) + j * 1024,
+                            l0 + c * 32 < in ? r * cpitch + l0 / 2 + c * 16 : kOutside);
+        }
+#pragma unroll
+        for (int j = 0; j < kScaleLoads; ++j) {
+            constexpr int kPer = WORDS ? L / 64 : L / 16;  // words or scales of a feature
+            const int at = j * kWave + lane, r = at / kPer, c = at % kPer;
+            load_to_lds<WORDS ? 4 : 1>(scales, frows * spitch, to + kCodes + w * kScaleBytes + j * 256,
+                                       l0 + c * (L / kPer) < in ? r * spitch + l0 / 16 + c * (WORDS ? 4 : 1) : kOutside);
+        }
+#pragma unroll
+        for (int j = 0; j < kRowLoads; ++j) {
+            const int at = w * kRowLoads + j, r = at * (64 / kRowChunks) + lane / kRowChunks;
+            const int c = (lane % kRowChunks) ^ (r % 16);
+            load_to_lds<16>(x, t.rows * in * 2, to + kCodes + kScales + at * 1024,
+                            l0 + c * 8 < in ? r * in * 2 + l0 * 2 + c * 16 : kOutside);
+        }
     };
-    const int32_t chunks = (in + WK * KC - 1) / (WK * KC);
-    // Weights of chunk c of this wave: values [l, l + KC), l = (c WK + wk) KC.
-    // Past a feature's end the next one's codes arrive (zeros past the last).
-    auto load = [&](Chunk& ch, int32_t c) {
-        const int32_t l = (c * WK + wk) * KC;
+    f32x4 acc[FW / 16][NT / 16] = {};
+    const int32_t steps = (in + L - 1) / L;
+    for (int s = 0; s < BUFS - 1; ++s) load(s);
+    for (int32_t s = 0; s < steps; ++s) {
+        // This step's loads have landed when only the later steps' are
+        // outstanding: loads return in order, and past the end they still
+        // count, and write zeros.  Behind the barrier every wave's have, and
+        // every wave is done with the last step's buffer, which is filled next.
+        asm volatile("s_waitcnt vmcnt(%0)" ::"n"((BUFS - 2) * kLoads) : "memory");
+        lds_barrier();
+        load(s + BUFS - 1);
+        const uint8_t* const from = lds + s % BUFS * kBuffer;
+        v4u cw[FW / 16][kLane / 32];
+        float sc[FW / 16][kLane / 16];
 #pragma unroll
-        for (int j = 0; j < kCodes; ++j) ch.codes[j] = __builtin_amdgcn_raw_buffer_load_b128(rc, voff_c + l / 2 + j * 16, 0, 2);
+        for (int g = 0; g < FW / 16; ++g) {
+            const int r = g * 16 + i;
+            const uint8_t* const p = from + (w * FW + r) * kCodeRow;
 #pragma unroll
-        for (int j = 0; j < kScales; ++j) {
-            const int32_t at = voff_s + l / 16 + j * 4;
-            if constexpr (WORDS) {
-                ch.scales[j] = __builtin_amdgcn_raw_buffer_load_b32(rsc, at, 0, 0);
-            } else {  // features whose scales start between words
-                uint32_t v = 0;
+            for (int h = 0; h < kLane / 32; ++h) {
+                const int c = q * (kLane / 32) + h;
+                cw[g][h] = *reinterpret_cast<const v4u*>(p + (c ^ (L == 256 ? r / 2 % 8 : r / 4 % 4)) * 16);
+            }
+            const uint8_t* const ps = from + kCodes + w * kScaleBytes;
+            const int b = r * (L / 16) + q * (kLane / 16);  // the lane's first block
 #pragma unroll
-                for (int b = 0; b < 4; ++b)
-                    v |= (uint32_t)(uint8_t)__builtin_amdgcn_raw_buffer_load_b8(rsc, at + b, 0, 0) << (8 * b);
-                ch.scales[j] = v;
+            for (int h = 0; h < kLane / 16; ++h) {
+                if constexpr (WORDS && L == 256)
+                    sc[g][h] = e4m3_of(*reinterpret_cast<const uint32_t*>(ps + b), h);
+                else if constexpr (WORDS)
+                    sc[g][h] = e4m3_of(*reinterpret_cast<const uint16_t*>(ps + b), h);
+                else
+                    sc[g][h] = e4m3_of(reinterpret_cast<const uint32_t*>(ps)[b + h], 0);
             }
         }
-    };
-    // The rows' part of chunk c: row r at r * kPitch of the wave group's buffer.
-    auto stage = [&](int32_t c) {
-        const int32_t l = (c * WK + wk) * KC;
-        uint8_t* to = lds + (c % 3) * kBuffer + wk * NR * kPitch;
-        const int32_t voff = l + lane * 8 < in ? (l + lane * 8) * 2 : kOutside;
-        for (int r = wn; r < t.rows; r += kWN)
-            if (KC == 512 || lane < 32)
-                load_to_lds(a.x + (t.first + r) * in, in * 2, reinterpret_cast<uint16_t*>(to + r * kPitch), voff);
-    };
-    f32x4 acc[NR / 16] = {};
-    auto compute = [&](const Chunk& ch, int32_t c) {
-        const uint8_t* from = lds + (c % 3) * kBuffer + wk * NR * kPitch + i * kPitch + q * (kLane * 2);
-        const int32_t left = (in - (c * WK + wk) * KC - q * kLane) / 16;  // of this lane's blocks: those before the end
-        uint32_t sc[kScales];
-#pragma unroll
-        for (int j = 0; j < kScales; ++j) {
-            const int n = min(max(left - 4 * j, 0), 4);
-            sc[j] = n == 4 ? ch.scales[j] : ch.scales[j] & ((1u << (8 * n)) - 1);
-        }
+        const uint8_t* const rows = from + kCodes + kScales + i * kRowBytes;
 #pragma unroll
         for (int j = 0; j < kLane / 8; ++j) {
-            const bf16x8 wv = weights8(ch.codes[j / 4][j % 4], e4m3_of(sc[j / 8], j / 2 % 4));
+            bf16x8 wv[FW / 16];
 #pragma unroll
-            for (int n = 0; n < NR / 16; ++n) {
-                const bf16x8 xv = *reinterpret_cast<const bf16x8*>(from + n * 16 * kPitch + j * 16);
-                acc[n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wv, xv, acc[n], 0, 0, 0);
-            }
-        }
-    };
-    Chunk ch[2];
-    stage(0);
-    load(ch[0], 0);
-    asm volatile("" ::: "memory");  // chunk 0's loads are the older ones
-    if (chunks > 1) {
-        stage(1);
-        load(ch[1], 1);
-    }
-    for (int32_t c = 0; c < chunks; c += 2) {
+            for (int g = 0; g < FW / 16; ++g) wv[g] = weights8(cw[g][j / 4][j % 4], sc[g][j / 2]);
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            if (c + h >= chunks) break;
-            // This chunk's rows are in LDS once all loads but the next chunk's
-            // weights have returned (loads return in order).
-            if (c + h + 1 < chunks)
-                asm volatile("s_waitcnt vmcnt(%0)" ::"n"(kCodes + kScales) : "memory");
-            else
-                asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-            lds_barrier();
-            compute(ch[h], c + h);
-            asm volatile("" ::: "memory");
-            if (c + h + 2 < chunks) {
-                stage(c + h + 2);
-                load(ch[h], c + h + 2);
+            for (int n = 0; n < NT / 16; ++n) {
+                const bf16x8 xv = *reinterpret_cast<const bf16x8*>(rows + n * 16 * kRowBytes +
+                                                                   ((q * (kLane / 8) + j) ^ i) * 16);
+#pragma unroll
+                for (int g = 0; g < FW / 16; ++g)
+                    acc[g][n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wv[g], xv, acc[g][n], 0, 0, 0);
             }
         }
     }
-    if constexpr (WK > 1) {  // the waves' shares, added in their order
-        f32x4* part = reinterpret_cast<f32x4*>(lds);
-        __syncthreads();
-        if (wk > 0)
+    // No load may land in LDS that belongs to another workgroup by then.
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    // acc[g][n][j]: feature f0 + 16 g + 4 q + j, row 16 n + i
 #pragma unroll
-            for (int n = 0; n < NR / 16; ++n) part[(((wk - 1) * kWN + wn) * (NR / 16) + n) * kWave + lane] = acc[n];
-        __syncthreads();
-        if (wk > 0) return;
+    for (int g = 0; g < FW / 16; ++g) {
+        const int32_t fe = g * 16 + q * 4;
+        if (f0 + fe >= a.on) continue;
+        const v2u rs = *reinterpret_cast<const v2u*>(a.rowscale + row0 + fe);
 #pragma unroll
-        for (int s = 0; s < WK - 1; ++s)
-#pragma unroll
-            for (int n = 0; n < NR / 16; ++n) acc[n] += part[((s * kWN + wn) * (NR / 16) + n) * kWave + lane];
-    }
-    // acc[n][j]: feature f0 + 4 q + j, row 16 n + i
-    const int32_t fe = f0 + q * 4;
-    if (fe >= a.on) return;
-    const v2u rs = *reinterpret_cast<const v2u*>(a.rowscale + row0 + q * 4);
-#pragma unroll
-    for (int n = 0; n < NR / 16; ++n) {
-        const int32_t r = n * 16 + i;
-        if (r >= t.rows) continue;
-        const v2u o = {pack_bf16x2(acc[n][0] * bf16_lo(rs.x), acc[n][1] * bf16_hi(rs.x)),
-                       pack_bf16x2(acc[n][2] * bf16_lo(rs.y), acc[n][3] * bf16_hi(rs.y))};
-        *reinterpret_cast<v2u*>(static_cast<uint16_t*>(a.out) + (t.first + r) * a.on + fe) = o;
+        for (int n = 0; n < NT / 16; ++n) {
+            const int32_t r = n * 16 + i;
+            if (r >= t.rows) continue;
+            const v2u o = {pack_bf16x2(acc[g][n][0] * bf16_lo(rs.x), acc[g][n][1] * bf16_hi(rs.x)),
+                           pack_bf16x2(acc[g][n][2] * bf16_lo(rs.y), acc[g][n][3] * bf16_hi(rs.y))};
+            *reinterpret_cast<v2u*>(static_cast<uint16_t*>(a.out) + (t.first + r) * a.on + f0 + fe) = o;
+        }
     }
 }
 
-template <int NR, int KC, int WK>
-hipError_t few(const ExpertArgs& a, hipStream_t stream) {
-    constexpr int kF = 64 / WK;
+// BYTES: steps that LDS holds where the scales travel as bytes.
+template <int NT, int FW, int WAVES, int L, int BUFS, int BYTES>
+hipError_t nvfp4(const ExpertArgs& a, hipStream_t stream) {
+    constexpr int kF = FW * WAVES;
     const int32_t ftiles = (a.on + kF - 1) / kF;
-    const int64_t tiles = max_row_tiles(a, NR) * ftiles, blocks = (tiles + 7) / 8 * 8;
+    const int64_t tiles = max_row_tiles(a, NT) * ftiles, blocks = (tiles + 7) / 8 * 8;
     if (tiles == 0) return hipSuccess;
-    if (blocks * kFewThreads > 0xFFFFFFFFll) return hipErrorInvalidValue;
+    if (blocks * WAVES * kWave > 0xFFFFFFFFll) return hipErrorInvalidValue;
     if (a.in % 64 == 0)
-        hipLaunchKernelGGL((k_nvfp4_few<NR, KC, WK, true>), dim3((unsigned)blocks), dim3(kFewThreads), 0, stream, a,
-                           ftiles);
+        hipLaunchKernelGGL((k_nvfp4<NT, FW, WAVES, L, BUFS, true>), dim3((unsigned)blocks), dim3(WAVES * kWave), 0,
+                           stream, a, ftiles);
     else
-        hipLaunchKernelGGL((k_nvfp4_few<NR, KC, WK, false>), dim3((unsigned)blocks), dim3(kFewThreads), 0, stream, a,
-                           ftiles);
+        hipLaunchKernelGGL((k_nvfp4<NT, FW, WAVES, L, BYTES, false>), dim3((unsigned)blocks), dim3(WAVES * kWave), 0,
+                           stream, a, ftiles);
     return hipGetLastError();
 }
 
@@ -202,10 +195,10 @@ hipError_t launch_expert_gemm_nvfp4(const ExpertArgs& a, hipStream_t stream) {
     const int64_t groups = a.slots < a.E + a.shared ? a.slots : a.E + a.shared;
     if (groups == 0) return hipSuccess;
     const int64_t mean = a.slots / groups;
-    if (mean > 24) return few<64, 256, 1>(a, stream);
-    if (mean > 10) return few<32, 256, 1>(a, stream);
-    if (groups * ((a.on + 63) / 64) < 256) return few<16, 256, 4>(a, stream);
-    return few<16, 512, 1>(a, stream);
+    if (mean > 56) return nvfp4<128, 32, 8, 128, 3, 2>(a, stream);
+    if (mean > 24) return nvfp4<64, 16, 8, 256, 3, 2>(a, stream);
+    if (mean > 10) return nvfp4<32, 16, 8, 256, 4, 3>(a, stream);
+    return nvfp4<16, 16, 4, 256, 4, 3>(a, stream);
 }
 
 }  // namespace epx
