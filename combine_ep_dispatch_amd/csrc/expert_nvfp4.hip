@@ -6,9 +6,9 @@
 // each wave turns the codes of its own features into bf16 operands of the
 // matrix instruction (a code times its block scale has at most 2 + 4
 // significant bits: exact in bf16) and multiplies them with all rows of the
-// tile.  Lane (i, q) of a wave takes feature i and the quarter q of the step's
-// values, so that it holds whole blocks; which value of a step is which does
-// not matter to the sum as long as the rows are read in the same order.
+// tile.  Lane (i, q) of a wave takes feature i and 32 values, two whole blocks,
+// of every 128 of the step; which value of a step is which does not matter to
+// the sum as long as the rows are read in the same order.
 #include "expert_device.h"
 
 namespace epx {
@@ -38,6 +38,15 @@ __device__ __forceinline__ bf16x8 weights8(uint32_t codes, float scale) {
     o.w = pack_bf16x2(p.x * scale, p.y * scale);
     return __builtin_bit_cast(bf16x8, o);
 }
+
+// LDS rows are swizzled, chunk c of 16 bytes of row r at c ^ swizzle(r).  A
+// 16-byte LDS read serves 16 lanes at a time, and those are rows 0-3 and 12-15
+// of one quarter q with rows 4-11 of the next: the swizzles keep these apart
+// for q even and odd (rows with bits 2 and 3 alike go to other chunks than the
+// rest, whatever q adds).
+__device__ __forceinline__ int swizzle_row(int r) { return (r % 16) ^ (r & 4) << 1; }            // 16 chunks or more
+__device__ __forceinline__ int swizzle_codes8(int r) { return r / 2 % 8; }                       // 8 chunks
+__device__ __forceinline__ int swizzle_codes4(int r) { return (r / 4 % 2) | ((r / 4 ^ r / 8) & 1) << 1; }  // 4 chunks
 
 // NT rows and WAVES * FW features a tile, L values a step, BUFS steps in LDS.
 // WORDS: every feature's scales start at a word (in_dim is a multiple of 64)
@@ -73,17 +82,14 @@ __global__ __launch_bounds__(WAVES * kWave) void k_nvfp4(ExpertArgs a, int32_t f
     const uint8_t* const scales = a.scales + row0 * spitch;
     const uint16_t* const x = a.x + t.first * in;
 
-    // Step s of this wave's features and of its share of the rows.  LDS rows
-    // are swizzled so that 16 lanes reading 16 rows fall on all banks: chunk c
-    // of a feature's codes lies at c ^ (feature / 2 or / 4), chunk c of a row
-    // at c ^ (row % 16).
+    // Step s of this wave's features and of its share of the rows.
     auto load = [&](int32_t s) {
         uint8_t* const to = lds + s % BUFS * kBuffer;
         const int32_t l0 = s * L;
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
             const int r = j * (64 / kCodeChunks) + lane / kCodeChunks;
-            const int c = (lane % kCodeChunks) ^ (L == 256 ? r / 2 % 8 : r / 4 % 4);
+            const int c = (lane % kCodeChunks) ^ (L == 256 ? swizzle_codes8(r) : swizzle_codes4(r));
             load_to_lds<16>(codes, frows * cpitch, to + w * (FW * kCodeRow) + j * 1024,
                             l0 + c * 32 < in ? r * cpitch + l0 / 2 + c * 16 : kOutside);
         }
@@ -97,7 +103,7 @@ __global__ __launch_bounds__(WAVES * kWave) void k_nvfp4(ExpertArgs a, int32_t f
 #pragma unroll
         for (int j = 0; j < kRowLoads; ++j) {
             const int at = w * kRowLoads + j, r = at * (64 / kRowChunks) + lane / kRowChunks;
-            const int c = (lane % kRowChunks) ^ (r % 16);
+            const int c = (lane % kRowChunks) ^ swizzle_row(r);
             load_to_lds<16>(x, t.rows * in * 2, to + kCodes + kScales + at * 1024,
                             l0 + c * 8 < in ? r * in * 2 + l0 * 2 + c * 16 : kOutside);
         }
@@ -120,21 +126,21 @@ __global__ __launch_bounds__(WAVES * kWave) void k_nvfp4(ExpertArgs a, int32_t f
         for (int g = 0; g < FW / 16; ++g) {
             const int r = g * 16 + i;
             const uint8_t* const p = from + (w * FW + r) * kCodeRow;
+            const uint8_t* const ps = from + kCodes + w * kScaleBytes;
 #pragma unroll
             for (int h = 0; h < kLane / 32; ++h) {
-                const int c = q * (kLane / 32) + h;
-                cw[g][h] = *reinterpret_cast<const v4u*>(p + (c ^ (L == 256 ? r / 2 % 8 : r / 4 % 4)) * 16);
-            }
-            const uint8_t* const ps = from + kCodes + w * kScaleBytes;
-            const int b = r * (L / 16) + q * (kLane / 16);  // the lane's first block
-#pragma unroll
-            for (int h = 0; h < kLane / 16; ++h) {
-                if constexpr (WORDS && L == 256)
-                    sc[g][h] = e4m3_of(*reinterpret_cast<const uint32_t*>(ps + b), h);
-                else if constexpr (WORDS)
-                    sc[g][h] = e4m3_of(*reinterpret_cast<const uint16_t*>(ps + b), h);
-                else
-                    sc[g][h] = e4m3_of(reinterpret_cast<const uint32_t*>(ps)[b + h], 0);
+                const int c = h * 4 + q;  // the chunk of 32 codes; its blocks are 2 c and 2 c + 1
+                cw[g][h] = *reinterpret_cast<const v4u*>(p + (c ^ (L == 256 ? swizzle_codes8(r) : swizzle_codes4(r))) * 16);
+                const int b = r * (L / 16) + c * 2;
+                if constexpr (WORDS) {
+                    const uint32_t two = *reinterpret_cast<const uint16_t*>(ps + b);
+                    sc[g][2 * h] = e4m3_of(two, 0);
+                    sc[g][2 * h + 1] = e4m3_of(two, 1);
+                } else {
+                    const v2u two = *reinterpret_cast<const v2u*>(ps + b * 4);
+                    sc[g][2 * h] = e4m3_of(two.x, 0);
+                    sc[g][2 * h + 1] = e4m3_of(two.y, 0);
+                }
             }
         }
         const uint8_t* const rows = from + kCodes + kScales + i * kRowBytes;
@@ -146,7 +152,7 @@ __global__ __launch_bounds__(WAVES * kWave) void k_nvfp4(ExpertArgs a, int32_t f
 #pragma unroll
             for (int n = 0; n < NT / 16; ++n) {
                 const bf16x8 xv = *reinterpret_cast<const bf16x8*>(rows + n * 16 * kRowBytes +
-                                                                   ((q * (kLane / 8) + j) ^ i) * 16);
+                                                                   (((j / 4 * 4 + q) * 4 + j % 4) ^ swizzle_row(i)) * 16);
 #pragma unroll
                 for (int g = 0; g < FW / 16; ++g)
                     acc[g][n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wv[g], xv, acc[g][n], 0, 0, 0);
