@@ -82,30 +82,47 @@ __global__ __launch_bounds__(WAVES * kWave) void k_nvfp4(ExpertArgs a, int32_t f
     const uint8_t* const scales = a.scales + row0 * spitch;
     const uint16_t* const x = a.x + t.first * in;
 
-    // Step s of this wave's features and of its share of the rows.
+    // A wave's loads of a step: where the lane's bytes are in the operands'
+    // step 0, and the first value they hold.
+    int32_t off[kLoads], first[kLoads];
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+        const int r = j * (64 / kCodeChunks) + lane / kCodeChunks;
+        const int c = (lane % kCodeChunks) ^ (L == 256 ? swizzle_codes8(r) : swizzle_codes4(r));
+        off[j] = r * cpitch + c * 16;
+        first[j] = c * 32;
+    }
+#pragma unroll
+    for (int j = 0; j < kScaleLoads; ++j) {
+        constexpr int kPer = WORDS ? L / 64 : L / 16;  // words or scales of a feature
+        const int at = j * kWave + lane, r = at / kPer, c = at % kPer;
+        off[2 + j] = r * spitch + c * (WORDS ? 4 : 1);
+        first[2 + j] = c * (L / kPer);
+    }
+#pragma unroll
+    for (int j = 0; j < kRowLoads; ++j) {
+        const int r = (w * kRowLoads + j) * (64 / kRowChunks) + lane / kRowChunks;
+        const int c = (lane % kRowChunks) ^ swizzle_row(r);
+        off[2 + kScaleLoads + j] = r * in * 2 + c * 16;
+        first[2 + kScaleLoads + j] = c * 8;
+    }
+    // Step s of this wave's features and of its share of the rows; lanes past
+    // the end of the summed dimension read nothing.
     auto load = [&](int32_t s) {
         uint8_t* const to = lds + s % BUFS * kBuffer;
         const int32_t l0 = s * L;
+        const bool whole = l0 + L <= in;
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            const int r = j * (64 / kCodeChunks) + lane / kCodeChunks;
-            const int c = (lane % kCodeChunks) ^ (L == 256 ? swizzle_codes8(r) : swizzle_codes4(r));
-            load_to_lds<16>(codes, frows * cpitch, to + w * (FW * kCodeRow) + j * 1024,
-                            l0 + c * 32 < in ? r * cpitch + l0 / 2 + c * 16 : kOutside);
-        }
-#pragma unroll
-        for (int j = 0; j < kScaleLoads; ++j) {
-            constexpr int kPer = WORDS ? L / 64 : L / 16;  // words or scales of a feature
-            const int at = j * kWave + lane, r = at / kPer, c = at % kPer;
-            load_to_lds<WORDS ? 4 : 1>(scales, frows * spitch, to + kCodes + w * kScaleBytes + j * 256,
-                                       l0 + c * (L / kPer) < in ? r * spitch + l0 / 16 + c * (WORDS ? 4 : 1) : kOutside);
-        }
-#pragma unroll
-        for (int j = 0; j < kRowLoads; ++j) {
-            const int at = w * kRowLoads + j, r = at * (64 / kRowChunks) + lane / kRowChunks;
-            const int c = (lane % kRowChunks) ^ swizzle_row(r);
-            load_to_lds<16>(x, t.rows * in * 2, to + kCodes + kScales + at * 1024,
-                            l0 + c * 8 < in ? r * in * 2 + l0 * 2 + c * 16 : kOutside);
+        for (int j = 0; j < kLoads; ++j) {
+            const int32_t v = whole || l0 + first[j] < in ? off[j] : kOutside;
+            if (j < 2)
+                load_to_lds<16>(codes, frows * cpitch, to + w * (FW * kCodeRow) + j * 1024, v, l0 / 2);
+            else if (j < 2 + kScaleLoads)
+                load_to_lds<WORDS ? 4 : 1>(scales, frows * spitch, to + kCodes + w * kScaleBytes + (j - 2) * 256, v,
+                                           l0 / 16);
+            else
+                load_to_lds<16>(x, t.rows * in * 2,
+                                to + kCodes + kScales + (w * kRowLoads + j - 2 - kScaleLoads) * 1024, v, l0 * 2);
         }
     };
     f32x4 acc[FW / 16][NT / 16] = {};
@@ -204,7 +221,7 @@ hipError_t launch_expert_gemm_nvfp4(const ExpertArgs& a, hipStream_t stream) {
     if (mean > 56) return nvfp4<128, 32, 8, 128, 3, 2>(a, stream);
     if (mean > 24) return nvfp4<64, 16, 8, 256, 3, 2>(a, stream);
     if (mean > 10) return nvfp4<32, 16, 8, 256, 4, 3>(a, stream);
-    return nvfp4<16, 16, 4, 256, 4, 3>(a, stream);
+    return nvfp4<16, 16, 4, 256, 3, 3>(a, stream);
 }
 
 }  // namespace epx
