@@ -4,7 +4,17 @@
 // moe_router_dtype: fp32 routing weights; fused_a2a page,
 // HybridEPDispatch.forward: topk_idx with -1 for unused slots).
 //
-// One wave per token; lane l holds experts l, l + 64, ...
+// One wave per token; lane l holds experts [l VPL, (l + 1) VPL).  Keys are
+// 32-bit integers that order like the floats they stand for, so that the
+// largest of a wave is six cross-lane maxima; the K experts are taken one by
+// one.
+//
+// Without a bias a key is the logit, and the order is exact.  With one it is
+// score + bias, whose fp32 value is off by a few roundings (key_error below):
+// wherever two keys, or two groups' keys, lie closer than that, the token is
+// chosen again from 64-bit keys.  That is about one token in a hundred with
+// normal logits; 64-bit keys for all of them took 15.9 instead of 5.2 us at
+// 4096 tokens of 256 experts.
 #include "epx_device.h"
 
 namespace epx {
@@ -13,55 +23,141 @@ namespace {
 constexpr int kTopkThreads = 256;
 constexpr int kTopkWaves = kTopkThreads / kWave;
 
-template <typename T>
-__device__ __forceinline__ T wave_sum(T v) {
+typedef uint32_t v4u __attribute__((ext_vector_type(4)));
+typedef uint32_t v2u __attribute__((ext_vector_type(2)));
+
+// DPP controls for a reduction over the wave: row shifts by 1, 2, 4 and 8
+// lanes, then the last lane of a row into the next rows.  Lane 63 has it all.
+template <typename F>
+__device__ __forceinline__ uint32_t wave_reduce(uint32_t v, uint32_t identity, F f) {
+    v = f(v, (uint32_t)__builtin_amdgcn_update_dpp((int)identity, (int)v, 0x111, 0xf, 0xf, false));
+    v = f(v, (uint32_t)__builtin_amdgcn_update_dpp((int)identity, (int)v, 0x112, 0xf, 0xf, false));
+    v = f(v, (uint32_t)__builtin_amdgcn_update_dpp((int)identity, (int)v, 0x114, 0xf, 0xf, false));
+    v = f(v, (uint32_t)__builtin_amdgcn_update_dpp((int)identity, (int)v, 0x118, 0xf, 0xf, false));
+    v = f(v, (uint32_t)__builtin_amdgcn_update_dpp((int)identity, (int)v, 0x142, 0xa, 0xf, false));
+    v = f(v, (uint32_t)__builtin_amdgcn_update_dpp((int)identity, (int)v, 0x143, 0xc, 0xf, false));
+    return (uint32_t)__builtin_amdgcn_readlane((int)v, 63);
+}
+__device__ __forceinline__ uint32_t wave_max(uint32_t v) {
+    return wave_reduce(v, 0u, [](uint32_t a, uint32_t b) { return a > b ? a : b; });
+}
+__device__ __forceinline__ float wave_sum(float v) {
+    return __uint_as_float(wave_reduce(__float_as_uint(v), 0u, [](uint32_t a, uint32_t b) {
+        return __float_as_uint(__uint_as_float(a) + __uint_as_float(b));
+    }));
+}
+
+// Floats as integers of the same order, from 1 on (0: no candidate); NaN has none.
+__device__ __forceinline__ uint32_t ordered(float f) {
+    const uint32_t u = __float_as_uint(f + 0.0f);  // -0 and +0 are one value
+    return u ^ ((uint32_t)((int32_t)u >> 31) | 0x80000000u);
+}
+__device__ __forceinline__ float unordered(uint32_t u) {
+    return __uint_as_float(u ^ (u >> 31 ? 0x80000000u : 0xFFFFFFFFu));
+}
+
+__device__ __forceinline__ float lane_value(float v, int lane) {
+    return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), lane));
+}
+
+template <bool BF16>
+__device__ __forceinline__ float logit(const void* p, int64_t i) {
+    if constexpr (BF16) return bf16_lo(static_cast<const uint16_t*>(p)[i]);
+    return static_cast<const float*>(p)[i];
+}
+
+// The lane's VPL logits; -infinity past the last expert.  Rows of 64 VPL
+// experts are read as vectors.
+template <int VPL, bool BF16>
+__device__ __forceinline__ void load_logits(const TopkArgs& a, int64_t row, int lane, float (&z)[VPL]) {
+    if (VPL % 4 == 0 && a.E == VPL * kWave) {
 #pragma unroll
-    for (int o = kWave / 2; o > 0; o >>= 1) v += __shfl_xor(v, o, kWave);
-    return v;
-}
-
-__device__ __forceinline__ float load_logit(const TopkArgs& a, int64_t i) {
-    if (a.bf16) return bf16_lo(static_cast<const uint16_t*>(a.logits)[i]);
-    return static_cast<const float*>(a.logits)[i];
-}
-
-// VPL: experts of a lane.
-template <int VPL>
-__global__ __launch_bounds__(kTopkThreads) void k_route(TopkArgs a) {
-    __shared__ double s_key[kTopkWaves][VPL * kWave];
-    const int w = threadIdx.x / kWave, lane = threadIdx.x & (kWave - 1);
-    const int32_t t = uniform((int32_t)(blockIdx.x * kTopkWaves + w));
-    if (t >= a.T) return;  // no barrier below: each wave uses its own part of s_key
-    const int64_t row = (int64_t)t * a.E;
-    if (a.mask != nullptr && a.mask[t] == 0) {
-        if (lane < a.K) {
-            a.ids[(int64_t)t * a.K + lane] = -1;
-            a.probs[(int64_t)t * a.K + lane] = 0.0f;
+        for (int i = 0; i < VPL / 4 * 4; i += 4) {
+            const int64_t at = row + lane * VPL + i;
+            if constexpr (BF16) {
+                const v2u v = *reinterpret_cast<const v2u*>(static_cast<const uint16_t*>(a.logits) + at);
+                z[i] = bf16_lo(v.x), z[i + 1] = bf16_hi(v.x), z[i + 2] = bf16_lo(v.y), z[i + 3] = bf16_hi(v.y);
+            } else {
+                const v4u v = *reinterpret_cast<const v4u*>(static_cast<const float*>(a.logits) + at);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) z[i + j] = __uint_as_float(v[j]);
+            }
         }
         return;
     }
-    float z[VPL];
-    double key[VPL];
-    float zmax = -INFINITY;
 #pragma unroll
     for (int i = 0; i < VPL; ++i) {
-        const int32_t e = i * kWave + lane;
-        z[i] = e < a.E ? load_logit(a, row + e) : -INFINITY;
-        zmax = fmaxf(zmax, z[i]);
+        const int32_t e = lane * VPL + i;
+        z[i] = e < a.E ? logit<BF16>(a.logits, row + e) : -INFINITY;
     }
+}
+
+// A bound on how far an fp32 key with a bias is from the 64-bit one.  Sigmoid:
+// exp2 of a rounded argument, 1 + e, the reciprocal, the sum with the bias:
+// each at most 2^-24 of a value of at most 1, or of the key.  Softmax: exp's
+// argument is rounded relative to its size d (d exp(-d) < 0.4), the sum over
+// the experts and the division by it: fewer than 40 + VPL such roundings.
+__device__ __forceinline__ float key_error(const TopkArgs& a, float largest, int vpl) {
+    return ((a.sigmoid ? 6.0f : 42.0f + vpl) + largest) * 1.1920929e-7f;  // 2^-23
+}
+
+// The two largest of two sorted pairs.
+template <typename T>
+__device__ __forceinline__ void merge(T& b0, T& b1, T o0, T o1) {
+    const T lo = b0 < o0 ? b0 : o0, hi = b1 < o1 ? o1 : b1;
+    b0 = b0 < o0 ? o0 : b0;
+    b1 = lo < hi ? hi : lo;
+}
+
+// Largest (with a bias: sum of the two largest) key of every group, in all
+// lanes that hold the group's experts; per: lanes of a group.  Only where
+// every lane's experts belong to one group.
+template <int VPL>
+__device__ __forceinline__ float group_key(const float (&key)[VPL], int per, bool two) {
+    float b0 = -INFINITY, b1 = -INFINITY;
 #pragma unroll
-    for (int o = kWave / 2; o > 0; o >>= 1) zmax = fmaxf(zmax, __shfl_xor(zmax, o, kWave));
+    for (int i = 0; i < VPL; ++i) {
+        b1 = fmaxf(b1, fminf(b0, key[i]));
+        b0 = fmaxf(b0, key[i]);
+    }
+    auto across = [&](int ctrl_is, float v) {
+        const int u = __float_as_int(v);
+        switch (ctrl_is) {
+            case 1: return __int_as_float(__builtin_amdgcn_update_dpp(u, u, 0xB1, 0xf, 0xf, false));   // lane ^ 1
+            case 2: return __int_as_float(__builtin_amdgcn_update_dpp(u, u, 0x4E, 0xf, 0xf, false));   // lane ^ 2
+            case 4: return __int_as_float(__builtin_amdgcn_update_dpp(u, u, 0x141, 0xf, 0xf, false));  // 7 - lane of 8
+            case 8: return __int_as_float(__builtin_amdgcn_update_dpp(u, u, 0x140, 0xf, 0xf, false));  // 15 - lane of 16
+            default: return __shfl_xor(v, ctrl_is, kWave);
+        }
+    };
+#define EPX_MERGE(n)                                         \
+    if (per > n) {                                           \
+        const float o0 = across(n, b0), o1 = across(n, b1);  \
+        merge(b0, b1, o0, o1);                               \
+    }
+    EPX_MERGE(1) EPX_MERGE(2) EPX_MERGE(4) EPX_MERGE(8) EPX_MERGE(16) EPX_MERGE(32)
+#undef EPX_MERGE
+    return two ? b0 + b1 : b0;
+}
+
+// The choice in full: keys of 64 bits where there is a bias, groups of any
+// size.  Lane k gets the k-th expert (-1: none) and its logit.
+template <int VPL>
+__device__ void choose_exactly(const TopkArgs& a, const float (&z)[VPL], float zmax, int lane, double* s_key,
+                               int32_t& my_id, float& my_z) {
+    double key[VPL];
     double total = 1.0;
-    if (!a.sigmoid) {
-        double sum = 0.0;
+    if (a.bias != nullptr && !a.sigmoid) {
+        total = 0.0;
 #pragma unroll
         for (int i = 0; i < VPL; ++i)
-            if (i * kWave + lane < a.E) sum += exp((double)z[i] - (double)zmax);
-        total = wave_sum(sum);
+            if (lane * VPL + i < a.E) total += exp((double)z[i] - (double)zmax);
+#pragma unroll
+        for (int o = kWave / 2; o > 0; o >>= 1) total += __shfl_xor(total, o, kWave);
     }
 #pragma unroll
     for (int i = 0; i < VPL; ++i) {
-        const int32_t e = i * kWave + lane;
+        const int32_t e = lane * VPL + i;
         key[i] = z[i];
         if (a.bias != nullptr && e < a.E) {
             const double s = a.sigmoid ? 1.0 / (1.0 + exp(-(double)z[i])) : exp((double)z[i] - (double)zmax) / total;
@@ -72,15 +168,14 @@ __global__ __launch_bounds__(kTopkThreads) void k_route(TopkArgs a) {
     if (a.groups > 1) {
         const int per = a.E / a.groups;
 #pragma unroll
-        for (int i = 0; i < VPL; ++i) s_key[w][i * kWave + lane] = key[i];
+        for (int i = 0; i < VPL; ++i) s_key[lane * VPL + i] = key[i];
         __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
         double gkey = -INFINITY;
         if (lane < a.groups) {
             double b0 = -INFINITY, b1 = -INFINITY;
             for (int j = 0; j < per; ++j) {
-                const double k = s_key[w][lane * per + j];
-                b1 = k > b0 ? b0 : (k > b1 ? k : b1);
-                b0 = k > b0 ? k : b0;
+                const double k = s_key[lane * per + j];
+                merge(b0, b1, k, (double)-INFINITY);
             }
             gkey = a.bias != nullptr && per > 1 ? b0 + b1 : b0;
         }
@@ -92,12 +187,11 @@ __global__ __launch_bounds__(kTopkThreads) void k_route(TopkArgs a) {
         const uint64_t kept = __builtin_amdgcn_ballot_w64(lane < a.groups && before < a.top_groups);
 #pragma unroll
         for (int i = 0; i < VPL; ++i) {
-            const int32_t e = i * kWave + lane;
+            const int32_t e = lane * VPL + i;
             if (e >= a.E || !((kept >> (e / per)) & 1)) key[i] = -INFINITY;
         }
     }
-    int32_t my_id = -1;
-    float my_s = 0.0f;
+    my_id = -1;
     for (int k = 0; k < a.K; ++k) {
         double best = -INFINITY;
         int32_t at = 0x7FFFFFFF;
@@ -105,7 +199,7 @@ __global__ __launch_bounds__(kTopkThreads) void k_route(TopkArgs a) {
         for (int i = 0; i < VPL; ++i)
             if (key[i] > best) {
                 best = key[i];
-                at = i * kWave + lane;
+                at = lane * VPL + i;
             }
 #pragma unroll
         for (int o = kWave / 2; o > 0; o >>= 1) {
@@ -117,47 +211,176 @@ __global__ __launch_bounds__(kTopkThreads) void k_route(TopkArgs a) {
             }
         }
         if (!(best > -INFINITY)) break;  // no expert left to choose
-        float s = 0.0f;
+        float zk = 0.0f;
 #pragma unroll
         for (int i = 0; i < VPL; ++i)
-            if (at == i * kWave + lane) {
+            if (at == lane * VPL + i) {
                 key[i] = -INFINITY;
-                s = z[i];
+                zk = z[i];
             }
-        s = __shfl(s, at & (kWave - 1), kWave);
-        s = a.sigmoid ? 1.0f / (1.0f + expf(-s)) : expf(s - zmax) / (float)total;
+        zk = __shfl(zk, at / VPL, kWave);
         if (lane == k) {
             my_id = at;
-            my_s = s;
+            my_z = zk;
         }
-    }
-    float p = my_s;
-    if (a.normalize) p = my_s / (wave_sum(my_s) + 1e-20f);
-    if (lane < a.K) {
-        a.ids[(int64_t)t * a.K + lane] = my_id;
-        a.probs[(int64_t)t * a.K + lane] = a.scale * p;
     }
 }
 
+template <int VPL, bool BF16>
+__global__ __launch_bounds__(kTopkThreads) void k_route(TopkArgs a) {
+    __shared__ double s_key[kTopkWaves][VPL * kWave];
+    const int w = uniform((int32_t)(threadIdx.x / kWave)), lane = threadIdx.x & (kWave - 1);
+    const int32_t t = (int32_t)(blockIdx.x * kTopkWaves) + w;
+    if (t >= a.T) return;  // no barrier below: each wave uses its own part of s_key
+    const int64_t slot = (int64_t)t * a.K + lane;
+    if (a.mask != nullptr && a.mask[t] == 0) {
+        if (lane < a.K) {
+            a.ids[slot] = -1;
+            a.probs[slot] = 0.0f;
+        }
+        return;
+    }
+    float z[VPL];
+    load_logits<VPL, BF16>(a, (int64_t)t * a.E, lane, z);
+    float zmax = -INFINITY, total = 1.0f;
+    if (!a.sigmoid) {
+#pragma unroll
+        for (int i = 0; i < VPL; ++i) zmax = fmaxf(zmax, z[i]);
+        zmax = unordered(wave_max(ordered(zmax)));
+        float sum = 0.0f;
+#pragma unroll
+        for (int i = 0; i < VPL; ++i) sum += expf(z[i] - zmax);
+        total = wave_sum(sum);
+    }
+    // keys, in fp32; unavailable experts have -infinity
+    float key[VPL];
+    float largest = 0.0f;
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) {
+        key[i] = z[i];
+        if (a.bias != nullptr) {
+            const int32_t e = lane * VPL + i;
+            const float s = a.sigmoid ? __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-1.44269504f * z[i]))
+                                      : expf(z[i] - zmax) / total;
+            key[i] = s + (e < a.E ? a.bias[e] : 0.0f);
+            largest = fmaxf(largest, fabsf(key[i]));
+        }
+        if (!(z[i] > -INFINITY)) key[i] = -INFINITY;
+    }
+    const bool biased = a.bias != nullptr;
+    float off = 0.0f;
+    if (biased) off = 2.0f * key_error(a, __uint_as_float(wave_max(__float_as_uint(largest))), VPL);
+
+    // Groups whose experts fill whole lanes here; the others in full.
+    const int per = a.E / a.groups;  // experts of a group
+    bool sure = a.groups == 1 || (a.E == VPL * kWave && per % VPL == 0 &&
+                                  (a.groups & (a.groups - 1)) == 0);
+    if (sure && a.groups > 1) {
+        const int lanes = per / VPL;
+        const float gkey = group_key<VPL>(key, lanes, biased && per > 1);
+        int before = 0, maybe = 0;  // groups that come before this one, for sure and at most
+        for (int g = 0; g < a.groups; ++g) {
+            const float other = lane_value(gkey, g * lanes);
+            const bool mine = lane / lanes == g;
+            if (biased) {
+                before += other > gkey + 2.0f * off;
+                maybe += !mine && !(other < gkey - 2.0f * off);
+            } else {
+                before += other > gkey || (other == gkey && g < lane / lanes);
+            }
+        }
+        if (!biased) maybe = before;
+        sure = __builtin_amdgcn_ballot_w64(before < a.top_groups && maybe >= a.top_groups) == 0;
+        if (before >= a.top_groups)
+#pragma unroll
+            for (int i = 0; i < VPL; ++i) key[i] = -INFINITY;
+    }
+    int32_t my_id = -1;
+    float my_z = 0.0f;
+    if (sure) {
+        uint32_t u[VPL];
+#pragma unroll
+        for (int i = 0; i < VPL; ++i) u[i] = key[i] > -INFINITY ? ordered(key[i]) : 0u;
+        for (int k = 0; k < a.K; ++k) {
+            uint32_t m = 0;
+#pragma unroll
+            for (int i = 0; i < VPL; ++i) m = m < u[i] ? u[i] : m;
+            const uint32_t best = wave_max(m);
+            if (best == 0) break;  // no expert left to choose
+            if (biased) {
+                const uint32_t near = ordered(unordered(best) - off);
+                int close = 0;
+#pragma unroll
+                for (int i = 0; i < VPL; ++i) close += __builtin_popcountll(__builtin_amdgcn_ballot_w64(u[i] >= near));
+                if (close > 1) {
+                    sure = false;
+                    break;
+                }
+            }
+            int at = 0;
+            float zk = z[0];
+#pragma unroll
+            for (int i = VPL - 1; i >= 0; --i)
+                if (u[i] == best) {
+                    at = i;
+                    zk = z[i];
+                }
+            const int from = __builtin_ctzll(__builtin_amdgcn_ballot_w64(m == best));
+            at = __builtin_amdgcn_readlane(at, from);
+            zk = lane_value(zk, from);
+#pragma unroll
+            for (int i = 0; i < VPL; ++i)
+                if (i == at && lane == from) u[i] = 0;
+            if (lane == k) {
+                my_id = from * VPL + at;
+                my_z = zk;
+            }
+        }
+    }
+    if (!sure) choose_exactly<VPL>(a, z, zmax, lane, s_key[w], my_id, my_z);
+    float q = 0.0f;
+    if (my_id >= 0) q = a.sigmoid ? 1.0f / (1.0f + expf(-my_z)) : expf(my_z - zmax) / total;
+    float p = q;
+    if (a.normalize) p = q / (wave_sum(q) + 1e-20f);
+    if (lane < a.K) {
+        a.ids[slot] = my_id;
+        a.probs[slot] = a.scale * p;
+    }
+}
+
+template <int VPL, bool BF16>
 __global__ __launch_bounds__(kTopkThreads) void k_route_bwd(TopkArgs a) {
-    const int w = threadIdx.x / kWave, lane = threadIdx.x & (kWave - 1);
-    const int32_t t = uniform((int32_t)(blockIdx.x * kTopkWaves + w));
+    const int w = uniform((int32_t)(threadIdx.x / kWave)), lane = threadIdx.x & (kWave - 1);
+    const int32_t t = (int32_t)(blockIdx.x * kTopkWaves) + w;
     if (t >= a.T) return;
     const int64_t row = (int64_t)t * a.E;
-    int32_t id = lane < a.K ? a.ids[(int64_t)t * a.K + lane] : -1;
-    if (id < 0 || id >= a.E) id = -1;
+    int32_t id = -1;
+    float g = 0.0f, zk = 0.0f, z[VPL];
+    if (lane < a.K) {
+        id = a.ids[(int64_t)t * a.K + lane];
+        g = a.grad_probs[(int64_t)t * a.K + lane];
+    }
+    if (!a.sigmoid) load_logits<VPL, BF16>(a, row, lane, z);
+    if (id < 0 || id >= a.E) {
+        id = -1;
+        g = 0.0f;
+    } else {
+        zk = logit<BF16>(a.logits, row + id);
+    }
     const bool any = __builtin_amdgcn_ballot_w64(id >= 0) != 0;
-    const float g = id >= 0 ? a.grad_probs[(int64_t)t * a.K + lane] : 0.0f;
-    const float zk = id >= 0 ? load_logit(a, row + id) : 0.0f;
     float zmax = 0.0f, total = 1.0f;
-    if (!a.sigmoid && any) {
+    if (!a.sigmoid) {
         zmax = -INFINITY;
-        for (int32_t e = lane; e < a.E; e += kWave) zmax = fmaxf(zmax, load_logit(a, row + e));
 #pragma unroll
-        for (int o = kWave / 2; o > 0; o >>= 1) zmax = fmaxf(zmax, __shfl_xor(zmax, o, kWave));
-        total = 0.0f;
-        for (int32_t e = lane; e < a.E; e += kWave) total += expf(load_logit(a, row + e) - zmax);
-        total = wave_sum(total);
+        for (int i = 0; i < VPL; ++i) zmax = fmaxf(zmax, z[i]);
+        zmax = unordered(wave_max(ordered(zmax)));
+        float sum = 0.0f;
+#pragma unroll
+        for (int i = 0; i < VPL; ++i) {
+            z[i] = expf(z[i] - zmax);
+            sum += z[i];
+        }
+        total = wave_sum(sum);
     }
     float q = 0.0f;
     if (id >= 0) q = a.sigmoid ? 1.0f / (1.0f + expf(-zk)) : expf(zk - zmax) / total;
@@ -167,50 +390,76 @@ __global__ __launch_bounds__(kTopkThreads) void k_route_bwd(TopkArgs a) {
         gq = a.scale * (g - wave_sum(g * q) / Q) / Q;
     }
     if (id < 0) gq = 0.0f;
-    const float dot = wave_sum(gq * q);
     const float own = a.sigmoid ? gq * q * (1.0f / (1.0f + expf(zk))) : gq;
-    for (int32_t e0 = 0; e0 < a.E; e0 += kWave) {
-        const int32_t e = e0 + lane;
-        float sum = 0.0f;  // of the slots that chose e
-        for (int k = 0; k < a.K; ++k) {
-            const float o = __shfl(own, k, kWave);
-            sum += __shfl(id, k, kWave) == e ? o : 0.0f;
+    float gz[VPL];
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) gz[i] = 0.0f;
+    for (int k = 0; k < a.K; ++k) {
+        const int32_t e = __builtin_amdgcn_readlane(id, k);
+        const float o = lane_value(own, k);
+#pragma unroll
+        for (int i = 0; i < VPL; ++i) gz[i] += e == lane * VPL + i ? o : 0.0f;
+    }
+    if (!a.sigmoid) {
+        const float dot = wave_sum(gq * q);
+#pragma unroll
+        for (int i = 0; i < VPL; ++i) gz[i] = any ? z[i] / total * (gz[i] - dot) : 0.0f;
+    }
+    if (VPL % 4 == 0 && a.E == VPL * kWave) {
+#pragma unroll
+        for (int i = 0; i < VPL / 4 * 4; i += 4) {
+            const int64_t at = row + lane * VPL + i;
+            if constexpr (BF16) {
+                const v2u v = {pack_bf16x2(gz[i], gz[i + 1]), pack_bf16x2(gz[i + 2], gz[i + 3])};
+                *reinterpret_cast<v2u*>(static_cast<uint16_t*>(a.grad_logits) + at) = v;
+            } else {
+                const v4u v = {__float_as_uint(gz[i]), __float_as_uint(gz[i + 1]), __float_as_uint(gz[i + 2]),
+                               __float_as_uint(gz[i + 3])};
+                *reinterpret_cast<v4u*>(static_cast<float*>(a.grad_logits) + at) = v;
+            }
         }
-        float gz = sum;
-        if (!a.sigmoid && any && e < a.E) gz = expf(load_logit(a, row + e) - zmax) / total * (sum - dot);
+        return;
+    }
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) {
+        const int32_t e = lane * VPL + i;
         if (e >= a.E) continue;
-        if (a.bf16)
-            static_cast<uint16_t*>(a.grad_logits)[row + e] = (uint16_t)f32_to_bf16(gz);
+        if constexpr (BF16)
+            static_cast<uint16_t*>(a.grad_logits)[row + e] = (uint16_t)f32_to_bf16(gz[i]);
         else
-            static_cast<float*>(a.grad_logits)[row + e] = gz;
+            static_cast<float*>(a.grad_logits)[row + e] = gz[i];
     }
 }
 
 template <int VPL>
-hipError_t route(const TopkArgs& a, hipStream_t stream) {
-    const unsigned blocks = (unsigned)((a.T + kTopkWaves - 1) / kTopkWaves);
-    hipLaunchKernelGGL(k_route<VPL>, dim3(blocks), dim3(kTopkThreads), 0, stream, a);
+hipError_t route(const TopkArgs& a, bool bwd, hipStream_t stream) {
+    const dim3 blocks((unsigned)((a.T + kTopkWaves - 1) / kTopkWaves)), threads(kTopkThreads);
+    if (bwd && a.bf16)
+        hipLaunchKernelGGL((k_route_bwd<VPL, true>), blocks, threads, 0, stream, a);
+    else if (bwd)
+        hipLaunchKernelGGL((k_route_bwd<VPL, false>), blocks, threads, 0, stream, a);
+    else if (a.bf16)
+        hipLaunchKernelGGL((k_route<VPL, true>), blocks, threads, 0, stream, a);
+    else
+        hipLaunchKernelGGL((k_route<VPL, false>), blocks, threads, 0, stream, a);
     return hipGetLastError();
+}
+
+hipError_t by_experts(const TopkArgs& a, bool bwd, hipStream_t stream) {
+    if (a.T == 0) return hipSuccess;
+    const int vpl = (a.E + kWave - 1) / kWave;
+    if (vpl <= 1) return route<1>(a, bwd, stream);
+    if (vpl <= 2) return route<2>(a, bwd, stream);
+    if (vpl <= 4) return route<4>(a, bwd, stream);
+    if (vpl <= 8) return route<8>(a, bwd, stream);
+    if (vpl <= 16) return route<16>(a, bwd, stream);
+    return route<32>(a, bwd, stream);
 }
 
 }  // namespace
 
-hipError_t launch_route(const TopkArgs& a, hipStream_t stream) {
-    if (a.T == 0) return hipSuccess;
-    const int vpl = (a.E + kWave - 1) / kWave;
-    if (vpl <= 1) return route<1>(a, stream);
-    if (vpl <= 2) return route<2>(a, stream);
-    if (vpl <= 4) return route<4>(a, stream);
-    if (vpl <= 8) return route<8>(a, stream);
-    if (vpl <= 16) return route<16>(a, stream);
-    return route<32>(a, stream);
-}
+hipError_t launch_route(const TopkArgs& a, hipStream_t stream) { return by_experts(a, false, stream); }
 
-hipError_t launch_route_bwd(const TopkArgs& a, hipStream_t stream) {
-    if (a.T == 0) return hipSuccess;
-    const unsigned blocks = (unsigned)((a.T + kTopkWaves - 1) / kTopkWaves);
-    hipLaunchKernelGGL(k_route_bwd, dim3(blocks), dim3(kTopkThreads), 0, stream, a);
-    return hipGetLastError();
-}
+hipError_t launch_route_bwd(const TopkArgs& a, hipStream_t stream) { return by_experts(a, true, stream); }
 
 }  // namespace epx
