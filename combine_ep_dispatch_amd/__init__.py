@@ -166,7 +166,8 @@ def _tensor(t: Optional[torch.Tensor], name: str, dtype, numel: int, device=None
 
 def _stream(stream, device) -> int:
     if stream is None:
-        return torch.cuda.current_stream(device).cuda_stream
+        # the raw handle of torch.cuda.current_stream(device), without the 2 us its object costs
+        return torch._C._cuda_getCurrentRawStream(device.index)
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -438,6 +439,21 @@ def _call(name: str, dev, stream, *args) -> None:
     _check(status, name)
 
 
+def _arrays(layout: Layout, cfg: EpConfig, device, *names: str) -> EpLayout:
+    """The layout arrays a call reads, checked (with those that zeroing pad rows reads)."""
+    if cfg.flags & EP_ZERO_PAD_ROWS:
+        names = (*names, "counts", "row_offsets", "seg_base")
+    S, G = cfg.num_segments, cfg.groups_per_segment
+    c = EpLayout()
+    for name in names:
+        t = getattr(layout, name)
+        numel = (cfg.num_tokens * cfg.kp if name == "token_row" else S * G if name == "counts" else
+                 S * (G + 1) if name == "row_offsets" else S + 1)
+        _tensor(t, name, torch.int32, numel, device)
+        setattr(c, name, t.data_ptr())
+    return c
+
+
 def _ptr(t: Optional[torch.Tensor]):
     return None if t is None else t.data_ptr()
 
@@ -497,8 +513,8 @@ def ep_swiglu(cfg: EpConfig, layout: Layout, h: torch.Tensor, probs: Optional[to
     _tensor(h, "h", torch.bfloat16, R * 2 * inter)
     if probs is not None:
         _tensor(probs, "probs", torch.float32, cfg.num_tokens * cfg.top_k, dev)
-    layout.check(cfg, dev)
-    _call("ep_swiglu", dev, stream, ctypes.byref(cfg.to_c()), ctypes.byref(layout.to_c()), inter, h.data_ptr(),
+    lay = _arrays(layout, cfg, dev, "token_row")
+    _call("ep_swiglu", dev, stream, ctypes.byref(cfg.to_c()), ctypes.byref(lay), inter, h.data_ptr(),
           _ptr(probs), act.data_ptr())
 
 
@@ -513,8 +529,8 @@ def ep_swiglu_bwd(cfg: EpConfig, layout: Layout, h: torch.Tensor, probs: Optiona
     for t, name in ((probs, "probs"), (grad_probs, "grad_probs")):
         if t is not None:
             _tensor(t, name, torch.float32, cfg.num_tokens * cfg.top_k, dev)
-    layout.check(cfg, dev)
-    _call("ep_swiglu_bwd", dev, stream, ctypes.byref(cfg.to_c()), ctypes.byref(layout.to_c()), inter, h.data_ptr(),
+    lay = _arrays(layout, cfg, dev, "token_row")
+    _call("ep_swiglu_bwd", dev, stream, ctypes.byref(cfg.to_c()), ctypes.byref(lay), inter, h.data_ptr(),
           _ptr(probs), grad_act.data_ptr(), grad_h.data_ptr(), _ptr(grad_probs))
 
 
@@ -524,8 +540,8 @@ def ep_expert_gemm(cfg: EpConfig, layout: Layout, x: torch.Tensor, w: torch.Tens
     dev, R = x.device, cfg.recv_rows
     n_in, n_out = _columns(x, "x", R), _columns(y, "y", R, device=dev)
     _weights(cfg, w, "w", torch.bfloat16, (n_out, n_in), dev)
-    layout.check(cfg, dev)
-    _call("ep_expert_gemm", dev, stream, ctypes.byref(cfg.to_c()), ctypes.byref(layout.to_c()), n_in, n_out,
+    lay = _arrays(layout, cfg, dev, "counts", "row_offsets", "seg_base")
+    _call("ep_expert_gemm", dev, stream, ctypes.byref(cfg.to_c()), ctypes.byref(lay), n_in, n_out,
           x.data_ptr(), w.data_ptr(), y.data_ptr())
 
 
@@ -535,8 +551,8 @@ def ep_expert_gemm_bwd_x(cfg: EpConfig, layout: Layout, grad_y: torch.Tensor, w:
     dev, R = grad_y.device, cfg.recv_rows
     n_in, n_out = _columns(grad_x, "grad_x", R, device=dev), _columns(grad_y, "grad_y", R)
     _weights(cfg, w, "w", torch.bfloat16, (n_out, n_in), dev)
-    layout.check(cfg, dev)
-    _call("ep_expert_gemm_bwd_x", dev, stream, ctypes.byref(cfg.to_c()), ctypes.byref(layout.to_c()), n_in, n_out,
+    lay = _arrays(layout, cfg, dev, "counts", "row_offsets", "seg_base")
+    _call("ep_expert_gemm_bwd_x", dev, stream, ctypes.byref(cfg.to_c()), ctypes.byref(lay), n_in, n_out,
           grad_y.data_ptr(), w.data_ptr(), grad_x.data_ptr())
 
 
@@ -550,8 +566,8 @@ def ep_expert_gemm_bwd_w(cfg: EpConfig, layout: Layout, grad_y: torch.Tensor, x:
         raise ValueError(f"grad_w must be torch.float32{'' if accumulate else ' or torch.bfloat16'}, got {grad_w.dtype}")
     n_in, n_out = _columns(x, "x", R, device=dev), _columns(grad_y, "grad_y", R)
     _weights(cfg, grad_w, "grad_w", grad_w.dtype, (n_out, n_in), dev)
-    layout.check(cfg, dev)
-    _call("ep_expert_gemm_bwd_w", dev, stream, ctypes.byref(cfg.to_c()), ctypes.byref(layout.to_c()), n_in, n_out,
+    lay = _arrays(layout, cfg, dev, "counts", "row_offsets", "seg_base")
+    _call("ep_expert_gemm_bwd_w", dev, stream, ctypes.byref(cfg.to_c()), ctypes.byref(lay), n_in, n_out,
           grad_y.data_ptr(), x.data_ptr(), grad_w.data_ptr(), kinds[grad_w.dtype])
 
 
@@ -564,8 +580,8 @@ def ep_expert_gemm_nvfp4(cfg: EpConfig, layout: Layout, x: torch.Tensor, codes: 
     _weights(cfg, codes, "codes", torch.uint8, (n_out, n_in // 2), dev)
     _weights(cfg, scales, "scales", torch.uint8, (n_out, n_in // 16), dev)
     _weights(cfg, rowscale, "rowscale", torch.bfloat16, (n_out,), dev)
-    layout.check(cfg, dev)
-    _call("ep_expert_gemm_nvfp4", dev, stream, ctypes.byref(cfg.to_c()), ctypes.byref(layout.to_c()), n_in, n_out,
+    lay = _arrays(layout, cfg, dev, "counts", "row_offsets", "seg_base")
+    _call("ep_expert_gemm_nvfp4", dev, stream, ctypes.byref(cfg.to_c()), ctypes.byref(lay), n_in, n_out,
           x.data_ptr(), codes.data_ptr(), scales.data_ptr(), rowscale.data_ptr(), y.data_ptr())
 
 
