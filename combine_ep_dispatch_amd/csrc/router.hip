@@ -11,10 +11,9 @@
 //
 // Without a bias a key is the logit, and the order is exact.  With one it is
 // score + bias, whose fp32 value is off by a few roundings (key_error below):
-// wherever two keys, or two groups' keys, lie closer than that, the token is
-// chosen again from 64-bit keys.  That is about one token in a hundred with
-// normal logits; 64-bit keys for all of them took 15.9 instead of 5.2 us at
-// 4096 tokens of 256 experts.
+// where other keys lie closer to the largest than that, these few are compared
+// in 64 bits, where groups' keys do, the groups are ranked in 64 bits, and where
+// many experts' do, the token is chosen again from 64-bit keys.
 #include "epx_device.h"
 
 namespace epx {
@@ -22,6 +21,8 @@ namespace {
 
 constexpr int kTopkThreads = 256;
 constexpr int kTopkWaves = kTopkThreads / kWave;
+
+constexpr int kMaxClose = 8;  // keys too close to tell that are settled one by one
 
 typedef uint32_t v4u __attribute__((ext_vector_type(4)));
 typedef uint32_t v2u __attribute__((ext_vector_type(2)));
@@ -140,29 +141,56 @@ __device__ __forceinline__ float group_key(const float (&key)[VPL], int per, boo
     return two ? b0 + b1 : b0;
 }
 
+// The 64-bit key of an expert with logit z; total: sum of exp(z - zmax) in 64 bits.
+__device__ __forceinline__ double exact_key(const TopkArgs& a, float z, float zmax, double total, int32_t e) {
+    const double s = a.sigmoid ? 1.0 / (1.0 + exp(-(double)z)) : exp((double)z - (double)zmax) / total;
+    return s + (double)a.bias[e];
+}
+
+template <int VPL>
+__device__ __forceinline__ double exact_total(const TopkArgs& a, const float (&z)[VPL], float zmax, int lane) {
+    double total = 0.0;
+#pragma unroll
+    for (int i = 0; i < VPL; ++i)
+        if (lane * VPL + i < a.E) total += exp((double)z[i] - (double)zmax);
+#pragma unroll
+    for (int o = kWave / 2; o > 0; o >>= 1) total += __shfl_xor(total, o, kWave);
+    return total;
+}
+
+// How many groups come before the lane's, from 64-bit keys; lanes: of a group.
+template <int VPL>
+__device__ __forceinline__ int exact_group_rank(const TopkArgs& a, const float (&z)[VPL], float zmax, int lane, int lanes) {
+    const double total = a.sigmoid ? 1.0 : exact_total<VPL>(a, z, zmax, lane);
+    double b0 = -INFINITY, b1 = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < VPL; ++i)
+        if (z[i] > -INFINITY) merge(b0, b1, exact_key(a, z[i], zmax, total, lane * VPL + i), (double)-INFINITY);
+    for (int o = 1; o < lanes; o *= 2) {
+        const double o0 = __shfl_xor(b0, o, kWave), o1 = __shfl_xor(b1, o, kWave);
+        merge(b0, b1, o0, o1);
+    }
+    const double mine = lanes * VPL > 1 ? b0 + b1 : b0;
+    int before = 0;
+    for (int g = 0; g < a.groups; ++g) {
+        const double other = __shfl(mine, g * lanes, kWave);
+        before += other > mine || (other == mine && g < lane / lanes);
+    }
+    return before;
+}
+
 // The choice in full: keys of 64 bits where there is a bias, groups of any
 // size.  Lane k gets the k-th expert (-1: none) and its logit.
 template <int VPL>
-__device__ void choose_exactly(const TopkArgs& a, const float (&z)[VPL], float zmax, int lane, double* s_key,
+__device__ __forceinline__ void choose_exactly(const TopkArgs& a, const float (&z)[VPL], float zmax, int lane, double* s_key,
                                int32_t& my_id, float& my_z) {
     double key[VPL];
-    double total = 1.0;
-    if (a.bias != nullptr && !a.sigmoid) {
-        total = 0.0;
-#pragma unroll
-        for (int i = 0; i < VPL; ++i)
-            if (lane * VPL + i < a.E) total += exp((double)z[i] - (double)zmax);
-#pragma unroll
-        for (int o = kWave / 2; o > 0; o >>= 1) total += __shfl_xor(total, o, kWave);
-    }
+    const double total = a.bias != nullptr && !a.sigmoid ? exact_total<VPL>(a, z, zmax, lane) : 1.0;
 #pragma unroll
     for (int i = 0; i < VPL; ++i) {
         const int32_t e = lane * VPL + i;
         key[i] = z[i];
-        if (a.bias != nullptr && e < a.E) {
-            const double s = a.sigmoid ? 1.0 / (1.0 + exp(-(double)z[i])) : exp((double)z[i] - (double)zmax) / total;
-            key[i] = s + (double)a.bias[e];
-        }
+        if (a.bias != nullptr && e < a.E) key[i] = exact_key(a, z[i], zmax, total, e);
         if (!(z[i] > -INFINITY) || e >= a.E) key[i] = -INFINITY;
     }
     if (a.groups > 1) {
@@ -290,7 +318,8 @@ __global__ __launch_bounds__(kTopkThreads) void k_route(TopkArgs a) {
             }
         }
         if (!biased) maybe = before;
-        sure = __builtin_amdgcn_ballot_w64(before < a.top_groups && maybe >= a.top_groups) == 0;
+        if (__builtin_amdgcn_ballot_w64(before < a.top_groups && maybe >= a.top_groups) != 0)
+            before = exact_group_rank<VPL>(a, z, zmax, lane, lanes);
         if (before >= a.top_groups)
 #pragma unroll
             for (int i = 0; i < VPL; ++i) key[i] = -INFINITY;
@@ -301,36 +330,65 @@ __global__ __launch_bounds__(kTopkThreads) void k_route(TopkArgs a) {
         uint32_t u[VPL];
 #pragma unroll
         for (int i = 0; i < VPL; ++i) u[i] = key[i] > -INFINITY ? ordered(key[i]) : 0u;
+        double exact = 0.0;  // softmax's sum in 64 bits, once it is needed
         for (int k = 0; k < a.K; ++k) {
             uint32_t m = 0;
 #pragma unroll
             for (int i = 0; i < VPL; ++i) m = m < u[i] ? u[i] : m;
-            const uint32_t best = wave_max(m);
+            uint32_t best = wave_max(m);
             if (best == 0) break;  // no expert left to choose
+            int32_t chosen = -1;
             if (biased) {
                 const uint32_t near = ordered(unordered(best) - off);
                 int close = 0;
 #pragma unroll
                 for (int i = 0; i < VPL; ++i) close += __builtin_popcountll(__builtin_amdgcn_ballot_w64(u[i] >= near));
-                if (close > 1) {
+                if (close > kMaxClose) {
                     sure = false;
                     break;
                 }
+                if (close > 1) {  // the largest of these in 64 bits
+                    if (!a.sigmoid && exact == 0.0) exact = exact_total<VPL>(a, z, zmax, lane);
+                    double top = -INFINITY;
+#pragma unroll
+                    for (int i = 0; i < VPL; ++i) {
+                        uint64_t left = __builtin_amdgcn_ballot_w64(u[i] >= near);
+                        if (left == 0) continue;
+                        const double mine = u[i] >= near ? exact_key(a, z[i], zmax, exact, lane * VPL + i) : 0.0;
+                        for (; left != 0; left &= left - 1) {
+                            const int from = __builtin_ctzll(left);
+                            const uint64_t bits = __builtin_bit_cast(uint64_t, mine);
+                            const uint64_t lo = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)bits, from);
+                            const uint64_t hi = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)(bits >> 32), from);
+                            const double other = __builtin_bit_cast(double, hi << 32 | lo);
+                            const int32_t e = from * VPL + i;
+                            if (other > top || (other == top && e < chosen)) {
+                                top = other;
+                                chosen = e;
+                            }
+                        }
+                    }
+                }
             }
             int at = 0;
+            int from;
+            if (chosen >= 0) {
+                from = chosen / VPL;
+                at = chosen - from * VPL;
+            } else {
+#pragma unroll
+                for (int i = VPL - 1; i >= 0; --i)
+                    if (u[i] == best) at = i;
+                from = __builtin_ctzll(__builtin_amdgcn_ballot_w64(m == best));
+                at = __builtin_amdgcn_readlane(at, from);
+            }
             float zk = z[0];
 #pragma unroll
-            for (int i = VPL - 1; i >= 0; --i)
-                if (u[i] == best) {
-                    at = i;
-                    zk = z[i];
-                }
-            const int from = __builtin_ctzll(__builtin_amdgcn_ballot_w64(m == best));
-            at = __builtin_amdgcn_readlane(at, from);
-            zk = lane_value(zk, from);
-#pragma unroll
-            for (int i = 0; i < VPL; ++i)
+            for (int i = 0; i < VPL; ++i) {
+                if (i == at) zk = z[i];
                 if (i == at && lane == from) u[i] = 0;
+            }
+            zk = lane_value(zk, from);
             if (lane == k) {
                 my_id = from * VPL + at;
                 my_z = zk;
@@ -345,6 +403,35 @@ __global__ __launch_bounds__(kTopkThreads) void k_route(TopkArgs a) {
     if (lane < a.K) {
         a.ids[slot] = my_id;
         a.probs[slot] = a.scale * p;
+    }
+}
+
+// The lane's VPL gradients of a row that `lanes` lanes hold.
+template <int VPL, bool BF16>
+__device__ __forceinline__ void store_gradient(const TopkArgs& a, int64_t row, int lane, int lanes, const float (&gz)[VPL]) {
+    if (VPL % 4 == 0 && a.E == VPL * lanes) {
+#pragma unroll
+        for (int i = 0; i < VPL / 4 * 4; i += 4) {
+            const int64_t at = row + lane * VPL + i;
+            if constexpr (BF16) {
+                const v2u v = {pack_bf16x2(gz[i], gz[i + 1]), pack_bf16x2(gz[i + 2], gz[i + 3])};
+                *reinterpret_cast<v2u*>(static_cast<uint16_t*>(a.grad_logits) + at) = v;
+            } else {
+                const v4u v = {__float_as_uint(gz[i]), __float_as_uint(gz[i + 1]), __float_as_uint(gz[i + 2]),
+                               __float_as_uint(gz[i + 3])};
+                *reinterpret_cast<v4u*>(static_cast<float*>(a.grad_logits) + at) = v;
+            }
+        }
+        return;
+    }
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) {
+        const int32_t e = lane * VPL + i;
+        if (e >= a.E) continue;
+        if constexpr (BF16)
+            static_cast<uint16_t*>(a.grad_logits)[row + e] = (uint16_t)f32_to_bf16(gz[i]);
+        else
+            static_cast<float*>(a.grad_logits)[row + e] = gz[i];
     }
 }
 
@@ -405,30 +492,179 @@ __global__ __launch_bounds__(kTopkThreads) void k_route_bwd(TopkArgs a) {
 #pragma unroll
         for (int i = 0; i < VPL; ++i) gz[i] = any ? z[i] / total * (gz[i] - dot) : 0.0f;
     }
-    if (VPL % 4 == 0 && a.E == VPL * kWave) {
+    store_gradient<VPL, BF16>(a, row, lane, kWave, gz);
+}
+
+// Narrow forms, four tokens a wave: a token has the 16 lanes of a DPP row, lane
+// l of them experts [l VPL, (l + 1) VPL), so that each cross-lane step serves
+// four tokens.  For at most 16 slots, and forward only where the logits are the
+// keys (no bias, no groups).  65 536 tokens of 64 experts: forward 25.6 us with
+// a wave per token, backward 19.0.
+constexpr int kRowLanes = 16;
+constexpr int kNarrowTokens = kTopkWaves * kWave / kRowLanes;  // of a workgroup
+
+template <typename F>
+__device__ __forceinline__ uint32_t row_reduce(uint32_t v, F f) {
+    v = f(v, (uint32_t)__builtin_amdgcn_update_dpp((int)v, (int)v, 0xB1, 0xf, 0xf, false));   // lane ^ 1
+    v = f(v, (uint32_t)__builtin_amdgcn_update_dpp((int)v, (int)v, 0x4E, 0xf, 0xf, false));   // lane ^ 2
+    v = f(v, (uint32_t)__builtin_amdgcn_update_dpp((int)v, (int)v, 0x141, 0xf, 0xf, false));  // 7 - lane of 8
+    v = f(v, (uint32_t)__builtin_amdgcn_update_dpp((int)v, (int)v, 0x140, 0xf, 0xf, false));  // 15 - lane of 16
+    return v;
+}
+__device__ __forceinline__ uint32_t row_max(uint32_t v) {
+    return row_reduce(v, [](uint32_t a, uint32_t b) { return a > b ? a : b; });
+}
+__device__ __forceinline__ float row_sum(float v) {
+    return __uint_as_float(row_reduce(__float_as_uint(v), [](uint32_t a, uint32_t b) {
+        return __float_as_uint(__uint_as_float(a) + __uint_as_float(b));
+    }));
+}
+
+// As load_logits and its store, for 16 lanes a row.
+template <int VPL, bool BF16>
+__device__ __forceinline__ void load_row(const TopkArgs& a, int64_t row, int l, bool on, float (&z)[VPL]) {
+    if (VPL % 4 == 0 && a.E == VPL * kRowLanes) {
 #pragma unroll
         for (int i = 0; i < VPL / 4 * 4; i += 4) {
-            const int64_t at = row + lane * VPL + i;
+            const int64_t at = on ? row + l * VPL + i : 0;
             if constexpr (BF16) {
-                const v2u v = {pack_bf16x2(gz[i], gz[i + 1]), pack_bf16x2(gz[i + 2], gz[i + 3])};
-                *reinterpret_cast<v2u*>(static_cast<uint16_t*>(a.grad_logits) + at) = v;
+                const v2u v = *reinterpret_cast<const v2u*>(static_cast<const uint16_t*>(a.logits) + at);
+                z[i] = bf16_lo(v.x), z[i + 1] = bf16_hi(v.x), z[i + 2] = bf16_lo(v.y), z[i + 3] = bf16_hi(v.y);
             } else {
-                const v4u v = {__float_as_uint(gz[i]), __float_as_uint(gz[i + 1]), __float_as_uint(gz[i + 2]),
-                               __float_as_uint(gz[i + 3])};
-                *reinterpret_cast<v4u*>(static_cast<float*>(a.grad_logits) + at) = v;
+                const v4u v = *reinterpret_cast<const v4u*>(static_cast<const float*>(a.logits) + at);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) z[i + j] = __uint_as_float(v[j]);
             }
         }
         return;
     }
 #pragma unroll
     for (int i = 0; i < VPL; ++i) {
-        const int32_t e = lane * VPL + i;
-        if (e >= a.E) continue;
-        if constexpr (BF16)
-            static_cast<uint16_t*>(a.grad_logits)[row + e] = (uint16_t)f32_to_bf16(gz[i]);
-        else
-            static_cast<float*>(a.grad_logits)[row + e] = gz[i];
+        const int32_t e = l * VPL + i;
+        z[i] = on && e < a.E ? logit<BF16>(a.logits, row + e) : -INFINITY;
     }
+}
+
+template <int VPL, bool BF16>
+__global__ __launch_bounds__(kTopkThreads) void k_route_narrow(TopkArgs a) {
+    __shared__ int32_t s_id[kNarrowTokens][kRowLanes];
+    __shared__ float s_z[kNarrowTokens][kRowLanes];
+    const int lane = threadIdx.x & (kWave - 1), l = lane % kRowLanes, mine = threadIdx.x / kRowLanes;
+    const int32_t t = (int32_t)(blockIdx.x * kNarrowTokens) + mine;
+    const bool in = t < a.T, on = in && (a.mask == nullptr || a.mask[t] != 0);
+    float z[VPL];
+    load_row<VPL, BF16>(a, (int64_t)t * a.E, l, on, z);
+    float zmax = -INFINITY, total = 1.0f;
+    if (!a.sigmoid) {
+#pragma unroll
+        for (int i = 0; i < VPL; ++i) zmax = fmaxf(zmax, z[i]);
+        zmax = unordered(row_max(ordered(zmax)));
+        float sum = 0.0f;
+#pragma unroll
+        for (int i = 0; i < VPL; ++i) sum += expf(z[i] - zmax);
+        total = row_sum(sum);
+    }
+    uint32_t u[VPL];
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) u[i] = on && z[i] > -INFINITY ? ordered(z[i]) : 0u;
+    s_id[mine][l] = -1;  // each row writes and reads its own line of these, in program order
+    for (int k = 0; k < a.K; ++k) {
+        uint32_t m = 0;
+#pragma unroll
+        for (int i = 0; i < VPL; ++i) m = m < u[i] ? u[i] : m;
+        const uint32_t best = row_max(m);
+        if (__builtin_amdgcn_ballot_w64(best != 0) == 0) break;  // no token has an expert left to choose
+        const uint32_t at_best = (uint32_t)(__builtin_amdgcn_ballot_w64(m == best && best != 0) >> (lane & 48)) & 0xFFFFu;
+        if (best != 0 && l == __builtin_ctz(at_best | 0x10000u)) {  // the lowest lane that holds it, and its lowest
+            int at = 0;
+#pragma unroll
+            for (int i = VPL - 1; i >= 0; --i)
+                if (u[i] == best) at = i;
+#pragma unroll
+            for (int i = 0; i < VPL; ++i)
+                if (i == at) u[i] = 0;
+            s_id[mine][k] = l * VPL + at;
+            s_z[mine][k] = unordered(best);  // the key is the logit
+        }
+    }
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    const int32_t id = s_id[mine][l];
+    float q = 0.0f;
+    if (id >= 0) {
+        const float zk = s_z[mine][l];
+        q = a.sigmoid ? 1.0f / (1.0f + expf(-zk)) : expf(zk - zmax) / total;
+    }
+    float p = q;
+    if (a.normalize) p = q / (row_sum(q) + 1e-20f);
+    if (in && l < a.K) {
+        a.ids[(int64_t)t * a.K + l] = id;
+        a.probs[(int64_t)t * a.K + l] = a.scale * p;
+    }
+}
+
+template <int VPL, bool BF16>
+__global__ __launch_bounds__(kTopkThreads) void k_route_bwd_narrow(TopkArgs a) {
+    __shared__ int32_t s_id[kNarrowTokens][kRowLanes];
+    __shared__ float s_own[kNarrowTokens][kRowLanes];
+    const int l = threadIdx.x % kRowLanes, mine = threadIdx.x / kRowLanes;
+    const int32_t t = (int32_t)(blockIdx.x * kNarrowTokens) + mine;
+    const bool in = t < a.T;
+    const int64_t row = (int64_t)t * a.E;
+    int32_t id = -1;
+    float g = 0.0f, zk = 0.0f, z[VPL];
+    if (in && l < a.K) {
+        id = a.ids[(int64_t)t * a.K + l];
+        g = a.grad_probs[(int64_t)t * a.K + l];
+    }
+    if (!a.sigmoid) load_row<VPL, BF16>(a, row, l, in, z);
+    if (id < 0 || id >= a.E) {
+        id = -1;
+        g = 0.0f;
+    } else {
+        zk = logit<BF16>(a.logits, row + id);
+    }
+    const bool any = row_max(id >= 0) != 0;
+    float zmax = 0.0f, total = 1.0f;
+    if (!a.sigmoid) {
+        zmax = -INFINITY;
+#pragma unroll
+        for (int i = 0; i < VPL; ++i) zmax = fmaxf(zmax, z[i]);
+        zmax = unordered(row_max(ordered(zmax)));
+        float sum = 0.0f;
+#pragma unroll
+        for (int i = 0; i < VPL; ++i) {
+            z[i] = expf(z[i] - zmax);
+            sum += z[i];
+        }
+        total = row_sum(sum);
+    }
+    float q = 0.0f;
+    if (id >= 0) q = a.sigmoid ? 1.0f / (1.0f + expf(-zk)) : expf(zk - zmax) / total;
+    float gq = a.scale * g;
+    if (a.normalize) {
+        const float Q = row_sum(q) + 1e-20f;
+        gq = a.scale * (g - row_sum(g * q) / Q) / Q;
+    }
+    if (id < 0) gq = 0.0f;
+    s_id[mine][l] = id;
+    s_own[mine][l] = a.sigmoid ? gq * q * (1.0f / (1.0f + expf(zk))) : gq;
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    float gz[VPL];
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) gz[i] = 0.0f;
+    for (int k = 0; k < a.K; ++k) {
+        const int32_t e = s_id[mine][k];
+        const float o = s_own[mine][k];
+#pragma unroll
+        for (int i = 0; i < VPL; ++i) gz[i] += e == l * VPL + i ? o : 0.0f;
+    }
+    if (!a.sigmoid) {
+        const float dot = row_sum(gq * q);
+#pragma unroll
+        for (int i = 0; i < VPL; ++i) gz[i] = any ? z[i] / total * (gz[i] - dot) : 0.0f;
+    }
+    if (!in) return;
+    store_gradient<VPL, BF16>(a, row, l, kRowLanes, gz);
 }
 
 template <int VPL>
@@ -445,8 +681,29 @@ hipError_t route(const TopkArgs& a, bool bwd, hipStream_t stream) {
     return hipGetLastError();
 }
 
+template <int VPL>
+hipError_t narrow(const TopkArgs& a, bool bwd, hipStream_t stream) {
+    const dim3 blocks((unsigned)((a.T + kNarrowTokens - 1) / kNarrowTokens)), threads(kTopkThreads);
+    if (bwd && a.bf16)
+        hipLaunchKernelGGL((k_route_bwd_narrow<VPL, true>), blocks, threads, 0, stream, a);
+    else if (bwd)
+        hipLaunchKernelGGL((k_route_bwd_narrow<VPL, false>), blocks, threads, 0, stream, a);
+    else if (a.bf16)
+        hipLaunchKernelGGL((k_route_narrow<VPL, true>), blocks, threads, 0, stream, a);
+    else
+        hipLaunchKernelGGL((k_route_narrow<VPL, false>), blocks, threads, 0, stream, a);
+    return hipGetLastError();
+}
+
 hipError_t by_experts(const TopkArgs& a, bool bwd, hipStream_t stream) {
     if (a.T == 0) return hipSuccess;
+    if (a.K <= kRowLanes && a.E <= 16 * kRowLanes && (bwd || (a.bias == nullptr && a.groups == 1))) {
+        if (a.E <= kRowLanes) return narrow<1>(a, bwd, stream);
+        if (a.E <= 2 * kRowLanes) return narrow<2>(a, bwd, stream);
+        if (a.E <= 4 * kRowLanes) return narrow<4>(a, bwd, stream);
+        if (a.E <= 8 * kRowLanes) return narrow<8>(a, bwd, stream);
+        return narrow<16>(a, bwd, stream);
+    }
     const int vpl = (a.E + kWave - 1) / kWave;
     if (vpl <= 1) return route<1>(a, bwd, stream);
     if (vpl <= 2) return route<2>(a, bwd, stream);
