@@ -148,4 +148,19 @@ __device__ __forceinline__ int32_t xcd_tile(int32_t row_tiles, int32_t ftiles, i
     return uniform(r0 + in % height);
 }
 
+// As xcd_tile for the weights' gradients, whose tiles cost as much as their
+// experts have rows: the XCDs take blocks of 2 row tiles by all feature tiles
+// in turn, so that no XCD gets all the busy experts (with an eighth each,
+// experts of 400 to 2200 rows left seven XCDs waiting for the first).
+__device__ __forceinline__ int32_t xcd_tile_in_turn(int32_t row_tiles, int32_t ftiles, int32_t& f) {
+    const int32_t b = (int32_t)(blockIdx.x / 8), unit = 2 * ftiles;
+    const int32_t r0 = (b / unit * 8 + (int32_t)(blockIdx.x % 8)) * 2, height = min(2, row_tiles - r0);
+    f = 0;
+    if (height <= 0) return kNoTile;
+    const int32_t in = b % unit;
+    if (in >= height * ftiles) return kNoTile;
+    f = uniform(in / height);
+    return uniform(r0 + in % height);
+}
+
 }  // namespace epx

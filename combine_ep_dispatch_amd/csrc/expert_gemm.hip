@@ -137,7 +137,7 @@ __global__ __launch_bounds__(kWideThreads) void k_expert_wide(ExpertArgs a, int3
     NOp no;
     if constexpr (P == kWeightGrad) {
         int32_t f;
-        const int32_t n = pick((a.E + a.shared) * ntiles, f);
+        const int32_t n = xcd_tile_in_turn((a.E + a.shared) * ntiles, ftiles, f);
         if (n == kNoTile) return;
         expert = n / ntiles;
         const int32_t n0 = (n - expert * ntiles) * NT;
@@ -235,9 +235,10 @@ template <Product P, int NT>
 hipError_t wide(const ExpertArgs& a, hipStream_t stream) {
     const int32_t F = P == kForward ? a.on : a.in;
     const int32_t ftiles = (F + kFeatures - 1) / kFeatures, ntiles = (a.on + NT - 1) / NT;
-    const int64_t tiles = (P == kWeightGrad ? (int64_t)ntiles * (a.E + a.shared) : max_row_tiles(a, NT)) * ftiles;
-    if (tiles == 0) return hipSuccess;
-    const int64_t blocks = (tiles + 7) / 8 * 8;
+    int64_t rtiles = P == kWeightGrad ? (int64_t)ntiles * (a.E + a.shared) : max_row_tiles(a, NT);
+    if (P == kWeightGrad) rtiles = (rtiles + 15) / 16 * 16;  // whole turns of the XCDs
+    const int64_t blocks = (rtiles * ftiles + 7) / 8 * 8;
+    if (blocks == 0) return hipSuccess;
     if (blocks * kWideThreads > 0xFFFFFFFFll) return hipErrorInvalidValue;
     hipLaunchKernelGGL((k_expert_wide<P, NT>), dim3((unsigned)blocks), dim3(kWideThreads), 0, stream, a, ftiles, ntiles);
     return hipGetLastError();
