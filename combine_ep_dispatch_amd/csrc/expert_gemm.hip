@@ -9,8 +9,8 @@
 // contiguous in an operand (rows) or its rows (columns).
 //
 // Tiles of 256 features by 256 or 128 rows, 8 waves of 128 x 64 or 64 x 64
-// results in registers; steps of 64 values of L, two or three of them in LDS,
-// copied there by the loads themselves, one barrier a step.
+// results in registers; steps of 64 values of L, two and a half or three of
+// them in LDS, copied there by the loads themselves, one barrier a step.
 #include <type_traits>
 
 #include "expert_device.h"
@@ -122,10 +122,11 @@ __global__ __launch_bounds__(kWideThreads) void k_expert_wide(ExpertArgs a, int3
     using NOp = typename std::conditional<P == kWeightGrad, ColsOperand<NT>, RowsOperand<NT>>::type;
     constexpr int kWavesN = NT / 64, kWavesF = 8 / kWavesN;  // a wave's tile: 64 rows
     constexpr int kF = kFeatures / kWavesF / 16, kN = 4;     // its fragments
-    constexpr int kBuffers = NT == 256 ? 2 : 3;  // what 160 KiB hold
-    constexpr int kBuffer = (kFeatures + NT) * kStepL;
-    __shared__ __align__(1024) uint16_t lds[kBuffers * kBuffer];
-    __shared__ int32_t scan[16];
+    constexpr bool kUnits = NT == 256;
+    constexpr int kUnit = kFeatures * kStepL, kBuffer = (kFeatures + NT) * kStepL;
+    static_assert(kF >= kN, "the second half's N fragments are read beside F's");
+    __shared__ __align__(1024) uint16_t lds[kUnits ? 5 * kUnit : 3 * kBuffer];
+    int32_t* const scan = reinterpret_cast<int32_t*>(lds);
     const int lane = threadIdx.x & (kWave - 1), w = uniform((int32_t)(threadIdx.x / kWave));
     const int wf = w / kWavesN * (kFeatures / kWavesF), wn = w % kWavesN * 64;
     const int32_t F = P == kForward ? a.on : a.in;
@@ -153,6 +154,7 @@ __global__ __launch_bounds__(kWideThreads) void k_expert_wide(ExpertArgs a, int3
         int32_t f;
         const RowTile t = find_row_tile<kWideThreads, NT>(a, scan, pick, f);
         if (t.expert < 0) return;
+        __syncthreads();  // the words that named the tile become step 0
         expert = t.expert;
         rows = t.rows;
         first = t.first;
@@ -170,41 +172,86 @@ __global__ __launch_bounds__(kWideThreads) void k_expert_wide(ExpertArgs a, int3
     }
 
     f32x4 acc[kF][kN] = {};
-    constexpr int kLoads = FOp::kLoads + NOp::kLoads;
-    auto load = [&](int32_t s) {
-        uint16_t* to = lds + s % kBuffers * kBuffer;
-#pragma unroll
-        for (int j = 0; j < FOp::kLoads; ++j) fo.load(to, s * kStepL, j);
-#pragma unroll
-        for (int j = 0; j < NOp::kLoads; ++j) no.load(to + kFeatures * kStepL, s * kStepL, j);
-    };
+    // What LDS holds: for tiles of 128 rows three steps, of both operands; for
+    // tiles of 256 five units of one operand's step, F's and N's in turn, which
+    // is half a step more in flight than two whole steps.
+    constexpr int kLoads = FOp::kLoads + NOp::kLoads;  // of a wave and step
+    constexpr int kSlots = kUnits ? 5 : 3;
+    auto next = [](int32_t v) { return v == kSlots - 1 ? 0 : v + 1; };
     const int32_t steps = (len + kStepL - 1) / kStepL;
     const bool busy = wn < rows;  // a wave past the tile's last row only loads
-    for (int s = 0; s < kBuffers - 1; ++s) load(s);
+    int32_t in_slot = 0, out_slot = kUnits ? 3 : 2;  // to use, and to fill, next
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+        uint16_t* const to = lds + s * (kUnits ? 2 * kUnit : kBuffer);
+#pragma unroll
+        for (int j = 0; j < FOp::kLoads; ++j) fo.load(to, s * kStepL, j);
+        if (kUnits && s == 1) break;
+#pragma unroll
+        for (int j = 0; j < NOp::kLoads; ++j) no.load(to + kUnit, s * kStepL, j);
+    }
     for (int32_t s = 0; s < steps; ++s) {
-        // This step's loads have landed when only the later steps' are
+        // This step's loads have landed when only the later ones are
         // outstanding: loads return in order, and past the end they still
         // count, and write zeros.  Behind the barrier every wave's have, and
-        // every wave is done with the last step's buffer, which is filled next.
-        asm volatile("s_waitcnt vmcnt(%0)" ::"n"((kBuffers - 2) * kLoads) : "memory");
+        // every wave is done with the last step's LDS, which is filled next.
+        asm volatile("s_waitcnt vmcnt(%0)" ::"n"(kUnits ? FOp::kLoads : kLoads) : "memory");
         lds_barrier();
-        load(s + kBuffers - 1);
-        if (!busy) continue;
-        const uint16_t* lf = lds + s % kBuffers * kBuffer;
-        const uint16_t* ln = lf + kFeatures * kStepL;
-#pragma unroll
-        for (int kk = 0; kk < 2; ++kk) {
-            bf16x8 fb[kN], fa[kF];
-#pragma unroll
-            for (int n = 0; n < kN; ++n) fb[n] = NOp::fragment(ln, wn + n * 16, kk);
-#pragma unroll
-            for (int f = 0; f < kF; ++f) fa[f] = FOp::fragment(lf, wf + f * 16, kk);
-#pragma unroll
-            for (int f = 0; f < kF; ++f)
-#pragma unroll
-                for (int n = 0; n < kN; ++n)
-                    acc[f][n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fa[f], fb[n], acc[f][n], 0, 0, 0);
+        uint16_t *to_f, *to_n;
+        const uint16_t *lf, *ln;
+        if constexpr (kUnits) {  // N of the next step, then F of the one after it
+            to_n = lds + out_slot * kUnit;
+            out_slot = next(out_slot);
+            to_f = lds + out_slot * kUnit;
+            lf = lds + in_slot * kUnit;
+            in_slot = next(in_slot);
+            ln = lds + in_slot * kUnit;
+        } else {
+            to_f = lds + out_slot * kBuffer;
+            to_n = to_f + kUnit;
+            lf = lds + in_slot * kBuffer;
+            ln = lf + kUnit;
         }
+        out_slot = next(out_slot);
+        in_slot = next(in_slot);
+        auto load = [&](int j) {
+            if (j < NOp::kLoads)
+                no.load(to_n, (s + (kUnits ? 1 : 2)) * kStepL, j);
+            else
+                fo.load(to_f, (s + 2) * kStepL, j - NOp::kLoads);
+        };
+        if (!busy) {
+#pragma unroll
+            for (int j = 0; j < kLoads; ++j) load(j);
+            continue;
+        }
+        bf16x8 fa[2][kF], fb[2][kN];
+#pragma unroll
+        for (int n = 0; n < kN; ++n) fb[0][n] = NOp::fragment(ln, wn + n * 16, 0);
+#pragma unroll
+        for (int f = 0; f < kF; ++f) fa[0][f] = FOp::fragment(lf, wf + f * 16, 0);
+        // The loads and the second half's LDS reads go between the matrix
+        // instructions of the first half.  All loads first keep every wave from
+        // its products until the 64 of the workgroup are issued (1930 instead of
+        // 1830 us); without the scheduling barriers the compiler collects them
+        // at the end (2210 us).
+#pragma unroll
+        for (int f = 0; f < kF; ++f) {
+            __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+            for (int j = f * kLoads / kF; j < (f + 1) * kLoads / kF; ++j) load(j);
+            fa[1][f] = FOp::fragment(lf, wf + f * 16, 1);
+            if (f < kN) fb[1][f] = NOp::fragment(ln, wn + f * 16, 1);
+#pragma unroll
+            for (int n = 0; n < kN; ++n)
+                acc[f][n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fa[0][f], fb[0][n], acc[f][n], 0, 0, 0);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int f = 0; f < kF; ++f)
+#pragma unroll
+            for (int n = 0; n < kN; ++n)
+                acc[f][n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fa[1][f], fb[1][n], acc[f][n], 0, 0, 0);
     }
     // No load may land in LDS that belongs to another workgroup by then.
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
