@@ -291,11 +291,14 @@ hipError_t wide(const ExpertArgs& a, hipStream_t stream) {
     return hipGetLastError();
 }
 
-// Row tiles of 256 where the groups hold that many rows on average.
+// Row tiles by the rows a group has on average.  Forward over 32 experts of
+// 4096 x 7168, us at 16, 64, 128, 256 and 512 rows a group: 128-row tiles 317
+// 335 454 716 1128, 256-row tiles 330 363 405 689 1008 (128 rows on average fill
+// a second tile of 128 in half of the groups).
 template <Product P>
 hipError_t by_rows(const ExpertArgs& a, hipStream_t stream) {
     const int64_t groups = a.slots < a.E + a.shared ? a.slots : a.E + a.shared;
-    return a.slots >= 256 * groups ? wide<P, 256>(a, stream) : wide<P, 128>(a, stream);
+    return a.slots >= 96 * groups ? wide<P, 256>(a, stream) : wide<P, 128>(a, stream);
 }
 
 }  // namespace

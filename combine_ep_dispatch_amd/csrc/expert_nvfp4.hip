@@ -65,6 +65,10 @@ __global__ __launch_bounds__(WAVES * kWave) void k_nvfp4(ExpertArgs a, int32_t f
     constexpr int kLoads = 2 + kScaleLoads + kRowLoads;  // of a wave and step
     constexpr int kCodes = kFeatures * kCodeRow, kScales = WAVES * kScaleBytes;
     constexpr int kBuffer = kCodes + kScales + NT * kRowBytes;
+    // Many rows: the next step's loads go between this step's products, and the
+    // next group's operands are made while the matrix pipe works on this one's
+    // (213 -> 197 us at 122 rows a group; few rows gain nothing).
+    constexpr bool kSpread = NT >= 64;
     static_assert(kRowLoads >= 1 && (BUFS - 2) * kLoads < 64, "");
     __shared__ __align__(1024) uint8_t lds[BUFS * kBuffer];
     __shared__ int32_t scan[16];
@@ -108,26 +112,23 @@ __global__ __launch_bounds__(WAVES * kWave) void k_nvfp4(ExpertArgs a, int32_t f
     }
     // Step s of this wave's features and of its share of the rows; lanes past
     // the end of the summed dimension read nothing.
-    auto load = [&](int32_t s) {
+    auto load = [&](int32_t s, int j) {
         uint8_t* const to = lds + s % BUFS * kBuffer;
         const int32_t l0 = s * L;
-        const bool whole = l0 + L <= in;
-#pragma unroll
-        for (int j = 0; j < kLoads; ++j) {
-            const int32_t v = whole || l0 + first[j] < in ? off[j] : kOutside;
-            if (j < 2)
-                load_to_lds<16>(codes, frows * cpitch, to + w * (FW * kCodeRow) + j * 1024, v, l0 / 2);
-            else if (j < 2 + kScaleLoads)
-                load_to_lds<WORDS ? 4 : 1>(scales, frows * spitch, to + kCodes + w * kScaleBytes + (j - 2) * 256, v,
-                                           l0 / 16);
-            else
-                load_to_lds<16>(x, t.rows * in * 2,
-                                to + kCodes + kScales + (w * kRowLoads + j - 2 - kScaleLoads) * 1024, v, l0 * 2);
-        }
+        const int32_t v = l0 + L <= in || l0 + first[j] < in ? off[j] : kOutside;
+        if (j < 2)
+            load_to_lds<16>(codes, frows * cpitch, to + w * (FW * kCodeRow) + j * 1024, v, l0 / 2);
+        else if (j < 2 + kScaleLoads)
+            load_to_lds<WORDS ? 4 : 1>(scales, frows * spitch, to + kCodes + w * kScaleBytes + (j - 2) * 256, v, l0 / 16);
+        else
+            load_to_lds<16>(x, t.rows * in * 2, to + kCodes + kScales + (w * kRowLoads + j - 2 - kScaleLoads) * 1024, v,
+                            l0 * 2);
     };
     f32x4 acc[FW / 16][NT / 16] = {};
     const int32_t steps = (in + L - 1) / L;
-    for (int s = 0; s < BUFS - 1; ++s) load(s);
+    for (int s = 0; s < BUFS - 1; ++s)
+#pragma unroll
+        for (int j = 0; j < kLoads; ++j) load(s, j);
     for (int32_t s = 0; s < steps; ++s) {
         // This step's loads have landed when only the later steps' are
         // outstanding: loads return in order, and past the end they still
@@ -135,7 +136,10 @@ __global__ __launch_bounds__(WAVES * kWave) void k_nvfp4(ExpertArgs a, int32_t f
         // every wave is done with the last step's buffer, which is filled next.
         asm volatile("s_waitcnt vmcnt(%0)" ::"n"((BUFS - 2) * kLoads) : "memory");
         lds_barrier();
-        load(s + BUFS - 1);
+        if (!kSpread) {
+#pragma unroll
+            for (int j = 0; j < kLoads; ++j) load(s + BUFS - 1, j);
+        }
         const uint8_t* const from = lds + s % BUFS * kBuffer;
         v4u cw[FW / 16][kLane / 32];
         float sc[FW / 16][kLane / 16];
@@ -161,18 +165,37 @@ __global__ __launch_bounds__(WAVES * kWave) void k_nvfp4(ExpertArgs a, int32_t f
             }
         }
         const uint8_t* const rows = from + kCodes + kScales + i * kRowBytes;
+        constexpr int kGroups = kLane / 8;  // of 8 values a lane: one matrix instruction each way
+        bf16x8 wv[2][FW / 16], xv[2][NT / 16];
+        auto operands = [&](int j) {
 #pragma unroll
-        for (int j = 0; j < kLane / 8; ++j) {
-            bf16x8 wv[FW / 16];
+            for (int g = 0; g < FW / 16; ++g) wv[j % 2][g] = weights8(cw[g][j / 4][j % 4], sc[g][j / 2]);
 #pragma unroll
-            for (int g = 0; g < FW / 16; ++g) wv[g] = weights8(cw[g][j / 4][j % 4], sc[g][j / 2]);
+            for (int n = 0; n < NT / 16; ++n)
+                xv[j % 2][n] = *reinterpret_cast<const bf16x8*>(rows + n * 16 * kRowBytes +
+                                                                (((j / 4 * 4 + q) * 4 + j % 4) ^ swizzle_row(i)) * 16);
+        };
+        operands(0);
 #pragma unroll
-            for (int n = 0; n < NT / 16; ++n) {
-                const bf16x8 xv = *reinterpret_cast<const bf16x8*>(rows + n * 16 * kRowBytes +
-                                                                   (((j / 4 * 4 + q) * 4 + j % 4) ^ swizzle_row(i)) * 16);
+        for (int j = 0; j < kGroups; ++j) {
+            if constexpr (kSpread) {
+                __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+                for (int k = j * kLoads / kGroups; k < (j + 1) * kLoads / kGroups; ++k) load(s + BUFS - 1, k);
+            }
+            if (j + 1 < kGroups) operands(j + 1);
+#pragma unroll
+            for (int n = 0; n < NT / 16; ++n)
 #pragma unroll
                 for (int g = 0; g < FW / 16; ++g)
-                    acc[g][n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wv[g], xv, acc[g][n], 0, 0, 0);
+                    acc[g][n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wv[j % 2][g], xv[j % 2][n], acc[g][n], 0, 0, 0);
+            if constexpr (kSpread) {
+                __builtin_amdgcn_sched_group_barrier(0x100, NT / 16, 0);  // LDS reads, then
+#pragma unroll
+                for (int n = 0; n < NT / 16 * (FW / 16); ++n) {
+                    __builtin_amdgcn_sched_group_barrier(0x8, 1, 0);  // a matrix instruction and
+                    __builtin_amdgcn_sched_group_barrier(0x2, 3, 0);  // its share of the conversions, in turn
+                }
             }
         }
     }
@@ -214,14 +237,20 @@ hipError_t nvfp4(const ExpertArgs& a, hipStream_t stream) {
 
 }  // namespace
 
+// By the rows a group has on average.  Measured over 64 experts of 4096 x 7168,
+// us at 8, 12, 16, 24, 32 and 64 rows a group:
+//   16-row tiles    257  286  343  444  516  854
+//   32              289  301  307  333  424  659
+//   64              334  339  347  351  365  505
+//   128             424  436  440  446  450  482
 hipError_t launch_expert_gemm_nvfp4(const ExpertArgs& a, hipStream_t stream) {
     const int64_t groups = a.slots < a.E + a.shared ? a.slots : a.E + a.shared;
     if (groups == 0) return hipSuccess;
     const int64_t mean = a.slots / groups;
-    if (mean > 56) return nvfp4<128, 32, 8, 128, 3, 2>(a, stream);
-    if (mean > 24) return nvfp4<64, 16, 8, 256, 3, 2>(a, stream);
-    if (mean > 10) return nvfp4<32, 16, 8, 256, 4, 3>(a, stream);
-    return nvfp4<16, 16, 4, 256, 3, 3>(a, stream);
+    if (mean <= 13) return nvfp4<16, 16, 4, 256, 3, 3>(a, stream);
+    if (mean <= 26) return nvfp4<32, 16, 4, 256, 2, 2>(a, stream);
+    if (mean <= 56) return nvfp4<64, 32, 8, 128, 2, 2>(a, stream);
+    return nvfp4<128, 32, 8, 128, 3, 2>(a, stream);
 }
 
 }  // namespace epx
