@@ -471,12 +471,18 @@ __global__ __launch_bounds__(kTopkThreads) void k_route_bwd(TopkArgs a) {
     }
     float q = 0.0f;
     if (id >= 0) q = a.sigmoid ? 1.0f / (1.0f + expf(-zk)) : expf(zk - zmax) / total;
-    float gq = a.scale * g;
+    // g_k - sum_j g_j q_j / Q as (sum_j (g_k - g_j) q_j + 1e-20 g_k) / Q: weights
+    // of nearly equal gradients, or a token's only one, cancel exactly.
+    float gq = a.scale * g, dot = 0.0f;
     if (a.normalize) {
-        const float Q = wave_sum(q) + 1e-20f;
-        gq = a.scale * (g - wave_sum(g * q) / Q) / Q;
+        const float Q = wave_sum(q) + 1e-20f, gq_sum = wave_sum(g * q);
+        float diff = 1e-20f * g;
+        for (int j = 0; j < a.K; ++j) diff += (g - lane_value(g, j)) * lane_value(q, j);
+        gq = a.scale * diff / Q / Q;
+        dot = a.scale * 1e-20f * gq_sum / Q / Q;  // sum_k gq_k q_k: the differences cancel in pairs
     }
     if (id < 0) gq = 0.0f;
+    if (!a.normalize) dot = wave_sum(gq * q);
     const float own = a.sigmoid ? gq * q * (1.0f / (1.0f + expf(zk))) : gq;
     float gz[VPL];
 #pragma unroll
@@ -488,7 +494,6 @@ __global__ __launch_bounds__(kTopkThreads) void k_route_bwd(TopkArgs a) {
         for (int i = 0; i < VPL; ++i) gz[i] += e == lane * VPL + i ? o : 0.0f;
     }
     if (!a.sigmoid) {
-        const float dot = wave_sum(gq * q);
 #pragma unroll
         for (int i = 0; i < VPL; ++i) gz[i] = any ? z[i] / total * (gz[i] - dot) : 0.0f;
     }
@@ -605,7 +610,7 @@ __global__ __launch_bounds__(kTopkThreads) void k_route_narrow(TopkArgs a) {
 template <int VPL, bool BF16>
 __global__ __launch_bounds__(kTopkThreads) void k_route_bwd_narrow(TopkArgs a) {
     __shared__ int32_t s_id[kNarrowTokens][kRowLanes];
-    __shared__ float s_own[kNarrowTokens][kRowLanes];
+    __shared__ float s_own[kNarrowTokens][kRowLanes], s_g[kNarrowTokens][kRowLanes], s_q[kNarrowTokens][kRowLanes];
     const int l = threadIdx.x % kRowLanes, mine = threadIdx.x / kRowLanes;
     const int32_t t = (int32_t)(blockIdx.x * kNarrowTokens) + mine;
     const bool in = t < a.T;
@@ -640,12 +645,19 @@ __global__ __launch_bounds__(kTopkThreads) void k_route_bwd_narrow(TopkArgs a) {
     }
     float q = 0.0f;
     if (id >= 0) q = a.sigmoid ? 1.0f / (1.0f + expf(-zk)) : expf(zk - zmax) / total;
-    float gq = a.scale * g;
+    float gq = a.scale * g, dot = 0.0f;  // as in k_route_bwd
     if (a.normalize) {
-        const float Q = row_sum(q) + 1e-20f;
-        gq = a.scale * (g - row_sum(g * q) / Q) / Q;
+        const float Q = row_sum(q) + 1e-20f, gq_sum = row_sum(g * q);
+        s_g[mine][l] = g;
+        s_q[mine][l] = q;
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        float diff = 1e-20f * g;
+        for (int j = 0; j < a.K; ++j) diff += (g - s_g[mine][j]) * s_q[mine][j];
+        gq = a.scale * diff / Q / Q;
+        dot = a.scale * 1e-20f * gq_sum / Q / Q;
     }
     if (id < 0) gq = 0.0f;
+    if (!a.normalize) dot = row_sum(gq * q);
     s_id[mine][l] = id;
     s_own[mine][l] = a.sigmoid ? gq * q * (1.0f / (1.0f + expf(zk))) : gq;
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
@@ -659,7 +671,6 @@ __global__ __launch_bounds__(kTopkThreads) void k_route_bwd_narrow(TopkArgs a) {
         for (int i = 0; i < VPL; ++i) gz[i] += e == l * VPL + i ? o : 0.0f;
     }
     if (!a.sigmoid) {
-        const float dot = row_sum(gq * q);
 #pragma unroll
         for (int i = 0; i < VPL; ++i) gz[i] = any ? z[i] / total * (gz[i] - dot) : 0.0f;
     }

@@ -219,6 +219,24 @@ def test_route_gradient_against_differences(G):
                 assert (gz[:, e].double().cpu() - slope).abs().max() < 1e-5
 
 
+def test_route_gradient_of_a_constant_weight(G):
+    """One expert a token with normalized weights, or equal gradients for all of
+    them: the weights do not move with the logits; what is left is the 1e-20 in
+    the sum, scale g 1e-20 / Q^2 at most (Q >= 1/E here), not fp32's rounding."""
+    T, E = 50, 64
+    for E, K in ((64, 1), (64, 6), (512, 1), (512, 6)):
+        for score in ("softmax", "sigmoid"):
+            cfg = G.epx.EpConfig(num_tokens=T, hidden=8, num_experts=E, num_segments=1, top_k=K)
+            r = G.epx.RouteConfig(score=score, scale=2.5)
+            logits = normal(8, T, E, dtype=torch.float32)
+            ids, p = torch.empty(T, K, dtype=torch.int32, device="cuda:0"), torch.empty(T, K, device="cuda:0")
+            G.epx.ep_route(cfg, r, logits, ids, p)
+            g = normal(9, T, 1, dtype=torch.float32).expand(T, K).contiguous()
+            gz = torch.empty_like(logits)
+            G.epx.ep_route_bwd(cfg, r, logits, ids, g, gz)
+            assert gz.abs().max().item() <= 2.5 * g.abs().max().item() * 1e-20 * E * E
+
+
 def test_route_bwd_skips_invalid_ids(G):
     """Ids outside [0, E) count as unused; a repeated id gets both slots' gradients."""
     cfg = G.epx.EpConfig(num_tokens=2, hidden=8, num_experts=8, num_segments=1, top_k=4)
