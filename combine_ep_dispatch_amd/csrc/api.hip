@@ -358,6 +358,9 @@ int check_expert(const Shape& d, const ep_layout_t* L, int32_t in_dim, int32_t o
     return EP_OK;
 }
 
+// A product whose tiles pass one grid is an argument error, found before the launch.
+int expert_status(hipError_t e) { return e == hipErrorInvalidConfiguration ? EP_EINVAL : status_of(e); }
+
 ExpertArgs expert_args(const Shape& d, const ep_layout_t* L, int32_t in_dim, int32_t out_dim, void* out) {
     ExpertArgs a = {};
     a.out = out;
@@ -786,7 +789,7 @@ int ep_expert_gemm(const ep_cfg_t* cfg, const ep_layout_t* layout, int32_t in_di
     ExpertArgs a = expert_args(d, layout, in_dim, out_dim, y);
     a.x = x;
     a.w = w;
-    if ((rc = status_of(launch_expert_gemm(a, st))) != EP_OK) return rc;
+    if ((rc = expert_status(launch_expert_gemm(a, st))) != EP_OK) return rc;
     return zero_pad(d, layout, y, (int64_t)out_dim * 2, st);
 }
 
@@ -803,7 +806,7 @@ int ep_expert_gemm_bwd_x(const ep_cfg_t* cfg, const ep_layout_t* layout, int32_t
     ExpertArgs a = expert_args(d, layout, in_dim, out_dim, grad_x);
     a.gy = grad_y;
     a.w = w;
-    if ((rc = status_of(launch_expert_gemm_bwd_x(a, st))) != EP_OK) return rc;
+    if ((rc = expert_status(launch_expert_gemm_bwd_x(a, st))) != EP_OK) return rc;
     return zero_pad(d, layout, grad_x, (int64_t)in_dim * 2, st);
 }
 
@@ -821,7 +824,7 @@ int ep_expert_gemm_bwd_w(const ep_cfg_t* cfg, const ep_layout_t* layout, int32_t
     a.gy = grad_y;
     a.x = x;
     a.grad_type = grad_type;
-    return status_of(launch_expert_gemm_bwd_w(a, static_cast<hipStream_t>(stream)));
+    return expert_status(launch_expert_gemm_bwd_w(a, static_cast<hipStream_t>(stream)));
 }
 
 int ep_expert_gemm_nvfp4(const ep_cfg_t* cfg, const ep_layout_t* layout, int32_t in_dim, int32_t out_dim,
@@ -832,7 +835,7 @@ int ep_expert_gemm_nvfp4(const ep_cfg_t* cfg, const ep_layout_t* layout, int32_t
     if (rc != EP_OK) return rc;
     if ((rc = check_expert(d, layout, in_dim, out_dim, 16)) != EP_OK) return rc;
     if (bad_buffer(x, d.R * in_dim * 2, 16) || bad_buffer(codes, 16, 16) || bad_buffer(scales, 16, 16) ||
-        bad_buffer(rowscale, 2, 2) || bad_buffer(y, d.R * out_dim * 2, 16))
+        bad_buffer(rowscale, 8, 8) || bad_buffer(y, d.R * out_dim * 2, 16))
         return EP_EINVAL;
     if ((rc = check_device()) != EP_OK) return rc;
     hipStream_t st = static_cast<hipStream_t>(stream);
@@ -841,7 +844,7 @@ int ep_expert_gemm_nvfp4(const ep_cfg_t* cfg, const ep_layout_t* layout, int32_t
     a.codes = codes;
     a.scales = scales;
     a.rowscale = rowscale;
-    if ((rc = status_of(launch_expert_gemm_nvfp4(a, st))) != EP_OK) return rc;
+    if ((rc = expert_status(launch_expert_gemm_nvfp4(a, st))) != EP_OK) return rc;
     return zero_pad(d, layout, y, (int64_t)out_dim * 2, st);
 }
 

@@ -1,5 +1,6 @@
 // Device-side helpers and kernel launchers shared by the epx HIP sources.
-// gfx950 (CDNA4) only: wave64, 64 KiB of LDS per workgroup used at most.
+// gfx950 (CDNA4) only: wave64, 64 KiB of LDS per workgroup used at most (the
+// experts' products: up to all 160 KiB).
 #pragma once
 
 #include <hip/hip_runtime.h>

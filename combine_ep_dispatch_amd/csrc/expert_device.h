@@ -18,8 +18,8 @@ constexpr int kOutside = 0x7FFFFFF0;                       // an offset past eve
 
 // BYTES (16, 4 or 1) a lane from offset voff + soff of a buffer of `bytes` bytes to
 // LDS: lane l's 16 at lds + 16 l, its 4 at lds + 4 l, its 1 as a word at
-// lds + 4 l; zeros for words past the buffer's end, and wherever voff alone is
-// past it.  base, bytes, lds and soff are the same in all lanes.  Written out, because the compiler waits for every
+// lds + 4 l; zeros for words past the buffer's end.  base, bytes, lds and soff
+// are the same in all lanes.  Written out, because the compiler waits for every
 // load in flight (vmcnt 0) before any LDS read that follows its builtin.
 // Nothing waits for this load by itself: whoever reads the LDS bytes waits for
 // vmcnt first.  (m0 holds the LDS address; one wait state between its write
@@ -69,6 +69,12 @@ __device__ __forceinline__ GroupRows group_rows(const ExpertArgs& a, int32_t g) 
 __device__ __forceinline__ int32_t group_expert(const ExpertArgs& a, int32_t g) {
     const int32_t s = g / a.G, gl = g - s * a.G;
     return gl < a.shared ? a.E : s * a.E_loc + gl - a.shared;
+}
+
+// A launch of `blocks` workgroups fits one grid (a count of work-items in 32
+// bits); the entry points answer EP_EINVAL to the error.
+inline hipError_t check_grid(int64_t blocks, int threads) {
+    return blocks * threads > 0xFFFFFFFFll ? hipErrorInvalidConfiguration : hipSuccess;
 }
 
 // Most row tiles of BM rows that the groups can need: every group with rows

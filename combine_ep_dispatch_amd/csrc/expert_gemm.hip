@@ -286,7 +286,7 @@ hipError_t wide(const ExpertArgs& a, hipStream_t stream) {
     if (P == kWeightGrad) rtiles = (rtiles + 15) / 16 * 16;  // whole turns of the XCDs
     const int64_t blocks = (rtiles * ftiles + 7) / 8 * 8;
     if (blocks == 0) return hipSuccess;
-    if (blocks * kWideThreads > 0xFFFFFFFFll) return hipErrorInvalidValue;
+    if (const hipError_t e = check_grid(blocks, kWideThreads)) return e;
     hipLaunchKernelGGL((k_expert_wide<P, NT>), dim3((unsigned)blocks), dim3(kWideThreads), 0, stream, a, ftiles, ntiles);
     return hipGetLastError();
 }

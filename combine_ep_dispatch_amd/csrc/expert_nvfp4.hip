@@ -225,7 +225,7 @@ hipError_t nvfp4(const ExpertArgs& a, hipStream_t stream) {
     const int32_t ftiles = (a.on + kF - 1) / kF;
     const int64_t tiles = max_row_tiles(a, NT) * ftiles, blocks = (tiles + 7) / 8 * 8;
     if (tiles == 0) return hipSuccess;
-    if (blocks * WAVES * kWave > 0xFFFFFFFFll) return hipErrorInvalidValue;
+    if (const hipError_t e = check_grid(blocks, WAVES * kWave)) return e;
     if (a.in % 64 == 0)
         hipLaunchKernelGGL((k_nvfp4<NT, FW, WAVES, L, BUFS, true>), dim3((unsigned)blocks), dim3(WAVES * kWave), 0,
                            stream, a, ftiles);

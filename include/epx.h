@@ -465,6 +465,7 @@ typedef struct ep_route_t {
  *   probs[t,k] = scale * s[id_k] / (sum_j s[id_j] + 1e-20)   normalize = 1
  *              = scale * s[id_k]                             normalize = 0
  * in fp32, from the scores without the bias.
+ * logits and grad_logits are 16-byte aligned.
  * An expert with a logit of -infinity or NaN is never chosen; a token with
  * fewer than K experts to choose from has id -1 and weight 0 in its last
  * slots.  Softmax sums over every expert of the token (a NaN or +infinity
@@ -529,7 +530,11 @@ int ep_swiglu_bwd(const ep_cfg_t* cfg, const ep_layout_t* layout, int32_t inter,
  *   shared expert last;  y  bf16 [R, out_dim].
  * in_dim and out_dim: multiples of 8 in [8, EP_MAX_EXPERT_DIM] (cfg->hidden
  * takes no part).  Uses layout->counts, row_offsets and seg_base, not the
- * ids: rows of one group belong to one expert.
+ * ids: rows of one group belong to one expert.  A row's results do not depend
+ * on which other rows its group holds, and repeat bit for bit.  This call, its
+ * gradients and ep_expert_gemm_nvfp4 return EP_EINVAL where their tiles pass
+ * one grid of 2^32 work-items (2^23 tiles of 128 x 256 results; 2^24 tiles of
+ * 16 x 64 for 4-bit weights).
  */
 int ep_expert_gemm(const ep_cfg_t* cfg, const ep_layout_t* layout, int32_t in_dim, int32_t out_dim,
                    const uint16_t* x, const uint16_t* w, uint16_t* y, void* stream);
@@ -567,7 +572,7 @@ int ep_expert_gemm_bwd_w(const ep_cfg_t* cfg, const ep_layout_t* layout, int32_t
  *   rowscale bf16  [E + shared, out_dim]
  *   y        bf16  [R, out_dim]
  * in_dim: a multiple of 16, out_dim of 8, both at most EP_MAX_EXPERT_DIM; codes
- * and scales 16-byte aligned.
+ * and scales 16-byte aligned, rowscale 8-byte.
  */
 int ep_expert_gemm_nvfp4(const ep_cfg_t* cfg, const ep_layout_t* layout, int32_t in_dim, int32_t out_dim,
                          const uint16_t* x, const uint8_t* codes, const uint8_t* scales,

@@ -291,6 +291,7 @@ LAYOUTS = {  # name: config, fraction of unused slots, expert weights (None: uni
     "skewed": (dict(num_tokens=333, num_experts=8, num_segments=2, top_k=2, align=16), 0.0, "skew"),
     "capacity": (dict(num_tokens=200, num_experts=8, num_segments=2, top_k=3, align=8, seg_capacity=217), 0.0, "skew"),
     "many-groups": (dict(num_tokens=40, num_experts=2000, num_segments=8, top_k=4, align=1), 0.0, None),
+    "twenty": (dict(num_tokens=40, num_experts=4, num_segments=1, top_k=2, align=16), 0.0, None),
     "tall": (dict(num_tokens=700, num_experts=2, num_segments=1, top_k=2, align=128), 0.0, None),
 }
 
@@ -479,7 +480,7 @@ def nvfp4_weights(seed, experts, n_out, n_in):
     return [t.to("cuda:0") for t in (torch.from_numpy(codes), torch.from_numpy(scales), rowscale)], w, rowscale.double()
 
 
-NV_DIMS = [(16, 8), (48, 264), (272, 72), (1040, 136), (528, 520)]
+NV_DIMS = [(16, 8), (48, 264), (64, 136), (272, 72), (320, 264), (1040, 136), (528, 520), (1152, 72)]
 
 
 @pytest.mark.parametrize("name", LAYOUTS)
@@ -546,6 +547,144 @@ def test_infinities_and_nan_stay_in_their_rows(G):
     assert torch.equal(got.view(torch.int16).cpu()[keep], clean.view(torch.int16).cpu()[keep])
     assert torch.equal(gotq.view(torch.int16).cpu()[keep], cleanq.view(torch.int16).cpu()[keep])
     assert not torch.isfinite(got.cpu()[bad].float()).all(1).any()
+
+
+def test_a_rows_results_do_not_depend_on_the_batch(G):
+    """The same row alone, among few and among many rows of its expert (other tile
+    sizes): the same bits."""
+    n_in, n_out = 448, 264
+    x1, w = normal(1, 1, n_in), normal(3, 1, n_out, n_in)
+    (codes, scales, rowscale), _, _ = nvfp4_weights(5, 1, n_out, n_in)
+    seen = []
+    for T in (1, 20, 40, 100, 700):
+        cfg = G.epx.EpConfig(num_tokens=T, hidden=16, num_experts=1, num_segments=1, top_k=1)
+        cfg.recv_rows = G.epx.ep_query(cfg).min_recv_rows
+        lay = G.epx.Layout.empty(cfg, "cuda:0")
+        ids = torch.zeros(T, dtype=torch.int32, device="cuda:0")
+        G.epx.ep_dispatch_layout(cfg, ids, G.epx.workspace_for(cfg, "cuda:0"), lay)
+        x = normal(T, T, n_in)
+        x[T // 2] = x1[0]
+        y, yq, gx = filled(T, n_out), filled(T, n_out), filled(T, n_out)
+        G.epx.ep_expert_gemm(cfg, lay, x, w, y)
+        G.epx.ep_expert_gemm_nvfp4(cfg, lay, x, codes, scales, rowscale, yq)
+        G.epx.ep_expert_gemm_bwd_x(cfg, lay, x, w.transpose(1, 2).contiguous(), gx)
+        seen.append([v[T // 2].view(torch.int16).cpu() for v in (y, yq, gx)])
+    for other in seen[1:]:
+        for a, b in zip(seen[0], other):
+            assert torch.equal(a, b)
+
+
+def test_offsets_past_32_bits(G):
+    """Receive rows, weights, codes, activations and logits of more than 2^32
+    bytes (and values): the last ones are right."""
+    dev = "cuda:0"
+    # rows: 330 000 of 7168 values
+    T, n_in, n_out = 330_000, 7168, 8
+    cfg = G.epx.EpConfig(num_tokens=T, hidden=16, num_experts=2, num_segments=1, top_k=1)
+    cfg.recv_rows = T
+    lay = G.epx.Layout.empty(cfg, dev)
+    ids = torch.arange(T, device=dev, dtype=torch.int32) % 2
+    G.epx.ep_dispatch_layout(cfg, ids, G.epx.workspace_for(cfg, dev), lay)
+    x = torch.empty(T, n_in, dtype=torch.bfloat16, device=dev).normal_()
+    w = normal(3, 2, n_out, n_in)
+    y, gx = filled(T, n_out), torch.empty_like(x)
+    some = torch.tensor([0, 1, T // 2 - 1, T // 2, 299_593, 299_594, T - 2, T - 1], device=dev)
+    e = (some >= T // 2).long()
+    G.say("[gpu] far rows")
+    G.epx.ep_expert_gemm(cfg, lay, x, w, y)
+    xs, ws = x[some].double().cpu(), w.double().cpu()[e.cpu()]
+    want, size = torch.einsum("rh,rnh->rn", xs, ws), torch.einsum("rh,rnh->rn", xs.abs(), ws.abs())
+    check(y[some], want, rounded(want, size * (n_in + 1) * U32), "far rows")
+    gy = normal(4, T, n_out)
+    G.epx.ep_expert_gemm_bwd_x(cfg, lay, gy, w, gx)
+    gs = gy[some].double().cpu()
+    want, size = torch.einsum("rn,rnh->rh", gs, ws), torch.einsum("rn,rnh->rh", gs.abs(), ws.abs())
+    check(gx[some], want, rounded(want, size * (n_out + 1) * U32), "far gradients")
+    act = gx.view(-1)[: T * n_in // 2].view(T, n_in // 2)
+    G.epx.ep_swiglu(cfg, lay, x, None, act)
+    a, b = xs.split(n_in // 2, 1)
+    want = a * torch.sigmoid(a) * b
+    check(act[some], want, rounded(want, want.abs() * (16 + a.abs()) * U32 + 2.0 ** -126), "far activations")
+    del x, gx, act
+    # weights: 70 experts of 8192 x 8192, 4-bit and bf16 (9.4 GB); one token each way
+    E, n = 70, 8192
+    cfg = G.epx.EpConfig(num_tokens=1, hidden=16, num_experts=E, num_segments=1, top_k=2)
+    cfg.recv_rows = 2
+    lay = G.epx.Layout.empty(cfg, dev)
+    G.epx.ep_dispatch_layout(cfg, torch.tensor([E - 1, 0], dtype=torch.int32, device=dev), G.epx.workspace_for(cfg, dev), lay)
+    x = normal(1, 2, n)
+    w = torch.empty(E, n, n, dtype=torch.bfloat16, device=dev).normal_()
+    y = filled(2, n)
+    G.say("[gpu] far weights")
+    G.epx.ep_expert_gemm(cfg, lay, x, w, y)
+    for row, e in ((0, 0), (1, E - 1)):
+        a, m = x[row].double(), w[e].double()
+        want, size = m @ a, m.abs() @ a.abs()
+        check(y[row], want, rounded(want, size * (n + 1) * U32), "far weights")
+    gw = w  # the gradient of all experts, in the weights' place
+    G.epx.ep_expert_gemm_bwd_w(cfg, lay, x, x, gw)
+    assert (gw[1:-1] == 0).all()
+    for row, e in ((0, 0), (1, E - 1)):
+        a = x[row].double()
+        want = torch.outer(a, a)
+        check(gw[e], want, rounded(want, want.abs() * 2 * U32), "far weights' gradient")
+    del w, gw
+    E = 140
+    cfg.num_experts = E
+    lay = G.epx.Layout.empty(cfg, dev)
+    G.epx.ep_dispatch_layout(cfg, torch.tensor([E - 1, 0], dtype=torch.int32, device=dev), G.epx.workspace_for(cfg, dev), lay)
+    codes = torch.randint(0, 256, (E, n, n // 2), dtype=torch.uint8, device=dev)
+    scales = torch.randint(0x30, 0x70, (E, n, n // 16), dtype=torch.uint8, device=dev)
+    rowscale = torch.rand(E, n, device=dev).to(torch.bfloat16)
+    G.say("[gpu] far codes")
+    G.epx.ep_expert_gemm_nvfp4(cfg, lay, x, codes, scales, rowscale, y)
+    for row, e in ((0, 0), (1, E - 1)):
+        c = codes[e].long().cpu()
+        v = torch.stack([E2M1[c & 15], E2M1[c >> 4]], -1).view(n, n // 16, 16)
+        m = (v * scales[e].cpu().view(torch.float8_e4m3fn).double()[..., None]).view(n, n)
+        a, rs = x[row].double().cpu(), rowscale[e].double().cpu()
+        want, size = m @ a * rs, m.abs() @ a.abs() * rs
+        check(y[row], want, rounded(want, size * (n + 2) * U32), "far codes")
+    del codes, scales, rowscale
+    # logits: 2.2 million tokens of 1024 experts
+    T, E, K = 2_200_000, 1024, 4
+    cfg = G.epx.EpConfig(num_tokens=T, hidden=8, num_experts=E, num_segments=1, top_k=K)
+    logits = torch.empty(T, E, device=dev).normal_()
+    ids, p = torch.empty(T, K, dtype=torch.int32, device=dev), torch.empty(T, K, device=dev)
+    r = G.epx.RouteConfig(score="sigmoid")
+    G.say("[gpu] far logits")
+    G.epx.ep_route(cfg, r, logits, ids, p)
+    some = torch.tensor([0, 1, T // 2, 2_097_152, 2_097_153, T - 1], device=dev)
+    want_ids, s, q, want = plain_route(logits[some], None, None, K, r)
+    np.testing.assert_array_equal(ids[some].cpu().numpy(), want_ids)
+    check(p[some], torch.from_numpy(want), torch.from_numpy(want * 64 * U32), "far weights")
+    gz = torch.full_like(logits, 7.0)
+    G.epx.ep_route_bwd(cfg, r, logits, ids, p, gz)
+    want, mag = plain_route_bwd(logits[some].double().cpu().numpy(), s, want_ids, q, p[some].double().cpu().numpy(), r)
+    check(gz[some], torch.from_numpy(want), torch.from_numpy(mag * 64 * U32 + 1e-30), "far gradients")
+
+
+def test_products_past_one_grid_are_refused(G):
+    """2048 groups of 2^20 features: more workgroups than a launch holds."""
+    E, big = 2048, 1 << 20
+    cfg = G.epx.EpConfig(num_tokens=E, hidden=8, num_experts=E, num_segments=1, top_k=1)
+    cfg.recv_rows = E
+    lay = G.epx.Layout.empty(cfg, "cuda:0")
+    ids = torch.arange(E, dtype=torch.int32, device="cuda:0")
+    G.epx.ep_dispatch_layout(cfg, ids, G.epx.workspace_for(cfg, "cuda:0"), lay)
+    w = torch.empty(E * big * 8, dtype=torch.bfloat16, device="cuda:0")
+    rows, few = torch.empty(E, big, dtype=torch.bfloat16, device="cuda:0"), normal(1, E, 8)
+    codes, scales = (torch.empty(E, big, n, dtype=torch.uint8, device="cuda:0") for n in (8, 1))
+    rowscale = torch.empty(E, big, dtype=torch.bfloat16, device="cuda:0")
+    calls = [
+        lambda: G.epx.ep_expert_gemm(cfg, lay, few, w.view(E, big, 8), rows),
+        lambda: G.epx.ep_expert_gemm_bwd_x(cfg, lay, few, w.view(E, 8, big), rows),
+        lambda: G.epx.ep_expert_gemm_bwd_w(cfg, lay, rows, few, w.view(E, big, 8)),
+        lambda: G.epx.ep_expert_gemm_nvfp4(cfg, lay, normal(2, E, 16), codes, scales, rowscale, rows),
+    ]
+    for call in calls:
+        with pytest.raises(G.epx.EpError, match="status -1"):
+            call()
 
 
 # ---------------------------------------------------------------------------
