@@ -9,6 +9,16 @@
 // tile.  Lane (i, q) of a wave takes feature i and 32 values, two whole blocks,
 // of every 128 of the step; which value of a step is which does not matter to
 // the sum as long as the rows are read in the same order.
+//
+// What bounds it: with one row an expert the latency of the first loads and
+// HBM (8 experts of 4096 x 7168, 132 MB: 30 us, 4.4 TB/s; loads alone 26, all
+// but the loads 25); at 8 rows HBM and the conversions (65 experts, 1.09 GB:
+// 248 us, 4.4 TB/s; loads alone 242, of which the 4-byte loads of the scales
+// are 55, all but the loads 143); at 122 rows the conversions, two instructions
+// a weight and row tile, and the matrix instructions of tiles that 122 rows
+// fill three quarters of (32 experts of 7168 x 2048: 190 us, 602 TFLOP/s; loads
+// alone 137, all but the loads 159).  Scales as 64-byte windows a step ahead load
+// in 187 us instead of 242, but their LDS costs a workgroup a CU: 254-274 us in all.
 #include "expert_device.h"
 
 namespace epx {
