@@ -17,8 +17,12 @@
 // are 55, all but the loads 143); at 122 rows the conversions, two instructions
 // a weight and row tile, and the matrix instructions of tiles that 122 rows
 // fill three quarters of (32 experts of 7168 x 2048: 190 us, 602 TFLOP/s; loads
-// alone 137, all but the loads 159).  Scales as 64-byte windows a step ahead load
-// in 187 us instead of 242, but their LDS costs a workgroup a CU: 254-274 us in all.
+// alone 137, all but the loads 159).  Measured instead: scales as 64-byte windows
+// load in 187 us instead of 242, but two of them in LDS cost a workgroup a CU
+// (254-274 us in all), and one, taken to registers for four steps, gains nothing
+// (262, and 36 us instead of 32 for one row); 4 waves of 64 features by 128 rows
+// for prompts, 233 us instead of 194; half the products of tiles that are at most
+// half full, 193.
 #include "expert_device.h"
 
 namespace epx {
