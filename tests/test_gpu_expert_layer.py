@@ -296,11 +296,18 @@ LAYOUTS = {  # name: config, fraction of unused slots, expert weights (None: uni
 }
 
 
+MANY = {  # enough tiles of 64 x 64 for the wide ones: by 256 rows, by 128, unevenly
+    "many-rows": (dict(num_tokens=3000, num_experts=4, num_segments=2, top_k=2, align=1, shared_expert=1), 0.02, None),
+    "many-75": (dict(num_tokens=1500, num_experts=40, num_segments=4, top_k=2, align=16), 0.0, None),
+    "many-skewed": (dict(num_tokens=3001, num_experts=6, num_segments=1, top_k=2, align=8), 0.1, "skew"),
+}
+
+
 class Rows:
     """A layout made by ep_dispatch_layout, and what the plain forms need of it."""
 
     def __init__(self, G, name, hidden=16, flags=0, seed=0):
-        kw, unused, weights = LAYOUTS[name]
+        kw, unused, weights = (LAYOUTS | MANY)[name]
         cfg = G.epx.EpConfig(hidden=hidden, flags=flags, **kw)
         cfg.recv_rows = G.epx.ep_query(cfg).min_recv_rows + 5  # rows behind the last segment
         rng = np.random.default_rng(seed + 17)
@@ -464,6 +471,12 @@ def test_expert_gemm_and_gradients(G, name, dims):
     d.untouched(gx)
 
 
+@pytest.mark.parametrize("name", MANY)
+@pytest.mark.parametrize("dims", [(520, 584), (1032, 520)], ids=str)
+def test_expert_gemm_and_gradients_of_many_rows(G, name, dims):
+    test_expert_gemm_and_gradients(G, name, dims)
+
+
 E2M1 = torch.tensor([0, .5, 1, 1.5, 2, 3, 4, 6, -0., -.5, -1, -1.5, -2, -3, -4, -6], dtype=torch.float64)
 
 
@@ -556,19 +569,21 @@ def test_a_rows_results_do_not_depend_on_the_batch(G):
     x1, w = normal(1, 1, n_in), normal(3, 1, n_out, n_in)
     (codes, scales, rowscale), _, _ = nvfp4_weights(5, 1, n_out, n_in)
     seen = []
-    for T in (1, 20, 40, 100, 700):
-        cfg = G.epx.EpConfig(num_tokens=T, hidden=16, num_experts=1, num_segments=1, top_k=1)
+    for E, T in ((1, 1), (1, 20), (1, 40), (1, 100), (1, 700), (1, 15000), (160, 1600)):
+        cfg = G.epx.EpConfig(num_tokens=T, hidden=16, num_experts=E, num_segments=1, top_k=1)
         cfg.recv_rows = G.epx.ep_query(cfg).min_recv_rows
         lay = G.epx.Layout.empty(cfg, "cuda:0")
-        ids = torch.zeros(T, dtype=torch.int32, device="cuda:0")
+        ids = torch.arange(T, dtype=torch.int32, device="cuda:0") % E
         G.epx.ep_dispatch_layout(cfg, ids, G.epx.workspace_for(cfg, "cuda:0"), lay)
+        at = lay.token_row.view(-1)[T // 2].item()
         x = normal(T, T, n_in)
-        x[T // 2] = x1[0]
+        x[at] = x1[0]
         y, yq, gx = filled(T, n_out), filled(T, n_out), filled(T, n_out)
-        G.epx.ep_expert_gemm(cfg, lay, x, w, y)
-        G.epx.ep_expert_gemm_nvfp4(cfg, lay, x, codes, scales, rowscale, yq)
-        G.epx.ep_expert_gemm_bwd_x(cfg, lay, x, w.transpose(1, 2).contiguous(), gx)
-        seen.append([v[T // 2].view(torch.int16).cpu() for v in (y, yq, gx)])
+        we, qe = w.repeat(E, 1, 1), [v.repeat(E, *[1] * (v.dim() - 1)) for v in (codes, scales, rowscale)]
+        G.epx.ep_expert_gemm(cfg, lay, x, we, y)
+        G.epx.ep_expert_gemm_nvfp4(cfg, lay, x, *qe, yq)
+        G.epx.ep_expert_gemm_bwd_x(cfg, lay, x, we.transpose(1, 2).contiguous(), gx)
+        seen.append([v[at].view(torch.int16).cpu() for v in (y, yq, gx)])
     for other in seen[1:]:
         for a, b in zip(seen[0], other):
             assert torch.equal(a, b)
