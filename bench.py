@@ -29,6 +29,7 @@ from __future__ import annotations
 
 import argparse
 import dataclasses
+import gc
 import hashlib
 import json
 import os
@@ -280,6 +281,9 @@ def main() -> int:
 
     def time_steps(launch):
         """(wall ms, event ms) per step of args.steps launches, between two syncs."""
+        # A full collection of the interpreter's objects takes about 25 ms, and
+        # falls into the timed steps or not by how many were made before.
+        gc.collect()
         torch.cuda.synchronize()
         t0 = time.perf_counter()
         start.record(stream)
