@@ -22,8 +22,10 @@ constexpr int kOutside = 0x7FFFFFF0;                       // an offset past eve
 // are the same in all lanes.  Written out, because the compiler waits for every
 // load in flight (vmcnt 0) before any LDS read that follows its builtin.
 // Nothing waits for this load by itself: whoever reads the LDS bytes waits for
-// vmcnt first.  (m0 holds the LDS address; one wait state between its write
-// and the load.)
+// vmcnt first.  The compiler puts no wait states before an instruction in here:
+// an SGPR that a vector instruction wrote (uniform() is one) may be read by a
+// memory instruction 5 wait states later at the earliest, m0, which holds the
+// LDS address, 1 later.  The write of m0 is one, s_nop 3 four.
 typedef int32_t i32x4 __attribute__((ext_vector_type(4)));
 template <int BYTES>
 __device__ __forceinline__ void load_to_lds(const void* base, int32_t bytes, const void* lds, int32_t voff,
@@ -34,15 +36,15 @@ __device__ __forceinline__ void load_to_lds(const void* base, int32_t bytes, con
                       kBufferWord3};
     const uint32_t to = uniform((uint32_t)(uintptr_t)(EPX_LDS const void*)lds);
     if constexpr (BYTES == 16)
-        asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds" ::"s"(to), "v"(voff),
+        asm volatile("s_mov_b32 m0, %0\n\ts_nop 3\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds" ::"s"(to), "v"(voff),
                      "s"(rs), "s"(soff)
                      : "memory");
     else if constexpr (BYTES == 4)
-        asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, %3 offen lds" ::"s"(to), "v"(voff),
+        asm volatile("s_mov_b32 m0, %0\n\ts_nop 3\n\tbuffer_load_dword %1, %2, %3 offen lds" ::"s"(to), "v"(voff),
                      "s"(rs), "s"(soff)
                      : "memory");
     else
-        asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_ubyte %1, %2, %3 offen lds" ::"s"(to), "v"(voff),
+        asm volatile("s_mov_b32 m0, %0\n\ts_nop 3\n\tbuffer_load_ubyte %1, %2, %3 offen lds" ::"s"(to), "v"(voff),
                      "s"(rs), "s"(soff)
                      : "memory");
 #endif
