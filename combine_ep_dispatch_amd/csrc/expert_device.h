@@ -25,8 +25,12 @@ constexpr int kOutside = 0x7FFFFFF0;                       // an offset past eve
 // vmcnt first.  The compiler puts no wait states before an instruction in here:
 // an SGPR that a vector instruction wrote (uniform() is one) may be read by a
 // memory instruction 5 wait states later at the earliest, m0, which holds the
-// LDS address, 1 later.  The write of m0 is one, s_nop 3 four.
+// LDS address, 1 later.  The write of m0 is one, s_nop 3 four.  m0 is declared as
+// written: the compiler warns that it is reserved, but otherwise takes a value of
+// its own there for unchanged.
 typedef int32_t i32x4 __attribute__((ext_vector_type(4)));
+#pragma clang diagnostic push
+#pragma clang diagnostic ignored "-Winline-asm"
 template <int BYTES>
 __device__ __forceinline__ void load_to_lds(const void* base, int32_t bytes, const void* lds, int32_t voff,
                                             int32_t soff) {
@@ -38,17 +42,18 @@ __device__ __forceinline__ void load_to_lds(const void* base, int32_t bytes, con
     if constexpr (BYTES == 16)
         asm volatile("s_mov_b32 m0, %0\n\ts_nop 3\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds" ::"s"(to), "v"(voff),
                      "s"(rs), "s"(soff)
-                     : "memory");
+                     : "memory", "m0");
     else if constexpr (BYTES == 4)
         asm volatile("s_mov_b32 m0, %0\n\ts_nop 3\n\tbuffer_load_dword %1, %2, %3 offen lds" ::"s"(to), "v"(voff),
                      "s"(rs), "s"(soff)
-                     : "memory");
+                     : "memory", "m0");
     else
         asm volatile("s_mov_b32 m0, %0\n\ts_nop 3\n\tbuffer_load_ubyte %1, %2, %3 offen lds" ::"s"(to), "v"(voff),
                      "s"(rs), "s"(soff)
-                     : "memory");
+                     : "memory", "m0");
 #endif
 }
+#pragma clang diagnostic pop
 
 // A group's rows in the receive buffers, whatever the layout holds: [first,
 // first + rows) lies inside [0, R).

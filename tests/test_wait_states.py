@@ -1,7 +1,8 @@
-"""Wait states around the loads to LDS that the experts' products issue from
-inline assembly: the compiler inserts the waits that the hardware needs between
-its own instructions, not before one inside an asm block.  The sources are
-compiled to assembly and read; nothing runs on a GPU."""
+"""What the loads to LDS that the experts' products issue from inline assembly
+owe the compiler: it inserts the wait states that the hardware needs between its
+own instructions, not before one inside an asm block, and takes M0 for unchanged
+unless the block says otherwise.  Sources are compiled to assembly and read;
+nothing runs on a GPU."""
 
 import os
 import re
@@ -70,17 +71,20 @@ def test_the_reader_sees_short_waits():
     assert short_waits("\tv_cmp_gt_i32_e64 s[8:9], v0, v1\n\tbuffer_load_dword v0, s[4:7], s10 offen lds\n") == ([], 1)
 
 
+def compiled(source, out):
+    """The device assembly of a source, as the library's build compiles it."""
+    subprocess.run([build.hipcc(), *build.compile_flags(), "-S", "--cuda-device-only", "-o", out, source], check=True,
+                   capture_output=True)
+    with open(out) as f:
+        return f.read()
+
+
 @pytest.fixture(scope="module")
 def assembly(tmp_path_factory):
-    """The device assembly of each source, as the library's build compiles it."""
     at = tmp_path_factory.mktemp("assembly")
 
     def one(name):
-        out = str(at / f"{name}.s")
-        subprocess.run([build.hipcc(), *build.compile_flags(), "-S", "--cuda-device-only", "-o", out,
-                        os.path.join(build.CSRC, f"{name}.hip")], check=True, capture_output=True)
-        with open(out) as f:
-            return f.read()
+        return compiled(os.path.join(build.CSRC, f"{name}.hip"), str(at / f"{name}.s"))
 
     with ThreadPoolExecutor(len(SOURCES)) as pool:
         return dict(zip(SOURCES, pool.map(one, SOURCES)))
@@ -91,3 +95,21 @@ def test_loads_to_lds_wait_for_their_descriptors(assembly, name):
     bad, loads = short_waits(assembly[name])
     assert loads > 50
     assert not bad
+
+
+def test_a_value_in_m0_is_written_again_behind_a_load(tmp_path):
+    """Two messages whose operand is m0, a load between them: m0 has to be set for
+    the second one too."""
+    source = tmp_path / "m0.hip"
+    source.write_text("""
+        #include "expert_device.h"
+        __global__ void k(const int* p, int n, int m) {
+            __shared__ int lds[64];
+            __builtin_amdgcn_s_sendmsg(1, m);
+            epx::load_to_lds<4>(p, n, lds, threadIdx.x * 4, 0);
+            __builtin_amdgcn_s_sendmsg(1, m);
+        }
+    """)
+    lines = compiled(str(source), str(tmp_path / "m0.s")).splitlines()
+    on = [line.split()[0] for line in lines if re.search(r"\bs_sendmsg\b|\bm0,|offen lds", line)]
+    assert on == ["s_mov_b32", "s_sendmsg", "s_mov_b32", "buffer_load_dword", "s_mov_b32", "s_sendmsg"]
