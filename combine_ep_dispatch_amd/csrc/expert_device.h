@@ -16,11 +16,12 @@ typedef uint32_t v4u __attribute__((ext_vector_type(4)));
 [[maybe_unused]] constexpr int kBufferWord3 = 0x00020000;  // buffer descriptor word 3: 32-bit data, raw addressing
 constexpr int kOutside = 0x7FFFFFF0;                       // an offset past every descriptor's end: loads zeros
 
-// BYTES (16, 4 or 1) a lane from offset voff + soff of a buffer of `bytes` bytes to
+// BYTES (16, 4 or 1) a lane from offset voff of a buffer of `bytes` bytes to
 // LDS: lane l's 16 at lds + 16 l, its 4 at lds + 4 l, its 1 as a word at
-// lds + 4 l; zeros for words past the buffer's end.  base, bytes, lds and soff
-// are the same in all lanes.  Written out, because the compiler waits for every
-// load in flight (vmcnt 0) before any LDS read that follows its builtin.
+// lds + 4 l; zeros for words past the buffer's end.  base, bytes and lds are the
+// same in all lanes.  The instruction's scalar offset stays 0: the range check
+// does not count it.  Written out, because the compiler waits for every load in
+// flight (vmcnt 0) before any LDS read that follows its builtin.
 // Nothing waits for this load by itself: whoever reads the LDS bytes waits for
 // vmcnt first.  The compiler puts no wait states before an instruction in here:
 // an SGPR that a vector instruction wrote (uniform() is one) may be read by a
@@ -32,24 +33,23 @@ typedef int32_t i32x4 __attribute__((ext_vector_type(4)));
 #pragma clang diagnostic push
 #pragma clang diagnostic ignored "-Winline-asm"
 template <int BYTES>
-__device__ __forceinline__ void load_to_lds(const void* base, int32_t bytes, const void* lds, int32_t voff,
-                                            int32_t soff) {
+__device__ __forceinline__ void load_to_lds(const void* base, int32_t bytes, const void* lds, int32_t voff) {
 #ifdef __HIP_DEVICE_COMPILE__
     const uint64_t p = reinterpret_cast<uint64_t>(base);
     const i32x4 rs = {(int32_t)uniform((uint32_t)p), (int32_t)uniform((uint32_t)(p >> 32) & 0xFFFFu), uniform(bytes),
                       kBufferWord3};
     const uint32_t to = uniform((uint32_t)(uintptr_t)(EPX_LDS const void*)lds);
     if constexpr (BYTES == 16)
-        asm volatile("s_mov_b32 m0, %0\n\ts_nop 3\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds" ::"s"(to), "v"(voff),
-                     "s"(rs), "s"(soff)
+        asm volatile("s_mov_b32 m0, %0\n\ts_nop 3\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(to), "v"(voff),
+                     "s"(rs)
                      : "memory", "m0");
     else if constexpr (BYTES == 4)
-        asm volatile("s_mov_b32 m0, %0\n\ts_nop 3\n\tbuffer_load_dword %1, %2, %3 offen lds" ::"s"(to), "v"(voff),
-                     "s"(rs), "s"(soff)
+        asm volatile("s_mov_b32 m0, %0\n\ts_nop 3\n\tbuffer_load_dword %1, %2, 0 offen lds" ::"s"(to), "v"(voff),
+                     "s"(rs)
                      : "memory", "m0");
     else
-        asm volatile("s_mov_b32 m0, %0\n\ts_nop 3\n\tbuffer_load_ubyte %1, %2, %3 offen lds" ::"s"(to), "v"(voff),
-                     "s"(rs), "s"(soff)
+        asm volatile("s_mov_b32 m0, %0\n\ts_nop 3\n\tbuffer_load_ubyte %1, %2, 0 offen lds" ::"s"(to), "v"(voff),
+                     "s"(rs)
                      : "memory", "m0");
 #endif
 }

@@ -69,7 +69,7 @@ struct RowsOperand {
     __device__ __forceinline__ void load(uint16_t* lds, int32_t l0, int j) const {
         const int w = uniform((int32_t)(threadIdx.x / kWave));
         load_to_lds<16>(base, records, lds + (w * kLoads + j) * 512,
-                    l0 + chunk[j % 2] * 8 < len ? voff[j] + l0 * 2 : kOutside, 0);
+                        l0 + chunk[j % 2] * 8 < len ? voff[j] + l0 * 2 : kOutside);
     }
     // Fragment of 16 rows from m0 on, values [32 kk, 32 kk + 32) of the step.
     static __device__ __forceinline__ bf16x8 fragment(const uint16_t* lds, int m0, int kk) {
@@ -112,7 +112,7 @@ struct ColsOperand {
     }
     __device__ __forceinline__ void load(uint16_t* lds, int32_t l0, int j) const {
         const int w = uniform((int32_t)(threadIdx.x / kWave));
-        load_to_lds<16>(base + (int64_t)l0 * ld, records(l0), lds + (w * kLoads + j) * 512, voff[j], 0);
+        load_to_lds<16>(base + (int64_t)l0 * ld, records(l0), lds + (w * kLoads + j) * 512, voff[j]);
     }
     static __device__ __forceinline__ bf16x8 fragment(const uint16_t* lds, int m0, int kk) {
         const int lane = threadIdx.x & (kWave - 1), i = lane % 16, q = lane / 16;

@@ -97,6 +97,14 @@ def test_loads_to_lds_wait_for_their_descriptors(assembly, name):
     assert not bad
 
 
+@pytest.mark.parametrize("name", SOURCES)
+def test_loads_to_lds_keep_their_offset_in_the_range_check(assembly, name):
+    """The check of an address against the buffer's size leaves the scalar offset
+    out: with one, a load past the buffer's last bytes is not caught."""
+    loads = re.findall(r"buffer_load_\w+ v\d+, s\[[\d:]+\], (\S+) offen lds", assembly[name])
+    assert len(loads) > 50 and set(loads) == {"0"}
+
+
 def test_a_value_in_m0_is_written_again_behind_a_load(tmp_path):
     """Two messages whose operand is m0, a load between them: m0 has to be set for
     the second one too."""
@@ -106,7 +114,7 @@ def test_a_value_in_m0_is_written_again_behind_a_load(tmp_path):
         __global__ void k(const int* p, int n, int m) {
             __shared__ int lds[64];
             __builtin_amdgcn_s_sendmsg(1, m);
-            epx::load_to_lds<4>(p, n, lds, threadIdx.x * 4, 0);
+            epx::load_to_lds<4>(p, n, lds, threadIdx.x * 4);
             __builtin_amdgcn_s_sendmsg(1, m);
         }
     """)
