@@ -26,6 +26,9 @@ The expert layer around the two, on the same layout:
     h = d.linear(recv, w1)                   # [R, 2 * inter], differentiable in both
     act = d.swiglu(h, probs)                 # weights applied to the rows; differentiable in both
     y = d.combine(d.linear(act, w2), None)
+
+The backward passes are library calls without gradients of their own: a second
+derivative raises.
 """
 
 from __future__ import annotations
@@ -33,6 +36,7 @@ from __future__ import annotations
 from typing import Optional
 
 import torch
+from torch.autograd.function import once_differentiable
 
 from . import (EpConfig, Layout, RouteConfig, ep_combine, ep_combine_bwd, ep_combine_bwd_probs, ep_dispatch,
                ep_dispatch_bwd, ep_dispatch_layout, ep_dispatch_with_layout, ep_expert_gemm, ep_expert_gemm_bwd_w,
@@ -55,6 +59,7 @@ class _Dispatch(torch.autograd.Function):
         return recv
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, grad_recv):
         cfg = ctx.cfg
         gx = torch.empty(cfg.num_tokens, cfg.hidden, dtype=torch.bfloat16, device=grad_recv.device)
@@ -75,6 +80,7 @@ class _Combine(torch.autograd.Function):
         return y
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, grad_y):
         cfg, layout = ctx.cfg, ctx.layout
         eo, p = ctx.saved_tensors
@@ -101,6 +107,7 @@ class _Gate(torch.autograd.Function):
         return ids, probs
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, _, grad_probs):
         logits, ids = ctx.saved_tensors
         grad = torch.empty_like(logits)
@@ -119,6 +126,7 @@ class _Linear(torch.autograd.Function):
         return y
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, grad_y):
         x, w = ctx.saved_tensors
         gy = grad_y.to(torch.bfloat16).contiguous()
@@ -145,6 +153,7 @@ class _Swiglu(torch.autograd.Function):
         return act
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, grad_act):
         h, p = ctx.saved_tensors
         ga = grad_act.to(torch.bfloat16).contiguous()
