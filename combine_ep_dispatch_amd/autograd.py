@@ -27,22 +27,56 @@ The expert layer around the two, on the same layout:
     act = d.swiglu(h, probs)                 # weights applied to the rows; differentiable in both
     y = d.combine(d.linear(act, w2), None)
 
-The backward passes are library calls without gradients of their own: a second
-derivative raises.
+The backward passes are library calls without gradients of their own: under
+create_graph the first derivatives can be had, differentiating them raises.
 """
 
 from __future__ import annotations
 
+import functools
 from typing import Optional
 
 import torch
-from torch.autograd.function import once_differentiable
 
 from . import (EpConfig, Layout, RouteConfig, ep_combine, ep_combine_bwd, ep_combine_bwd_probs, ep_dispatch,
                ep_dispatch_bwd, ep_dispatch_layout, ep_dispatch_with_layout, ep_expert_gemm, ep_expert_gemm_bwd_w,
                ep_expert_gemm_bwd_x, ep_query, ep_route, ep_route_bwd, ep_swiglu, ep_swiglu_bwd, workspace_for)
 
 __all__ = ["EpDispatcher"]
+
+
+class _Refuse(torch.autograd.Function):
+    """The first n tensors as they are, depending on all of them, with no way back."""
+
+    @staticmethod
+    def forward(ctx, n, *tensors):
+        return tuple(t.view_as(t) for t in tensors[:n])
+
+    @staticmethod
+    def backward(ctx, *grads):
+        raise RuntimeError("EpDispatcher's operators cannot be differentiated twice")
+
+
+def _first_only(backward):
+    """A backward pass whose results raise where they are differentiated.  They
+    depend on the incoming gradients and the saved inputs, so that every path to
+    a leaf meets the error (once_differentiable's leads nowhere: torch.autograd.grad
+    passes it by where another term reaches the leaf)."""
+
+    @functools.wraps(backward)
+    def wrapped(ctx, *grads):
+        with torch.no_grad():
+            out = backward(ctx, *grads)
+        if not torch.is_grad_enabled():
+            return out
+        sources = [t for t in (*grads, *ctx.saved_tensors) if t is not None and t.requires_grad]
+        if not sources:
+            return out
+        given = [t for t in out if t is not None]
+        refusing = iter(_Refuse.apply(len(given), *given, *sources))
+        return tuple(None if t is None else next(refusing) for t in out)
+
+    return wrapped
 
 
 class _Dispatch(torch.autograd.Function):
@@ -59,7 +93,7 @@ class _Dispatch(torch.autograd.Function):
         return recv
 
     @staticmethod
-    @once_differentiable
+    @_first_only
     def backward(ctx, grad_recv):
         cfg = ctx.cfg
         gx = torch.empty(cfg.num_tokens, cfg.hidden, dtype=torch.bfloat16, device=grad_recv.device)
@@ -71,16 +105,14 @@ class _Combine(torch.autograd.Function):
     @staticmethod
     def forward(ctx, expert_out, probs, cfg, layout):
         y = torch.empty(cfg.num_tokens, cfg.hidden, dtype=torch.bfloat16, device=expert_out.device)
-        eo = expert_out.contiguous()
-        p = None if probs is None else probs.contiguous().float()
-        ep_combine(cfg, layout, eo.view(-1), None if p is None else p.view(-1), y.view(-1))
+        ep_combine(cfg, layout, expert_out.view(-1), None if probs is None else probs.view(-1), y.view(-1))
         ctx.cfg, ctx.layout = cfg, layout
         ctx.has_probs = probs is not None
-        ctx.save_for_backward(eo, p if p is not None else torch.empty(0, device=eo.device))
+        ctx.save_for_backward(expert_out, probs if ctx.has_probs else torch.empty(0, device=expert_out.device))
         return y
 
     @staticmethod
-    @once_differentiable
+    @_first_only
     def backward(ctx, grad_y):
         cfg, layout = ctx.cfg, ctx.layout
         eo, p = ctx.saved_tensors
@@ -97,7 +129,6 @@ class _Combine(torch.autograd.Function):
 class _Gate(torch.autograd.Function):
     @staticmethod
     def forward(ctx, logits, bias, token_mask, cfg, route):
-        logits = logits.contiguous()
         ids = torch.empty(cfg.num_tokens, cfg.top_k, dtype=torch.int32, device=logits.device)
         probs = torch.empty(cfg.num_tokens, cfg.top_k, dtype=torch.float32, device=logits.device)
         ep_route(cfg, route, logits, ids, probs, bias=bias, token_mask=token_mask)
@@ -107,7 +138,7 @@ class _Gate(torch.autograd.Function):
         return ids, probs
 
     @staticmethod
-    @once_differentiable
+    @_first_only
     def backward(ctx, _, grad_probs):
         logits, ids = ctx.saved_tensors
         grad = torch.empty_like(logits)
@@ -118,7 +149,6 @@ class _Gate(torch.autograd.Function):
 class _Linear(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, w, cfg, layout):
-        x, w = x.contiguous(), w.contiguous()
         y = torch.zeros(cfg.recv_rows, w.shape[1], dtype=torch.bfloat16, device=x.device)
         ep_expert_gemm(cfg, layout, x, w, y)
         ctx.cfg, ctx.layout = cfg, layout
@@ -126,7 +156,7 @@ class _Linear(torch.autograd.Function):
         return y
 
     @staticmethod
-    @once_differentiable
+    @_first_only
     def backward(ctx, grad_y):
         x, w = ctx.saved_tensors
         gy = grad_y.to(torch.bfloat16).contiguous()
@@ -143,17 +173,15 @@ class _Linear(torch.autograd.Function):
 class _Swiglu(torch.autograd.Function):
     @staticmethod
     def forward(ctx, h, probs, cfg, layout):
-        h = h.contiguous()
-        p = None if probs is None else probs.contiguous().float()
         act = torch.zeros(h.shape[0], h.shape[1] // 2, dtype=torch.bfloat16, device=h.device)
-        ep_swiglu(cfg, layout, h, p, act)
+        ep_swiglu(cfg, layout, h, probs, act)
         ctx.cfg, ctx.layout = cfg, layout
         ctx.has_probs = probs is not None
-        ctx.save_for_backward(h, p if p is not None else torch.empty(0, device=h.device))
+        ctx.save_for_backward(h, probs if ctx.has_probs else torch.empty(0, device=h.device))
         return act
 
     @staticmethod
-    @once_differentiable
+    @_first_only
     def backward(ctx, grad_act):
         h, p = ctx.saved_tensors
         ga = grad_act.to(torch.bfloat16).contiguous()
@@ -163,6 +191,10 @@ class _Swiglu(torch.autograd.Function):
             gp = torch.empty(ctx.cfg.num_tokens, ctx.cfg.top_k, dtype=torch.float32, device=h.device)
         ep_swiglu_bwd(ctx.cfg, ctx.layout, h, p if ctx.has_probs else None, ga, gh, gp)
         return gh, gp, None, None
+
+
+def _weights(probs: Optional[torch.Tensor]) -> Optional[torch.Tensor]:
+    return None if probs is None else probs.contiguous().float()
 
 
 class EpDispatcher:
@@ -199,23 +231,23 @@ class EpDispatcher:
 
     def combine(self, expert_out: torch.Tensor, probs: Optional[torch.Tensor]) -> torch.Tensor:
         """[R, H] bf16 expert outputs -> [T, H] bf16, weighted by probs [T, K] (or 1)."""
-        return _Combine.apply(expert_out, probs, self.cfg, self.layout)
+        return _Combine.apply(expert_out.contiguous(), _weights(probs), self.cfg, self.layout)
 
     def gate(self, logits: torch.Tensor, route: RouteConfig, bias: Optional[torch.Tensor] = None,
              token_mask: Optional[torch.Tensor] = None):
         """[T, E] logits (float32 or bfloat16) -> topk_ids int32 [T, K] and probs
         float32 [T, K], differentiable in the logits."""
-        return _Gate.apply(logits, bias, token_mask, self.cfg, route)
+        return _Gate.apply(logits.contiguous(), bias, token_mask, self.cfg, route)
 
     def linear(self, rows: torch.Tensor, w: torch.Tensor) -> torch.Tensor:
         """[R, in] bf16 receive rows times their experts' weights bf16
         [E (+1 shared), out, in] -> [R, out]; rows no slot owns are zero."""
-        return _Linear.apply(rows, w, self.cfg, self.layout)
+        return _Linear.apply(rows.contiguous(), w.contiguous(), self.cfg, self.layout)
 
     def swiglu(self, h: torch.Tensor, probs: Optional[torch.Tensor]) -> torch.Tensor:
         """[R, 2*inter] bf16 (gate, then up) -> [R, inter], each row times its
         slot's probs [T, K] (or 1); rows no slot owns are zero."""
-        return _Swiglu.apply(h, probs, self.cfg, self.layout)
+        return _Swiglu.apply(h.contiguous(), _weights(probs), self.cfg, self.layout)
 
     def tokens_per_expert(self) -> torch.Tensor:
         """Routed rows per group [S, G] (the shared group included)."""

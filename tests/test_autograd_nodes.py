@@ -80,7 +80,7 @@ def test_second_derivatives_are_refused(plain, name):
     is an error, not the derivative of the other terms alone."""
     leaf, result = nodes()[name]
     first, = torch.autograd.grad(result().float().square().sum() + leaf.float().square().sum(), leaf, create_graph=True)
-    with pytest.raises(RuntimeError, match="once_differentiable"):
+    with pytest.raises(RuntimeError, match="differentiated twice"):
         torch.autograd.grad(first.float().sum(), leaf)
 
 
@@ -90,3 +90,31 @@ def test_first_derivatives_run_with_a_graph(plain, name):
     once, = torch.autograd.grad(result().float().sum(), leaf)
     graph, = torch.autograd.grad(result().float().sum(), leaf, create_graph=True)
     assert torch.isfinite(once).all() and once.abs().max() > 0 and torch.equal(once, graph)
+
+
+def dispatcher():
+    d = object.__new__(ag.EpDispatcher)
+    d.cfg = epx.EpConfig(num_tokens=T, hidden=H, num_experts=E, num_segments=1, top_k=K, recv_rows=T)
+    d.layout, d.workspace, d.device = None, None, torch.device("cpu")
+    return d
+
+
+def test_strided_inputs(plain):
+    """Inputs in another order than the calls take: the same results and first
+    derivatives, and the second ones refused."""
+    gen = torch.Generator().manual_seed(2)
+    d = dispatcher()
+    leaves = [torch.randn(*s, generator=gen).requires_grad_() for s in ((E, T), (2 * INTER, T), (H, T), (H, INTER, E), (K, T))]
+    z, h, x, w, p = leaves
+    turned = [z.t(), h.t().bfloat16(), x.t().bfloat16(), w.permute(2, 1, 0).bfloat16(), p.t().double()]
+    outs = []
+    for z, h, x, w, p in (turned, [v.contiguous() for v in turned]):
+        out = [d.gate(z, epx.RouteConfig())[1], d.linear(x, w), d.swiglu(h, p), d.combine(x, p)]
+        total = sum(v.float().square().sum() for v in out) + sum(v.square().sum() for v in leaves)
+        first = torch.autograd.grad(total, leaves, create_graph=True)
+        outs.append(out + list(first))
+        for g, leaf in zip(first, leaves):
+            with pytest.raises(RuntimeError, match="differentiated twice"):
+                torch.autograd.grad(g.sum(), leaf, retain_graph=True)
+    for a, b in zip(*outs):
+        assert torch.equal(a, b)
