@@ -188,15 +188,15 @@ __device__ __forceinline__ int exact_group_rank(const TopkArgs& a, const float (
 // The choice in full: keys of 64 bits where there is a bias, groups of any
 // size.  Lane k gets the k-th expert (-1: none) and its logit.
 template <int VPL>
-__device__ __forceinline__ void choose_exactly(const TopkArgs& a, const float (&z)[VPL], float zmax, int lane, double* s_key,
-                               int32_t& my_id, float& my_z) {
+__device__ __forceinline__ void choose_exactly(const TopkArgs& a, bool biased, const float (&z)[VPL], float zmax, int lane,
+                                               double* s_key, int32_t& my_id, float& my_z) {
     double key[VPL];
-    const double total = a.bias != nullptr && !a.sigmoid ? exact_total<VPL>(a, z, zmax, lane) : 1.0;
+    const double total = biased && !a.sigmoid ? exact_total<VPL>(a, z, zmax, lane) : 1.0;
 #pragma unroll
     for (int i = 0; i < VPL; ++i) {
         const int32_t e = lane * VPL + i;
         key[i] = z[i];
-        if (a.bias != nullptr && e < a.E) key[i] = exact_key(a, z[i], zmax, total, e);
+        if (biased && e < a.E) key[i] = exact_key(a, z[i], zmax, total, e);
         if (!(z[i] > -INFINITY) || e >= a.E) key[i] = -INFINITY;
     }
     if (a.groups > 1) {
@@ -211,7 +211,7 @@ __device__ __forceinline__ void choose_exactly(const TopkArgs& a, const float (&
                 const double k = s_key[lane * per + j];
                 merge(b0, b1, k, (double)-INFINITY);
             }
-            gkey = a.bias != nullptr && per > 1 ? b0 + b1 : b0;
+            gkey = biased && per > 1 ? b0 + b1 : b0;
         }
         int before = 0;  // groups that come before this one
         for (int g = 0; g < a.groups; ++g) {
@@ -286,13 +286,16 @@ __global__ __launch_bounds__(kTopkThreads) void k_route(TopkArgs a) {
         for (int i = 0; i < VPL; ++i) sum += expf(z[i] - zmax);
         total = wave_sum(sum);
     }
+    // Softmax over a NaN or +infinity leaves no scores to add a bias to (its sum is
+    // NaN): the choice goes by the logits then, and the weights show the NaN.
+    const bool biased = a.bias != nullptr && total == total;
     // keys, in fp32; unavailable experts have -infinity
     float key[VPL];
     float largest = 0.0f;
 #pragma unroll
     for (int i = 0; i < VPL; ++i) {
         key[i] = z[i];
-        if (a.bias != nullptr) {
+        if (biased) {
             const int32_t e = lane * VPL + i;
             const float s = a.sigmoid ? __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-1.44269504f * z[i]))
                                       : expf(z[i] - zmax) / total;
@@ -301,7 +304,6 @@ __global__ __launch_bounds__(kTopkThreads) void k_route(TopkArgs a) {
         }
         if (!(z[i] > -INFINITY)) key[i] = -INFINITY;
     }
-    const bool biased = a.bias != nullptr;
     float off = 0.0f;
     if (biased) off = 2.0f * key_error(a, __uint_as_float(wave_max(__float_as_uint(largest))), VPL);
 
@@ -401,7 +403,7 @@ __global__ __launch_bounds__(kTopkThreads) void k_route(TopkArgs a) {
             }
         }
     }
-    if (!sure) choose_exactly<VPL>(a, z, zmax, lane, s_key[w], my_id, my_z);
+    if (!sure) choose_exactly<VPL>(a, biased, z, zmax, lane, s_key[w], my_id, my_z);
     float q = 0.0f;
     if (my_id >= 0) q = a.sigmoid ? 1.0f / (1.0f + expf(-my_z)) : expf(my_z - zmax) / total;
     float p = q;

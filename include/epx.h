@@ -468,8 +468,9 @@ typedef struct ep_route_t {
  * logits and grad_logits are 16-byte aligned.
  * An expert with a logit of -infinity or NaN is never chosen; a token with
  * fewer than K experts to choose from has id -1 and weight 0 in its last
- * slots.  Softmax sums over every expert of the token (a NaN or +infinity
- * among its logits makes its weights NaN; the ids stay valid).  bias is finite.
+ * slots.  Softmax sums over every expert of the token: a NaN or +infinity
+ * among its logits makes its weights NaN, and its experts are chosen as without
+ * a bias.  bias is finite.
  * Only T, E, K (and their validity) of cfg are used.
  */
 int ep_route(const ep_cfg_t* cfg, const ep_route_t* route, const void* logits, const float* bias,

@@ -46,3 +46,32 @@ def test_operands_that_end_with_their_memory(G, name, n_in):  # noqa: F811
 
     for got, want in zip(run(*map(at_the_end, (x, gy, w, *q))), run(x, gy, w, *q)):
         assert torch.equal(got, want)
+
+
+# ---------------------------------------------------------------------------
+# Router
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("E,groups,top", [(64, 1, 1), (64, 8, 3), (96, 4, 2), (256, 8, 4)])
+def test_softmax_over_a_nan_or_infinity_shows_in_the_weights(G, E, groups, top):  # noqa: F811
+    """A token with a NaN or +infinity among its logits gets K experts, chosen by the
+    logits with a bias too, and NaN for their weights: it is not left out."""
+    T, K = 33, 6
+    rng = np.random.default_rng(E)
+    z = rng.standard_normal((T, E)).astype(np.float32)
+    z[::3, 5] = np.nan
+    z[1::3, 7] = np.inf
+    cfg = G.epx.EpConfig(num_tokens=T, hidden=8, num_experts=E, num_segments=1, top_k=K)
+    logits, bias = torch.from_numpy(z).to("cuda:0"), normal(1, E, dtype=torch.float32)
+    r = G.epx.RouteConfig(num_groups=groups, top_groups=top)
+    seen = []
+    for b in (bias, None):
+        ids, p = torch.full((T, K), -7, dtype=torch.int32, device="cuda:0"), torch.zeros(T, K, device="cuda:0")
+        G.epx.ep_route(cfg, r, logits, ids, p, bias=b)
+        seen.append((ids.cpu().numpy(), p.cpu().numpy()))
+    off = np.arange(T) % 3 < 2
+    for ids, p in seen:
+        assert ((ids >= 0) & (ids < E)).all()
+        assert np.isnan(p[off]).all() and np.isfinite(p[~off]).all()
+        assert (ids[1::3, 0] == 7).all() and not (ids[::3] == 5).any()
+    np.testing.assert_array_equal(seen[0][0][off], seen[1][0][off])
+    assert (seen[0][0][~off] != seen[1][0][~off]).any()
