@@ -45,6 +45,17 @@ from . import (EpConfig, Layout, RouteConfig, ep_combine, ep_combine_bwd, ep_com
 __all__ = ["EpDispatcher"]
 
 
+def _rows(t: torch.Tensor) -> torch.Tensor:
+    """t as the calls take it, contiguous and 16-byte aligned: itself or a copy (a
+    slice of a batch, or of a flat buffer, may begin off 16 bytes)."""
+    t = t.contiguous()
+    return t if t.data_ptr() % 16 == 0 else t.clone()
+
+
+def _weights(probs: Optional[torch.Tensor]) -> Optional[torch.Tensor]:
+    return None if probs is None else probs.contiguous().float()
+
+
 class _Refuse(torch.autograd.Function):
     """The first n tensors as they are, depending on all of them, with no way back."""
 
@@ -86,9 +97,9 @@ class _Dispatch(torch.autograd.Function):
         # decode-sized batches)
         recv = torch.zeros(cfg.recv_rows, cfg.hidden, dtype=torch.bfloat16, device=x.device)
         if topk_ids is None:
-            ep_dispatch(cfg, layout, x.contiguous().view(-1), recv.view(-1))
+            ep_dispatch(cfg, layout, x.view(-1), recv.view(-1))
         else:
-            ep_dispatch_with_layout(cfg, topk_ids, workspace, layout, x.contiguous().view(-1), recv.view(-1))
+            ep_dispatch_with_layout(cfg, topk_ids, workspace, layout, x.view(-1), recv.view(-1))
         ctx.cfg, ctx.layout = cfg, layout
         return recv
 
@@ -97,7 +108,7 @@ class _Dispatch(torch.autograd.Function):
     def backward(ctx, grad_recv):
         cfg = ctx.cfg
         gx = torch.empty(cfg.num_tokens, cfg.hidden, dtype=torch.bfloat16, device=grad_recv.device)
-        ep_dispatch_bwd(cfg, ctx.layout, grad_recv.to(torch.bfloat16).contiguous().view(-1), gx.view(-1))
+        ep_dispatch_bwd(cfg, ctx.layout, _rows(grad_recv.to(torch.bfloat16)).view(-1), gx.view(-1))
         return gx, None, None, None, None
 
 
@@ -116,7 +127,7 @@ class _Combine(torch.autograd.Function):
     def backward(ctx, grad_y):
         cfg, layout = ctx.cfg, ctx.layout
         eo, p = ctx.saved_tensors
-        gy = grad_y.to(torch.bfloat16).contiguous()
+        gy = _rows(grad_y.to(torch.bfloat16))
         g_out = torch.zeros(cfg.recv_rows, cfg.hidden, dtype=torch.bfloat16, device=gy.device)
         ep_combine_bwd(cfg, layout, gy.view(-1), p.view(-1) if ctx.has_probs else None, g_out.view(-1))
         g_probs = None
@@ -159,7 +170,7 @@ class _Linear(torch.autograd.Function):
     @_first_only
     def backward(ctx, grad_y):
         x, w = ctx.saved_tensors
-        gy = grad_y.to(torch.bfloat16).contiguous()
+        gy = _rows(grad_y.to(torch.bfloat16))
         gx = gw = None
         if ctx.needs_input_grad[0]:
             gx = torch.zeros_like(x)
@@ -184,17 +195,13 @@ class _Swiglu(torch.autograd.Function):
     @_first_only
     def backward(ctx, grad_act):
         h, p = ctx.saved_tensors
-        ga = grad_act.to(torch.bfloat16).contiguous()
+        ga = _rows(grad_act.to(torch.bfloat16))
         gh = torch.zeros_like(h)
         gp = None
         if ctx.has_probs and ctx.needs_input_grad[1]:
             gp = torch.empty(ctx.cfg.num_tokens, ctx.cfg.top_k, dtype=torch.float32, device=h.device)
         ep_swiglu_bwd(ctx.cfg, ctx.layout, h, p if ctx.has_probs else None, ga, gh, gp)
         return gh, gp, None, None
-
-
-def _weights(probs: Optional[torch.Tensor]) -> Optional[torch.Tensor]:
-    return None if probs is None else probs.contiguous().float()
 
 
 class EpDispatcher:
@@ -222,32 +229,32 @@ class EpDispatcher:
         the same call (ep_dispatch_with_layout) into a new layout that later
         calls use, as route() would."""
         if topk_ids is None:
-            return _Dispatch.apply(x, self.cfg, self.layout)
+            return _Dispatch.apply(_rows(x), self.cfg, self.layout)
         layout = Layout.empty(self.cfg, self.device)
         ids = topk_ids.to(torch.int32).contiguous().view(-1)
-        recv = _Dispatch.apply(x, self.cfg, layout, ids, self.workspace)
+        recv = _Dispatch.apply(_rows(x), self.cfg, layout, ids, self.workspace)
         self.layout = layout
         return recv
 
     def combine(self, expert_out: torch.Tensor, probs: Optional[torch.Tensor]) -> torch.Tensor:
         """[R, H] bf16 expert outputs -> [T, H] bf16, weighted by probs [T, K] (or 1)."""
-        return _Combine.apply(expert_out.contiguous(), _weights(probs), self.cfg, self.layout)
+        return _Combine.apply(_rows(expert_out), _weights(probs), self.cfg, self.layout)
 
     def gate(self, logits: torch.Tensor, route: RouteConfig, bias: Optional[torch.Tensor] = None,
              token_mask: Optional[torch.Tensor] = None):
         """[T, E] logits (float32 or bfloat16) -> topk_ids int32 [T, K] and probs
         float32 [T, K], differentiable in the logits."""
-        return _Gate.apply(logits.contiguous(), bias, token_mask, self.cfg, route)
+        return _Gate.apply(_rows(logits), bias, token_mask, self.cfg, route)
 
     def linear(self, rows: torch.Tensor, w: torch.Tensor) -> torch.Tensor:
         """[R, in] bf16 receive rows times their experts' weights bf16
         [E (+1 shared), out, in] -> [R, out]; rows no slot owns are zero."""
-        return _Linear.apply(rows.contiguous(), w.contiguous(), self.cfg, self.layout)
+        return _Linear.apply(_rows(rows), _rows(w), self.cfg, self.layout)
 
     def swiglu(self, h: torch.Tensor, probs: Optional[torch.Tensor]) -> torch.Tensor:
         """[R, 2*inter] bf16 (gate, then up) -> [R, inter], each row times its
         slot's probs [T, K] (or 1); rows no slot owns are zero."""
-        return _Swiglu.apply(h.contiguous(), _weights(probs), self.cfg, self.layout)
+        return _Swiglu.apply(_rows(h), _weights(probs), self.cfg, self.layout)
 
     def tokens_per_expert(self) -> torch.Tensor:
         """Routed rows per group [S, G] (the shared group included)."""

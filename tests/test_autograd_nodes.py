@@ -118,3 +118,32 @@ def test_strided_inputs(plain):
                 torch.autograd.grad(g.sum(), leaf, retain_graph=True)
     for a, b in zip(*outs):
         assert torch.equal(a, b)
+
+
+def test_inputs_and_gradients_off_16_bytes(plain):
+    """Contiguous slices that begin off 16 bytes, and gradients that arrive as such,
+    reach the calls as aligned copies."""
+    gen = torch.Generator().manual_seed(3)
+    d = dispatcher()
+
+    def flat(*shape, dtype=torch.bfloat16):  # the last values of a buffer one value longer
+        t = torch.randn(torch.Size(shape).numel() + 1, generator=gen).to(dtype).requires_grad_()
+        out = t[1:].view(*shape)
+        assert out.is_contiguous() and out.data_ptr() % 16 != 0
+        return out
+
+    z, h, x, w = flat(T, E, dtype=torch.float32), flat(T, 2 * INTER), flat(T, H), flat(E, INTER, H)
+    p = flat(T, K, dtype=torch.float32)
+    outs = [d.gate(z, epx.RouteConfig())[1], d.linear(x, w), d.swiglu(h, p), d.combine(x, p), d.dispatch(x)]
+    for out in outs:
+        gy = torch.randn(out.numel() + 1, generator=gen).to(out.dtype)[1:].view(out.shape)
+        assert gy.data_ptr() % 16 != 0
+        out.backward(gy)
+    needs = {"ep_route": (2,), "ep_route_bwd": (2, 5), "ep_swiglu": (2, 4), "ep_swiglu_bwd": (2, 4, 5), "ep_expert_gemm": (2, 3, 4),
+             "ep_expert_gemm_bwd_x": (2, 3, 4), "ep_expert_gemm_bwd_w": (2, 3, 4), "ep_dispatch": (2, 3),
+             "ep_dispatch_bwd": (2, 3), "ep_combine": (2, 4), "ep_combine_bwd": (2, 4), "ep_combine_bwd_probs": (2, 3)}
+    assert set(plain) == set(needs)
+    for name, at in needs.items():
+        for args, _ in plain[name]:
+            for i in at:
+                assert args[i].is_contiguous() and args[i].data_ptr() % 16 == 0, (name, i)

@@ -75,3 +75,23 @@ def test_softmax_over_a_nan_or_infinity_shows_in_the_weights(G, E, groups, top):
         assert (ids[1::3, 0] == 7).all() and not (ids[::3] == 5).any()
     np.testing.assert_array_equal(seen[0][0][off], seen[1][0][off])
     assert (seen[0][0][~off] != seen[1][0][~off]).any()
+
+
+def test_gate_of_a_slice_that_begins_off_16_bytes(G):  # noqa: F811
+    """A batch's logits from its second token on, 37 experts wide: the results and
+    gradients of an aligned copy."""
+    from combine_ep_dispatch_amd.autograd import EpDispatcher
+
+    T, E, K = 9, 37, 3
+    d = EpDispatcher(G.epx.EpConfig(num_tokens=T, hidden=8, num_experts=E, num_segments=1, top_k=K), "cuda:0")
+    for dtype in (torch.float32, torch.bfloat16):
+        batch, g = normal(1, T + 1, E, dtype=dtype), normal(2, T, K, dtype=torch.float32)
+        slices = [batch.clone().requires_grad_(), batch[1:].clone().requires_grad_()]
+        assert slices[0][1:].data_ptr() % 16 != 0
+        out = []
+        for z, leaf in ((slices[0][1:], slices[0]), (slices[1], slices[1])):
+            ids, p = d.gate(z, G.epx.RouteConfig())
+            p.backward(g)
+            out.append((ids, p.detach(), leaf.grad[-T:]))
+        for a, b in zip(*out):
+            assert torch.equal(a, b)
