@@ -166,8 +166,9 @@ def _tensor(t: Optional[torch.Tensor], name: str, dtype, numel: int, device=None
 
 def _stream(stream, device) -> int:
     if stream is None:
-        # the raw handle of torch.cuda.current_stream(device), without the 2 us its object costs
-        return torch._C._cuda_getCurrentRawStream(device.index)
+        # the raw handle, without the 2 us that current_stream's object costs, where torch has the call
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        return torch.cuda.current_stream(device).cuda_stream if raw is None else raw(device.index)
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
