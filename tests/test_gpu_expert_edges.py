@@ -95,3 +95,115 @@ def test_gate_of_a_slice_that_begins_off_16_bytes(G):  # noqa: F811
             out.append((ids, p.detach(), leaf.grad[-T:]))
         for a, b in zip(*out):
             assert torch.equal(a, b)
+
+
+RANKED = [(64, 8, 3), (64, 64, 9), (128, 16, 4), (256, 8, 4), (256, 64, 20), (512, 8, 2), (2048, 64, 7)]
+
+
+def close_groups(E, groups, top, T, size, rng):
+    """Logits and bias of T tokens whose groups number top and top + 1 (and here and
+    there the one after) have keys that tie, or differ by one ulp of one logit.
+    Experts of a group lie far apart; size: of the scores, which the bias stays below."""
+    per = E // groups
+    lo = 0.0 if per == 1 else -1.5
+    base = np.linspace(lo, 1.5, per, dtype=np.float32) if per > 1 else np.zeros(1, np.float32)
+    bias = np.tile((rng.standard_normal(per) * 0.02 * size).astype(np.float32), groups)
+    z = np.empty((T, groups, per), np.float32)
+    for t in range(T):
+        order = rng.permutation(groups)
+        level = np.linspace(1.0, -1.0, groups, dtype=np.float32)  # of the groups, best first
+        same = rng.integers(2, 4)
+        for rank, g in enumerate(order):
+            z[t, g] = base + (level[top - 1] if top - 1 <= rank < top - 1 + same else level[rank])
+        kind = t % 4
+        if kind:  # 0: a tie.  Otherwise one expert of one of the groups: the best, the second, or one that does not count
+            g = order[top - 1 + rng.integers(0, same)] if top - 1 + same <= groups else order[top - 1]
+            e = np.argsort(-z[t, g])[min(kind - 1, per - 1)]
+            z[t, g, e] = np.nextafter(z[t, g, e], np.float32(np.inf if rng.random() < 0.5 else -np.inf))
+    return z.reshape(T, E), bias
+
+
+@pytest.mark.parametrize("score", ["sigmoid", "softmax"])
+@pytest.mark.parametrize("E,groups,top", RANKED)
+def test_groups_too_close_to_tell_in_32_bits(G, E, groups, top, score):  # noqa: F811
+    """Which groups stay, and with them the ids, as 64-bit scores say: ties to the
+    lower index, differences of one ulp of one logit.  The groups' keys are closer
+    than fp32 can tell (a rounding of a key of about 1 is 2^-24), the experts' are not."""
+    from test_gpu_expert_layer import plain_route
+
+    T, K = 200, min(8, top * (E // groups))
+    G.say(f"[gpu] close groups E={E} groups={groups} top={top} {score}")
+    z, bias = close_groups(E, groups, top, T, 1.0 if score == "sigmoid" else 1.0 / E,
+                           np.random.default_rng(E + groups))
+    logits, b = torch.from_numpy(z).to("cuda:0"), torch.from_numpy(bias).to("cuda:0")
+    s = 1 / (1 + np.exp(-z.astype(np.float64))) if score == "sigmoid" else np.exp(z.astype(np.float64))
+    if score == "softmax":
+        s = s / s.sum(1, keepdims=True)
+    keys = np.sort((s + bias.astype(np.float64)).reshape(T, groups, -1), axis=2)
+    of_group = np.sort(keys[..., -2:].sum(2), axis=1)[:, ::-1]
+    gap = of_group[:, top - 1] - of_group[:, top]
+    assert (gap < 2.0 ** -20).all() and (gap[::4] == 0).all() and (gap > 0).sum() > T // 8
+    cfg = G.epx.EpConfig(num_tokens=T, hidden=8, num_experts=E, num_segments=1, top_k=K)
+    r = G.epx.RouteConfig(score=score, num_groups=groups, top_groups=top)
+    ids, p = torch.empty(T, K, dtype=torch.int32, device="cuda:0"), torch.empty(T, K, device="cuda:0")
+    G.epx.ep_route(cfg, r, logits, ids, p, bias=b)
+    np.testing.assert_array_equal(ids.cpu().numpy(), plain_route(logits, b, None, K, r)[0])
+
+
+# ---------------------------------------------------------------------------
+# Streams
+# ---------------------------------------------------------------------------
+def test_different_calls_on_two_streams(G):  # noqa: F811
+    """Every operator on two streams at once, each with its own layout, inputs and
+    sizes (and so other tiles): each gives the bits that it gives alone."""
+    def work(seed, name, n_in, n_out, T, E):
+        d = Rows(G, name)
+        x, gy, w = normal(seed, d.R, n_in), normal(seed + 1, d.R, n_out), normal(seed + 2, d.experts, n_out, n_in)
+        q, _, _ = nvfp4_weights(seed, d.experts, n_out, n_in)
+        h, ga = normal(seed + 3, d.R, 2 * n_out), normal(seed + 4, d.R, n_out)
+        cfg = G.epx.EpConfig(num_tokens=T, hidden=8, num_experts=E, num_segments=1, top_k=4)
+        r = G.epx.RouteConfig(score="sigmoid", num_groups=4, top_groups=2)
+        z, bias, gp = (normal(seed + 5 + i, *s, dtype=torch.float32) for i, s in enumerate(((T, E), (E,), (T, 4))))
+        e = G.epx
+
+        def buffers():
+            f32 = dict(dtype=torch.float32, device="cuda:0")
+            return dict(y=filled(d.R, n_out), yq=filled(d.R, n_out), gx=filled(d.R, n_in), gw=filled(d.experts, n_out, n_in),
+                        act=filled(d.R, n_out), gh=filled(d.R, 2 * n_out), gprobs=torch.zeros(d.T, d.K, **f32),
+                        ids=torch.zeros(T, 4, dtype=torch.int32, device="cuda:0"), p=torch.zeros(T, 4, **f32),
+                        gz=torch.zeros(T, E, **f32))
+
+        def calls(b, st):
+            return [
+                lambda: e.ep_expert_gemm(d.cfg, d.lay, x, w, b["y"], stream=st),
+                lambda: e.ep_route(cfg, r, z, b["ids"], b["p"], bias=bias, stream=st),
+                lambda: e.ep_expert_gemm_nvfp4(d.cfg, d.lay, x, *q, b["yq"], stream=st),
+                lambda: e.ep_swiglu(d.cfg, d.lay, h, d.probs, b["act"], stream=st),
+                lambda: e.ep_expert_gemm_bwd_w(d.cfg, d.lay, gy, x, b["gw"], stream=st),
+                lambda: e.ep_swiglu_bwd(d.cfg, d.lay, h, d.probs, ga, b["gh"], b["gprobs"], stream=st),
+                lambda: e.ep_expert_gemm_bwd_x(d.cfg, d.lay, gy, w, b["gx"], stream=st),
+                lambda: e.ep_route_bwd(cfg, r, z, b["ids"], gp, b["gz"], stream=st),
+            ]
+
+        return buffers, calls
+
+    jobs = [work(1, "tall", 528, 1040, 700, 256), work(50, "odd", 272, 72, 129, 64)]
+    want = []
+    for buffers, calls in jobs:
+        b = buffers()
+        for call in calls(b, None):
+            call()
+        torch.cuda.synchronize()
+        want.append(b)
+    streams = [torch.cuda.Stream() for _ in jobs]
+    for _ in range(3):
+        got = [buffers() for buffers, _ in jobs]
+        torch.cuda.synchronize()
+        both = [calls(b, st) for (_, calls), b, st in zip(jobs, got, streams)]
+        for pair in zip(both[0], both[1]):
+            for call in pair:
+                call()
+        torch.cuda.synchronize()
+        for g, w in zip(got, want):
+            for n in w:
+                assert torch.equal(g[n].view(torch.uint8), w[n].view(torch.uint8)), n
