@@ -207,3 +207,51 @@ def test_different_calls_on_two_streams(G):  # noqa: F811
         for g, w in zip(got, want):
             for n in w:
                 assert torch.equal(g[n].view(torch.uint8), w[n].view(torch.uint8)), n
+
+
+def test_captured_training_step_replays_like_the_eager_one(G):  # noqa: F811
+    """The layer through EpDispatcher, forward and gradients, captured into one
+    graph: every replay gives the eager step's bits, with new inputs in between."""
+    from combine_ep_dispatch_amd.autograd import EpDispatcher
+
+    T, H, E, K, inter = 40, 64, 8, 2, 32
+    shapes = dict(x=(T, H), logits=(T, E), w1=(E, 2 * inter, H), w2=(E, H, inter))
+    gy = normal(9, T, H)
+
+    def inputs(seed):
+        return {n: normal(seed + i, *s, dtype=torch.float32 if n == "logits" else torch.bfloat16)
+                for i, (n, s) in enumerate(shapes.items())}
+
+    def step(d, t):
+        ids, p = d.gate(t["logits"], G.epx.RouteConfig(score="sigmoid", num_groups=4, top_groups=2))
+        y = d.combine(d.linear(d.swiglu(d.linear(d.dispatch(t["x"], ids), t["w1"]), p), t["w2"]), None)
+        return [ids, y.detach(), *torch.autograd.grad(y, [t[n] for n in shapes], gy)]
+
+    def dispatcher():
+        return EpDispatcher(G.epx.EpConfig(num_tokens=T, hidden=H, num_experts=E, num_segments=2, top_k=K, align=8), "cuda:0")
+
+    eager, d = dispatcher(), dispatcher()
+    leaves = {n: v.requires_grad_() for n, v in inputs(1).items()}
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        for _ in range(3):
+            step(d, leaves)
+    torch.cuda.current_stream().wait_stream(side)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = step(d, leaves)
+    for i in range(4):
+        new = inputs(100 * i)
+        with torch.no_grad():
+            for n, v in new.items():
+                leaves[n].copy_(v)
+        want = step(eager, {n: v.requires_grad_() for n, v in new.items()})
+        torch.cuda.synchronize()
+        for v in got:
+            v.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        for k, (a, b) in enumerate(zip(got, want)):
+            assert torch.equal(a, b), (i, k)
