@@ -124,22 +124,22 @@ __global__ __launch_bounds__(WAVES * kWave) void k_nvfp4(ExpertArgs a, int32_t f
         off[2 + kScaleLoads + j] = r * in * 2 + c * 16;
         first[2 + kScaleLoads + j] = c * 8;
     }
-    // Step s of this wave's features and of its share of the rows: what is left
-    // of each operand from the step's first byte on (its last 16 codes may end
-    // in the middle of a lane's 16 bytes); lanes past the end of the summed
-    // dimension read nothing.
+    // Step s of this wave's features and of its share of the rows; lanes past
+    // the end of the summed dimension read nothing.  (The last 16 codes of a
+    // feature may end in the middle of a lane's 16 bytes: what follows them
+    // meets zeros of the rows, or the end of the buffer.)
     auto load = [&](int32_t s, int j) {
         uint8_t* const to = lds + s % BUFS * kBuffer;
         const int32_t l0 = s * L;
-        const int32_t v = l0 + L <= in || l0 + first[j] < in ? off[j] : kOutside;
+        const bool on = l0 + L <= in || l0 + first[j] < in;
         if (j < 2)
-            load_to_lds<16>(codes + l0 / 2, max(frows * cpitch - l0 / 2, 0), to + w * (FW * kCodeRow) + j * 1024, v);
+            load_to_lds<16>(codes, frows * cpitch, to + w * (FW * kCodeRow) + j * 1024, on ? off[j] + l0 / 2 : kOutside);
         else if (j < 2 + kScaleLoads)
-            load_to_lds<WORDS ? 4 : 1>(scales + l0 / 16, max(frows * spitch - l0 / 16, 0),
-                                       to + kCodes + w * kScaleBytes + (j - 2) * 256, v);
+            load_to_lds<WORDS ? 4 : 1>(scales, frows * spitch, to + kCodes + w * kScaleBytes + (j - 2) * 256,
+                                       on ? off[j] + l0 / 16 : kOutside);
         else
-            load_to_lds<16>(x + l0, max((t.rows * in - l0) * 2, 0),
-                            to + kCodes + kScales + (w * kRowLoads + j - 2 - kScaleLoads) * 1024, v);
+            load_to_lds<16>(x, t.rows * in * 2, to + kCodes + kScales + (w * kRowLoads + j - 2 - kScaleLoads) * 1024,
+                            on ? off[j] + l0 * 2 : kOutside);
     };
     f32x4 acc[FW / 16][NT / 16] = {};
     const int32_t steps = (in + L - 1) / L;
