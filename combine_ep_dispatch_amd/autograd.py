@@ -27,6 +27,9 @@ The expert layer around the two, on the same layout:
     act = d.swiglu(h, probs)                 # weights applied to the rows; differentiable in both
     y = d.combine(d.linear(act, w2), None)
 
+A step can be captured into a graph, backward pass included, on leaves that no
+eager autograd graph still holds (torch does not support capturing beside one).
+
 The backward passes are library calls without gradients of their own: under
 create_graph the first derivatives can be had, differentiating them raises.
 """

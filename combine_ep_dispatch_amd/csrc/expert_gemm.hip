@@ -11,19 +11,25 @@
 // Tiles of 256 features by 256 or 128 rows, 8 waves of 128 x 64 or 64 x 64
 // results in registers; steps of 64 values of L, two and a half or three of
 // them in LDS, copied there by the loads themselves, one barrier a step.  Where
-// those would be few, tiles of 64 by 64 (k_expert_small).
+// those would be few, the forward product and the input's gradient take tiles of
+// 64 by 64 (k_expert_small); the weights' gradient has the 256 by 256 ones alone,
+// each of which sums all rows of its expert: 4 experts of 128 x 128 with 4096 rows
+// each are 4 workgroups and take 86 us, of 1536 x 2048 (192 workgroups) 114.
 //
 // What bounds them: with few rows an expert HBM, which reads each weight once
-// (16 tokens of 8 of 32 experts, 4096 x 7168: 1.88 GB in 316 us, 5.9 TB/s of
+// (16 tokens of 8 of 32 experts, 4096 x 7168: 1.88 GB in 321 us, 5.9 TB/s of
 // the 6.0 that reading alone reaches); with many the way from L2 to LDS, 64 KiB
 // a step and CU beside 128 matrix instructions a SIMD.  32768 rows, same experts:
-// 1784 us, 1078 TFLOP/s (a library product of that size: 1359 us); its loads
-// alone take 1530 us, its products alone 1230, and 11 % of the tiles' rows are
-// past their group's end.  Gradients of 49152 rows, 64 experts of 2048 x 1416:
-// input's 337 us (846 TFLOP/s), weights' 356 (801); 1416 fills 92 % of 6 tiles.
-// Measured instead, for the 32768 rows: steps of 32 values, four in LDS, 2190 us
-// (64-byte requests); dword touches into L2 ahead of the loads 2000; the barrier
-// in the middle of a step 1850; tiles in another order of L 1850.
+// 1827 us, 1053 TFLOP/s (a library product of that size: 1298 us in the same run);
+// the matrix pipes are busy for 52 % of the cycles, LDS reads have no bank
+// conflicts, 4.9 GB come from beyond L2; 11 % of the tiles' rows are past their
+// group's end.  Gradients of 49152 rows, 64 experts of 2048 x 1416: input's 344 us
+// (829 TFLOP/s), weights' 359 (794; fp32 447, added to fp32 641, which write 743
+// MB and read as much); 1416 fills 92 % of 6 tiles.  Measured instead, for the
+// 32768 rows when they took 1784 us: the loads alone 1530, the products alone
+// 1230; steps of 32 values, four in LDS, 2190 (64-byte requests); dword touches
+// into L2 ahead of the loads 2000; the barrier in the middle of a step 1850; tiles
+// in another order of L 1850.
 #include <type_traits>
 
 #include "expert_device.h"
@@ -405,8 +411,9 @@ hipError_t launch(const ExpertArgs& a, hipStream_t stream) {
 // 2048 features (256) 38 and 91, 4096 (512) 86 and 112; 32 experts with 4 rows,
 // 4096 values, 512 features (272) 24 and 52, 1024 (544) 44 and 54, 2048 (1088)
 // 151 and 122; 128 rows, 2048 values, 512 features (768) 36 and 50, 1024 (1536)
-// 72 and 52.  Input's gradient (and the weights' with it), 32 experts with 4
-// rows of 4096 values, 512 features (272) 73 and 102, 1024 (544) 174 and 160.
+// 72 and 52.  Input's gradient, timed with the weights' behind it, which has no
+// small form and takes the same time on both sides: 32 experts with 4 rows of 4096
+// values, 512 features (272) 73 and 102, 1024 (544) 174 and 160.
 // Wide row tiles by the rows a group has on average.  Forward over 32 experts of
 // 4096 x 7168, us at 16, 64, 128, 256 and 512 rows a group: 128-row tiles 317
 // 335 454 716 1128, 256-row tiles 330 363 405 689 1008 (128 rows on average fill

@@ -13,11 +13,14 @@
 // What bounds it: with one row an expert the latency of the first loads and
 // HBM (8 experts of 4096 x 7168, 132 MB: 30 us, 4.4 TB/s; loads alone 26, all
 // but the loads 25); at 8 rows HBM and the conversions (65 experts, 1.09 GB:
-// 248 us, 4.4 TB/s; loads alone 242, of which the 4-byte loads of the scales
-// are 55, all but the loads 143); at 122 rows the conversions, two instructions
-// a weight and row tile, and the matrix instructions of tiles that 122 rows
-// fill three quarters of (32 experts of 7168 x 2048: 190 us, 602 TFLOP/s; loads
-// alone 137, all but the loads 159).  Measured instead: scales as 64-byte windows
+// 256 us, 4.3 TB/s; loads alone 242, of which the 4-byte loads of the scales
+// are 55, all but the loads 143; vector instructions for 68 % of the cycles); at
+// 122 rows the conversions, two instructions a weight and row tile, and the matrix
+// instructions of tiles that 122 rows fill three quarters of (32 experts of 7168 x
+// 2048: 197 us, 581 TFLOP/s; loads alone 137, all but the loads 159; the matrix
+// pipes are busy for 33 % of the cycles).  32 experts of 4096 x 7168 with 1024
+// rows each: 1981 us, 971 TFLOP/s.  Few tiles are slow: 4 experts of 512 x 2048
+// with 64 rows are 8 workgroups with work, 32 us.  Measured instead: scales as 64-byte windows
 // load in 187 us instead of 242, but two of them in LDS cost a workgroup a CU
 // (254-274 us in all), and one, taken to registers for four steps, gains nothing
 // (262, and 36 us instead of 32 for one row); 4 waves of 64 features by 128 rows

@@ -4,7 +4,9 @@
 // moe_router_dtype: fp32 routing weights; fused_a2a page,
 // HybridEPDispatch.forward: topk_idx with -1 for unused slots).
 //
-// One wave per token; lane l holds experts [l VPL, (l + 1) VPL).  Keys are
+// One wave per token; lane l holds experts [l VPL, (l + 1) VPL).  (Up to 256
+// experts and 16 slots four tokens share a wave: the gradient, and the choice
+// where there is neither bias nor groups; see the narrow forms.)  Keys are
 // 32-bit integers that order like the floats they stand for, so that the
 // largest of a wave is six cross-lane maxima; the K experts are taken one by
 // one.
@@ -13,13 +15,16 @@
 // score + bias, whose fp32 value is off by a few roundings (key_error below):
 // where other keys lie closer to the largest than that, these few are compared
 // in 64 bits, where groups' keys do, the groups are ranked in 64 bits, and where
-// many experts' do, the token is chosen again from 64-bit keys.
+// many experts' do, the token is chosen again from 64-bit keys.  So is every token
+// where the groups do not fill whole lanes (E other than 64 VPL, or a number of
+// groups that is no power of two), without a bias too.
 //
 // What bounds it: a few tokens, the launch and K dependent choices (16 tokens
-// of 256 experts, 4 of 8 groups, top-8: 6.8 us); many, instructions, for a
-// token's logits are read once (4096 tokens: 13.4 us forward, 4.9 backward, of
-// 1.7 us of bytes; 65 536 tokens of 64 took 119 us both ways with 64-bit keys
-// throughout, 43 with these).
+// of 256 experts, 4 of 8 groups, top-8: 6.9 us); many, instructions, for a
+// token's logits are read once (4096 tokens: 13.0 us forward, 5.5 backward, of
+// 1.7 us of bytes; in 64-bit keys 160 experts in 8 groups 16 us, 240 in 4 20;
+// 65 536 tokens of 64, four a wave: 12.3 us forward and 10.8 backward, 43 with
+// a wave each, 119 with 64-bit keys throughout).
 #include "epx_device.h"
 
 namespace epx {

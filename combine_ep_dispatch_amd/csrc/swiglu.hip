@@ -6,8 +6,8 @@
 //
 // Rows are found through token_row, so only those that a kept slot owns are
 // touched.  Bound by HBM: 3 inter values of a row read and written forward, 5
-// backward.  35 700 rows of 2048: 83 us forward (5.3 TB/s), 139 backward (5.3);
-// a copy of 1 GiB reaches 5.2.  128 rows (a decode step): 4.4 us.
+// backward.  35 700 rows of 2048: 84 us forward (5.2 TB/s), 140 backward (5.2);
+// a copy of 1 GiB reaches 5.2.  128 rows (a decode step): 4.5 us.
 #include "epx_device.h"
 
 namespace epx {

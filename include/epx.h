@@ -420,6 +420,8 @@ int ep_dispatch_layout_noalloc(const ep_cfg_t* cfg, const int32_t* topk_ids, con
  * (or ep_swiglu with probs NULL and ep_combine with probs).  Rows that no
  * kept slot owns (pad rows, rows past a segment's used rows, rows of dropped
  * slots) are never read and, unless EP_ZERO_PAD_ROWS is set, never written.
+ * No output of these calls may overlap an input (EP_GRAD_F32_ADD's grad_w is
+ * both).
  * ------------------------------------------------------------------------ */
 
 /* ep_route_t.score */
