@@ -19,7 +19,10 @@ Typical use (all tensors on one GPU, bf16 payloads as torch.bfloat16)::
 
 The expert layer around them: ep_route (logits -> topk_ids, probs) before the
 layout, ep_expert_gemm / ep_swiglu / ep_expert_gemm (or ep_expert_gemm_nvfp4)
-between dispatch and combine, each with its backward calls.
+between dispatch and combine, each with its backward calls.  ep_expert_gated (or
+ep_expert_gated_nvfp4) is the first product and the activation in one kernel.
+Requests with low-rank adapters (Adapters) call ep_lora_down before a product and
+its form with adapters.
 """
 
 from __future__ import annotations
@@ -34,7 +37,8 @@ from . import _lib
 from ._lib import (EP_FLAG_BAD_ID, EP_FLAG_DROPPED, EP_FLAG_INTERNAL, EP_FLAG_MAP_OVERFLOW,  # noqa: F401
                    EP_NOALLOC_SCRATCH_BYTES, EP_ZERO_PAD_ROWS, EP_LAYOUT_LOOKBACK, EP_LAYOUT_DIRECT,
                    EP_LAYOUT_BARRIER, EP_LAYOUT_COUNT, EP_GRAD_BF16, EP_GRAD_F32, EP_GRAD_F32_ADD,
-                   EP_SCORE_SIGMOID, EP_SCORE_SOFTMAX, EP_TYPE_BF16, EP_TYPE_F32, EpCfg, EpLayout, EpRoute)
+                   EP_SCORE_SIGMOID, EP_SCORE_SOFTMAX, EP_TYPE_BF16, EP_TYPE_F32, EP_GATED_PART,
+                   EpCfg, EpLayout, EpLora, EpRoute)
 
 __all__ = [
     "EpConfig", "Layout", "QueryResult", "ep_query", "workspace_for", "ep_dispatch_layout",
@@ -45,6 +49,9 @@ __all__ = [
     "EP_FLAG_BAD_ID", "EP_FLAG_INTERNAL",
     "RouteConfig", "ep_route", "ep_route_bwd", "ep_swiglu", "ep_swiglu_bwd", "ep_expert_gemm",
     "ep_expert_gemm_bwd_x", "ep_expert_gemm_bwd_w", "ep_expert_gemm_nvfp4",
+    "ep_expert_gated", "ep_expert_gated_nvfp4", "ep_expert_gated_bwd", "gated_workspace_for",
+    "Adapters", "ep_lora_down", "ep_expert_gemm_lora", "ep_expert_gemm_nvfp4_lora", "ep_lora_bwd_u",
+    "ep_expert_gemm_bwd_x_lora", "ep_lora_bwd_w",
 ]
 
 
@@ -584,6 +591,205 @@ def ep_expert_gemm_nvfp4(cfg: EpConfig, layout: Layout, x: torch.Tensor, codes: 
     lay = _arrays(layout, cfg, dev, "counts", "row_offsets", "seg_base")
     _call("ep_expert_gemm_nvfp4", dev, stream, ctypes.byref(cfg.to_c()), ctypes.byref(lay), n_in, n_out,
           x.data_ptr(), codes.data_ptr(), scales.data_ptr(), rowscale.data_ptr(), y.data_ptr())
+
+
+@dataclasses.dataclass
+class Adapters:
+    """Low-rank adapters of many requests beside a product (ep_lora_t in include/epx.h)."""
+
+    token_adapter: torch.Tensor           # int32 [T]: the token's adapter, -1 for none
+    a: torch.Tensor                       # bf16 [n, E (+1 shared), rank, in]
+    b: torch.Tensor                       # bf16 [n, E (+1 shared), out, rank]
+    scale: Optional[torch.Tensor] = None  # float32 [n], or None: 1
+
+    @property
+    def rank(self) -> int:
+        return self.a.shape[2] if self.a.dim() == 4 else 0
+
+    def to_c(self, cfg: EpConfig, n_in: Optional[int], n_out: Optional[int], device) -> EpLora:
+        """Checked against the product's dimensions, of which None is not read by the call."""
+        n, experts, rank = self.a.shape[0] if self.a.dim() == 4 else 0, cfg.num_experts + cfg.shared_expert, self.rank
+        for t, name, dims in ((self.a, "a", (rank, n_in)), (self.b, "b", (n_out, rank))):
+            want = [n, experts, *(t.shape[k + 2] if d is None and t.dim() == 4 else d for k, d in enumerate(dims))]
+            if t.dim() != 4 or list(t.shape) != want:
+                raise ValueError(f"adapters.{name} must be {want}, got {list(t.shape)}")
+            _tensor(t, f"adapters.{name}", torch.bfloat16, t.numel(), device)
+        _tensor(self.token_adapter, "adapters.token_adapter", torch.int32, cfg.num_tokens, device)
+        if self.scale is not None:
+            _tensor(self.scale, "adapters.scale", torch.float32, n, device)
+        return EpLora(self.token_adapter.data_ptr(), self.a.data_ptr(), self.b.data_ptr(), _ptr(self.scale), n, rank,
+                      0, 0)
+
+
+def _lora(cfg: EpConfig, adapters: Optional[Adapters], u: Optional[torch.Tensor], n_in: Optional[int],
+          n_out: Optional[int], device):
+    """The adapters of a call as (reference, to keep it alive; u's pointer)."""
+    if adapters is None:
+        if u is not None:
+            raise ValueError("u is given without adapters")
+        return None, None
+    c = adapters.to_c(cfg, n_in, n_out, device)
+    _tensor(u, "u", torch.float32, cfg.recv_rows * adapters.rank, device)
+    return ctypes.byref(c), u.data_ptr()
+
+
+_BLOCK_ARRAYS = ("counts", "row_offsets", "seg_base")
+
+
+def _block_layout(layout: Layout, cfg: EpConfig, device, *names: str) -> EpLayout:
+    c = _arrays(layout, cfg, device, *_BLOCK_ARRAYS, *names)
+    _tensor(layout.src_info, "src_info", torch.int32, 2 * cfg.recv_rows, device)
+    c.src_info = layout.src_info.data_ptr()
+    return c
+
+
+def ep_lora_down(cfg: EpConfig, layout: Layout, x: torch.Tensor, adapters: Adapters, u: torch.Tensor,
+                 stream=None) -> None:
+    """u[r] = scale * a[adapter, expert of r] @ x[r], for the products with adapters:
+    x bf16 [R, in], u float32 [R, rank] (words that hold two bf16 each, see include/epx.h)."""
+    dev = x.device
+    n_in = _columns(x, "x", cfg.recv_rows)
+    lora, pu = _lora(cfg, adapters, u, n_in, None, dev)
+    lay = _block_layout(layout, cfg, dev)
+    _call("ep_lora_down", dev, stream, ctypes.byref(cfg.to_c()), ctypes.byref(lay), lora, n_in, x.data_ptr(), pu)
+
+
+def ep_expert_gemm_lora(cfg: EpConfig, layout: Layout, x: torch.Tensor, w: torch.Tensor, y: torch.Tensor,
+                        adapters: Adapters, u: torch.Tensor, stream=None) -> None:
+    """ep_expert_gemm with y[r] += b[adapter, expert of r] @ u[r] before its rounding (u of ep_lora_down)."""
+    dev, R = x.device, cfg.recv_rows
+    n_in, n_out = _columns(x, "x", R), _columns(y, "y", R, device=dev)
+    _weights(cfg, w, "w", torch.bfloat16, (n_out, n_in), dev)
+    lora, pu = _lora(cfg, adapters, u, n_in, n_out, dev)
+    lay = _block_layout(layout, cfg, dev)
+    _call("ep_expert_gemm_lora", dev, stream, ctypes.byref(cfg.to_c()), ctypes.byref(lay), lora, n_in, n_out,
+          x.data_ptr(), w.data_ptr(), pu, y.data_ptr())
+
+
+def _nvfp4_weights(cfg: EpConfig, codes, scales, rowscale, n_out: int, n_in: int, dev) -> None:
+    _weights(cfg, codes, "codes", torch.uint8, (n_out, n_in // 2), dev)
+    _weights(cfg, scales, "scales", torch.uint8, (n_out, n_in // 16), dev)
+    _weights(cfg, rowscale, "rowscale", torch.bfloat16, (n_out,), dev)
+
+
+def ep_expert_gemm_nvfp4_lora(cfg: EpConfig, layout: Layout, x: torch.Tensor, codes: torch.Tensor,
+                              scales: torch.Tensor, rowscale: torch.Tensor, y: torch.Tensor, adapters: Adapters,
+                              u: torch.Tensor, stream=None) -> None:
+    """ep_expert_gemm_nvfp4 with the adapters' part, as ep_expert_gemm_lora."""
+    dev, R = x.device, cfg.recv_rows
+    n_in, n_out = _columns(x, "x", R), _columns(y, "y", R, device=dev)
+    _nvfp4_weights(cfg, codes, scales, rowscale, n_out, n_in, dev)
+    lora, pu = _lora(cfg, adapters, u, n_in, n_out, dev)
+    lay = _block_layout(layout, cfg, dev)
+    _call("ep_expert_gemm_nvfp4_lora", dev, stream, ctypes.byref(cfg.to_c()), ctypes.byref(lay), lora, n_in, n_out,
+          x.data_ptr(), codes.data_ptr(), scales.data_ptr(), rowscale.data_ptr(), pu, y.data_ptr())
+
+
+def ep_lora_bwd_u(cfg: EpConfig, layout: Layout, grad_y: torch.Tensor, adapters: Adapters, grad_u: torch.Tensor,
+                  stream=None) -> None:
+    """grad_u[r] = scale * b[adapter, expert of r]^T @ grad_y[r]: grad_y bf16 [R, out], grad_u as u."""
+    dev = grad_y.device
+    n_out = _columns(grad_y, "grad_y", cfg.recv_rows)
+    lora, pu = _lora(cfg, adapters, grad_u, None, n_out, dev)
+    lay = _block_layout(layout, cfg, dev)
+    _call("ep_lora_bwd_u", dev, stream, ctypes.byref(cfg.to_c()), ctypes.byref(lay), lora, n_out, grad_y.data_ptr(), pu)
+
+
+def ep_expert_gemm_bwd_x_lora(cfg: EpConfig, layout: Layout, grad_y: torch.Tensor, w: torch.Tensor,
+                              grad_x: torch.Tensor, adapters: Adapters, grad_u: torch.Tensor, stream=None) -> None:
+    """ep_expert_gemm_bwd_x with grad_x[r] += a[adapter, expert of r]^T @ grad_u[r] before its rounding."""
+    dev, R = grad_y.device, cfg.recv_rows
+    n_in, n_out = _columns(grad_x, "grad_x", R, device=dev), _columns(grad_y, "grad_y", R)
+    _weights(cfg, w, "w", torch.bfloat16, (n_out, n_in), dev)
+    lora, pu = _lora(cfg, adapters, grad_u, n_in, n_out, dev)
+    lay = _block_layout(layout, cfg, dev)
+    _call("ep_expert_gemm_bwd_x_lora", dev, stream, ctypes.byref(cfg.to_c()), ctypes.byref(lay), lora, n_in, n_out,
+          grad_y.data_ptr(), w.data_ptr(), pu, grad_x.data_ptr())
+
+
+def ep_lora_bwd_w(cfg: EpConfig, layout: Layout, x: torch.Tensor, grad_y: torch.Tensor, adapters: Adapters,
+                  u: torch.Tensor, grad_u: torch.Tensor, grad_a: torch.Tensor, grad_b: torch.Tensor,
+                  accumulate: bool = False, stream=None) -> None:
+    """The adapters' gradients, of the shapes of adapters.a and .b, both bf16 or both
+    float32; accumulate (float32 only) adds to what they hold."""
+    dev, R = x.device, cfg.recv_rows
+    kinds = {torch.bfloat16: EP_GRAD_BF16, torch.float32: EP_GRAD_F32_ADD if accumulate else EP_GRAD_F32}
+    if grad_a.dtype not in kinds or (accumulate and grad_a.dtype != torch.float32):
+        raise ValueError(f"grad_a must be torch.float32{'' if accumulate else ' or torch.bfloat16'}, got {grad_a.dtype}")
+    n_in, n_out = _columns(x, "x", R), _columns(grad_y, "grad_y", R, device=dev)
+    lora, pu = _lora(cfg, adapters, u, n_in, n_out, dev)
+    _tensor(grad_u, "grad_u", torch.float32, R * adapters.rank, dev)
+    for t, of, name in ((grad_a, adapters.a, "grad_a"), (grad_b, adapters.b, "grad_b")):
+        if t.shape != of.shape:
+            raise ValueError(f"{name} must be {list(of.shape)}, got {list(t.shape)}")
+        _tensor(t, name, grad_a.dtype, of.numel(), dev)
+    lay = _block_layout(layout, cfg, dev)
+    _call("ep_lora_bwd_w", dev, stream, ctypes.byref(cfg.to_c()), ctypes.byref(lay), lora, n_in, n_out, x.data_ptr(),
+          grad_y.data_ptr(), pu, grad_u.data_ptr(), grad_a.data_ptr(), grad_b.data_ptr(), kinds[grad_a.dtype])
+
+
+def ep_expert_gated(cfg: EpConfig, layout: Layout, x: torch.Tensor, w: torch.Tensor, probs: Optional[torch.Tensor],
+                    act: torch.Tensor, adapters: Optional[Adapters] = None, u: Optional[torch.Tensor] = None,
+                    stream=None) -> None:
+    """act[r] = w_r * silu(gate) * up in one kernel: x bf16 [R, in], w bf16 [E (+1
+    shared, last), 2*inter, in] (gate rows, then up rows), probs float32 [T, K] or
+    None (weight 1), act bf16 [R, inter]; adapters beside w, with u of ep_lora_down."""
+    dev, R = x.device, cfg.recv_rows
+    n_in, inter = _columns(x, "x", R), _columns(act, "act", R, device=dev)
+    _weights(cfg, w, "w", torch.bfloat16, (2 * inter, n_in), dev)
+    if probs is not None:
+        _tensor(probs, "probs", torch.float32, cfg.num_tokens * cfg.top_k, dev)
+    lora, pu = _lora(cfg, adapters, u, n_in, 2 * inter, dev)
+    lay = _block_layout(layout, cfg, dev)
+    _call("ep_expert_gated", dev, stream, ctypes.byref(cfg.to_c()), ctypes.byref(lay), lora, n_in, inter, x.data_ptr(),
+          w.data_ptr(), _ptr(probs), pu, act.data_ptr())
+
+
+def ep_expert_gated_nvfp4(cfg: EpConfig, layout: Layout, x: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor,
+                          rowscale: torch.Tensor, probs: Optional[torch.Tensor], act: torch.Tensor,
+                          adapters: Optional[Adapters] = None, u: Optional[torch.Tensor] = None, stream=None) -> None:
+    """ep_expert_gated over 4-bit weights (those of ep_expert_gemm_nvfp4, out = 2*inter)."""
+    dev, R = x.device, cfg.recv_rows
+    n_in, inter = _columns(x, "x", R), _columns(act, "act", R, device=dev)
+    _nvfp4_weights(cfg, codes, scales, rowscale, 2 * inter, n_in, dev)
+    if probs is not None:
+        _tensor(probs, "probs", torch.float32, cfg.num_tokens * cfg.top_k, dev)
+    lora, pu = _lora(cfg, adapters, u, n_in, 2 * inter, dev)
+    lay = _block_layout(layout, cfg, dev)
+    _call("ep_expert_gated_nvfp4", dev, stream, ctypes.byref(cfg.to_c()), ctypes.byref(lay), lora, n_in, inter,
+          x.data_ptr(), codes.data_ptr(), scales.data_ptr(), rowscale.data_ptr(), _ptr(probs), pu, act.data_ptr())
+
+
+def gated_workspace_for(cfg: EpConfig, inter: int, device) -> torch.Tensor:
+    """A uint8 device tensor large enough for ep_expert_gated_bwd's workspace."""
+    return torch.empty(cfg.num_tokens * cfg.top_k * -(-inter // EP_GATED_PART) * 4, dtype=torch.uint8, device=device)
+
+
+def ep_expert_gated_bwd(cfg: EpConfig, layout: Layout, x: torch.Tensor, w: torch.Tensor,
+                        probs: Optional[torch.Tensor], grad_act: torch.Tensor, grad_h: torch.Tensor,
+                        act: Optional[torch.Tensor] = None, grad_probs: Optional[torch.Tensor] = None,
+                        workspace: Optional[torch.Tensor] = None, adapters: Optional[Adapters] = None,
+                        u: Optional[torch.Tensor] = None, stream=None) -> None:
+    """grad_h bf16 [R, 2*inter] (and act again, and grad_probs float32 [T, K] with a
+    workspace of gated_workspace_for) from grad_act bf16 [R, inter]."""
+    dev, R = x.device, cfg.recv_rows
+    n_in, inter = _columns(x, "x", R), _columns(grad_act, "grad_act", R, device=dev)
+    _weights(cfg, w, "w", torch.bfloat16, (2 * inter, n_in), dev)
+    _tensor(grad_h, "grad_h", torch.bfloat16, R * 2 * inter, dev)
+    if act is not None:
+        _tensor(act, "act", torch.bfloat16, R * inter, dev)
+    for t, name in ((probs, "probs"), (grad_probs, "grad_probs")):
+        if t is not None:
+            _tensor(t, name, torch.float32, cfg.num_tokens * cfg.top_k, dev)
+    lora, pu = _lora(cfg, adapters, u, n_in, 2 * inter, dev)
+    lay = _block_layout(layout, cfg, dev)
+    if grad_probs is not None:
+        _tensor(workspace, "workspace", torch.uint8, 0 if workspace is None else workspace.numel(), dev)
+        _tensor(layout.token_row, "token_row", torch.int32, cfg.num_tokens * cfg.kp, dev)
+        lay.token_row = layout.token_row.data_ptr()
+    _call("ep_expert_gated_bwd", dev, stream, ctypes.byref(cfg.to_c()), ctypes.byref(lay), lora, n_in, inter,
+          x.data_ptr(), w.data_ptr(), _ptr(probs), pu, grad_act.data_ptr(), grad_h.data_ptr(), _ptr(act),
+          _ptr(grad_probs), _ptr(workspace), 0 if workspace is None else workspace.numel())
 
 
 def assert_no_overflow(layout: Layout, capacity: Optional[int] = None) -> None:

@@ -34,6 +34,9 @@ EP_TYPE_BF16 = 1
 EP_GRAD_BF16 = 0
 EP_GRAD_F32 = 1
 EP_GRAD_F32_ADD = 2
+EP_MAX_LORA_RANK = 128
+EP_MAX_ADAPTERS = 65536
+EP_GATED_PART = 32
 
 # Every symbol include/epx.h declares.
 SYMBOLS = ("ep_query", "ep_dispatch_layout", "ep_dispatch", "ep_dispatch_nvfp4", "ep_dispatch_fp8",
@@ -42,6 +45,8 @@ SYMBOLS = ("ep_query", "ep_dispatch_layout", "ep_dispatch", "ep_dispatch_nvfp4",
            "ep_combine_nvfp4", "ep_dispatch_with_layout", "ep_dispatch_nvfp4_with_layout",
            "ep_dispatch_fp8_with_layout", "ep_route", "ep_route_bwd", "ep_swiglu", "ep_swiglu_bwd",
            "ep_expert_gemm", "ep_expert_gemm_bwd_x", "ep_expert_gemm_bwd_w", "ep_expert_gemm_nvfp4",
+           "ep_lora_down", "ep_lora_bwd_u", "ep_lora_bwd_w", "ep_expert_gemm_lora", "ep_expert_gemm_nvfp4_lora",
+           "ep_expert_gemm_bwd_x_lora", "ep_expert_gated", "ep_expert_gated_nvfp4", "ep_expert_gated_bwd",
            "ep_strerror", "ep_abi_version")
 
 
@@ -70,6 +75,14 @@ class EpRoute(ctypes.Structure):
 
     _fields_ = [("score", ctypes.c_int32), ("normalize", ctypes.c_int32), ("num_groups", ctypes.c_int32),
                 ("top_groups", ctypes.c_int32), ("scale", ctypes.c_float), ("logits_type", ctypes.c_int32),
+                ("reserved0", ctypes.c_int32), ("reserved1", ctypes.c_int32)]
+
+
+class EpLora(ctypes.Structure):
+    """Mirror of ep_lora_t (device pointers)."""
+
+    _fields_ = [("token_adapter", ctypes.c_void_p), ("a", ctypes.c_void_p), ("b", ctypes.c_void_p),
+                ("scale", ctypes.c_void_p), ("num_adapters", ctypes.c_int32), ("rank", ctypes.c_int32),
                 ("reserved0", ctypes.c_int32), ("reserved1", ctypes.c_int32)]
 
 
@@ -111,6 +124,16 @@ def lib():
         L.ep_expert_gemm_bwd_x.argtypes = [cfg_p, lay_p, I32, I32, P, P, P, P]
         L.ep_expert_gemm_bwd_w.argtypes = [cfg_p, lay_p, I32, I32, P, P, P, I32, P]
         L.ep_expert_gemm_nvfp4.argtypes = [cfg_p, lay_p, I32, I32, P, P, P, P, P, P]
+        lora_p = ctypes.POINTER(EpLora)
+        L.ep_lora_down.argtypes = [cfg_p, lay_p, lora_p, I32, P, P, P]
+        L.ep_lora_bwd_u.argtypes = [cfg_p, lay_p, lora_p, I32, P, P, P]
+        L.ep_lora_bwd_w.argtypes = [cfg_p, lay_p, lora_p, I32, I32, P, P, P, P, P, P, I32, P]
+        L.ep_expert_gemm_lora.argtypes = [cfg_p, lay_p, lora_p, I32, I32, P, P, P, P, P]
+        L.ep_expert_gemm_nvfp4_lora.argtypes = [cfg_p, lay_p, lora_p, I32, I32, P, P, P, P, P, P, P]
+        L.ep_expert_gemm_bwd_x_lora.argtypes = [cfg_p, lay_p, lora_p, I32, I32, P, P, P, P, P]
+        L.ep_expert_gated.argtypes = [cfg_p, lay_p, lora_p, I32, I32, P, P, P, P, P, P]
+        L.ep_expert_gated_nvfp4.argtypes = [cfg_p, lay_p, lora_p, I32, I32, P, P, P, P, P, P, P, P]
+        L.ep_expert_gated_bwd.argtypes = [cfg_p, lay_p, lora_p, I32, I32, P, P, P, P, P, P, P, P, P, I64, P]
         for name in SYMBOLS[:-2]:
             getattr(L, name).restype = I
         L.ep_strerror.argtypes = [I]

@@ -382,6 +382,59 @@ ExpertArgs expert_args(const Shape& d, const ep_layout_t* L, int32_t in_dim, int
     return a;
 }
 
+// Adapters against the configuration; a and b as the call reads them.
+int check_lora(const Shape& d, const ep_lora_t* l, bool reads_a, bool reads_b) {
+    if (l == nullptr || l->reserved0 != 0 || l->reserved1 != 0) return EP_EINVAL;
+    if (l->num_adapters < 1 || l->num_adapters > EP_MAX_ADAPTERS) return EP_EINVAL;
+    if (l->rank < 8 || l->rank > EP_MAX_LORA_RANK || l->rank % 8 != 0) return EP_EINVAL;
+    if (bad_buffer(l->token_adapter, (int64_t)d.T * 4, 4) || misaligned(l->scale, 4)) return EP_EINVAL;
+    if ((reads_a && bad_buffer(l->a, 16, 16)) || (reads_b && bad_buffer(l->b, 16, 16))) return EP_EINVAL;
+    return EP_OK;
+}
+
+// What the gated block and the calls with adapters read of the layout.
+int check_block(const Shape& d, const ep_layout_t* L, int32_t in_dim, int32_t out_dim, int32_t in_multiple) {
+    const int rc = check_expert(d, L, in_dim, out_dim, in_multiple);
+    if (rc != EP_OK) return rc;
+    return bad_buffer(L->src_info, d.R * 8, 8) ? EP_EINVAL : EP_OK;
+}
+
+BlockArgs block_args(const Shape& d, const ep_layout_t* L, const ep_lora_t* l, int32_t in_dim, int32_t out_dim,
+                     const void* u, void* out) {
+    BlockArgs a = {};
+    a.e = expert_args(d, L, in_dim, out_dim, out);
+    if (l != nullptr) a.l = {l->token_adapter, l->a, l->b, l->scale, l->num_adapters, l->rank};
+    a.u = static_cast<const float*>(u);
+    a.src_info = L->src_info;
+    a.token_row = L->token_row;
+    a.T = d.T;
+    a.K = d.K;
+    a.Kp = d.Kp;
+    return a;
+}
+
+// Of the gated block: inter columns of act, optional adapters.
+int check_gated(const Shape& d, const ep_layout_t* L, const ep_lora_t* l, int32_t in_dim, int32_t inter,
+                int32_t in_multiple, const void* ulora, const float* probs) {
+    int rc;
+    if ((rc = check_block(d, L, in_dim, inter, in_multiple)) != EP_OK) return rc;
+    if (l != nullptr) {
+        if ((rc = check_lora(d, l, false, true)) != EP_OK) return rc;
+        if (bad_buffer(ulora, d.R * l->rank * 4, 16)) return EP_EINVAL;
+    } else if (ulora != nullptr) {
+        return EP_EINVAL;
+    }
+    return misaligned(probs, 4) ? EP_EINVAL : EP_OK;
+}
+
+BlockArgs gated_args(const Shape& d, const ep_layout_t* L, const ep_lora_t* l, int32_t in_dim, int32_t inter,
+                     const void* ulora, const float* probs, void* act) {
+    BlockArgs a = block_args(d, L, l, in_dim, 2 * inter, ulora, act);
+    a.probs = probs;
+    a.I = inter;
+    return a;
+}
+
 constexpr int64_t kScratchBytes = EP_NOALLOC_SCRATCH_BYTES;
 
 // Device address of `scratch` on the current device, looked up once per
@@ -846,6 +899,191 @@ int ep_expert_gemm_nvfp4(const ep_cfg_t* cfg, const ep_layout_t* layout, int32_t
     a.rowscale = rowscale;
     if ((rc = expert_status(launch_expert_gemm_nvfp4(a, st))) != EP_OK) return rc;
     return zero_pad(d, layout, y, (int64_t)out_dim * 2, st);
+}
+
+int ep_lora_down(const ep_cfg_t* cfg, const ep_layout_t* layout, const ep_lora_t* lora, int32_t in_dim,
+                 const uint16_t* x, void* u, void* stream) {
+    Shape d;
+    int rc = derive(cfg, &d);
+    if (rc != EP_OK) return rc;
+    if ((rc = check_block(d, layout, in_dim, 8, 8)) != EP_OK) return rc;
+    if ((rc = check_lora(d, lora, true, false)) != EP_OK) return rc;
+    if (bad_buffer(x, d.R * in_dim * 2, 16) || bad_buffer(u, d.R * lora->rank * 4, 16)) return EP_EINVAL;
+    if ((rc = check_device()) != EP_OK) return rc;
+    hipStream_t st = static_cast<hipStream_t>(stream);
+    BlockArgs a = block_args(d, layout, lora, in_dim, 8, nullptr, nullptr);
+    a.e.x = x;
+    if ((rc = expert_status(launch_lora_down(a, static_cast<float*>(u), st))) != EP_OK) return rc;
+    return zero_pad(d, layout, u, (int64_t)lora->rank * 4, st);
+}
+
+int ep_lora_bwd_u(const ep_cfg_t* cfg, const ep_layout_t* layout, const ep_lora_t* lora, int32_t out_dim,
+                  const uint16_t* grad_y, void* grad_u, void* stream) {
+    Shape d;
+    int rc = derive(cfg, &d);
+    if (rc != EP_OK) return rc;
+    if ((rc = check_block(d, layout, 8, out_dim, 8)) != EP_OK) return rc;
+    if ((rc = check_lora(d, lora, false, true)) != EP_OK) return rc;
+    if (bad_buffer(grad_y, d.R * out_dim * 2, 16) || bad_buffer(grad_u, d.R * lora->rank * 4, 16)) return EP_EINVAL;
+    if ((rc = check_device()) != EP_OK) return rc;
+    hipStream_t st = static_cast<hipStream_t>(stream);
+    BlockArgs a = block_args(d, layout, lora, 8, out_dim, nullptr, nullptr);
+    a.e.gy = grad_y;
+    if ((rc = expert_status(launch_lora_bwd_u(a, static_cast<float*>(grad_u), st))) != EP_OK) return rc;
+    return zero_pad(d, layout, grad_u, (int64_t)lora->rank * 4, st);
+}
+
+int ep_expert_gemm_lora(const ep_cfg_t* cfg, const ep_layout_t* layout, const ep_lora_t* lora, int32_t in_dim,
+                        int32_t out_dim, const uint16_t* x, const uint16_t* w, const void* u, uint16_t* y, void* stream) {
+    Shape d;
+    int rc = derive(cfg, &d);
+    if (rc != EP_OK) return rc;
+    if ((rc = check_block(d, layout, in_dim, out_dim, 8)) != EP_OK) return rc;
+    if ((rc = check_lora(d, lora, false, true)) != EP_OK) return rc;
+    if (bad_buffer(x, d.R * in_dim * 2, 16) || bad_buffer(w, 16, 16) || bad_buffer(u, d.R * lora->rank * 4, 16) ||
+        bad_buffer(y, d.R * out_dim * 2, 16))
+        return EP_EINVAL;
+    if ((rc = check_device()) != EP_OK) return rc;
+    hipStream_t st = static_cast<hipStream_t>(stream);
+    BlockArgs a = block_args(d, layout, lora, in_dim, out_dim, u, y);
+    a.e.x = x;
+    a.e.w = w;
+    if ((rc = expert_status(launch_gemm_lora(a, st))) != EP_OK) return rc;
+    return zero_pad(d, layout, y, (int64_t)out_dim * 2, st);
+}
+
+int ep_expert_gemm_nvfp4_lora(const ep_cfg_t* cfg, const ep_layout_t* layout, const ep_lora_t* lora, int32_t in_dim,
+                              int32_t out_dim, const uint16_t* x, const uint8_t* codes, const uint8_t* scales,
+                              const uint16_t* rowscale, const void* u, uint16_t* y, void* stream) {
+    Shape d;
+    int rc = derive(cfg, &d);
+    if (rc != EP_OK) return rc;
+    if ((rc = check_block(d, layout, in_dim, out_dim, 16)) != EP_OK) return rc;
+    if ((rc = check_lora(d, lora, false, true)) != EP_OK) return rc;
+    if (bad_buffer(x, d.R * in_dim * 2, 16) || bad_buffer(codes, 16, 16) || bad_buffer(scales, 16, 16) ||
+        bad_buffer(rowscale, 8, 8) || bad_buffer(u, d.R * lora->rank * 4, 16) || bad_buffer(y, d.R * out_dim * 2, 16))
+        return EP_EINVAL;
+    if ((rc = check_device()) != EP_OK) return rc;
+    hipStream_t st = static_cast<hipStream_t>(stream);
+    BlockArgs a = block_args(d, layout, lora, in_dim, out_dim, u, y);
+    a.e.x = x;
+    a.e.codes = codes;
+    a.e.scales = scales;
+    a.e.rowscale = rowscale;
+    if ((rc = expert_status(launch_gemm_nvfp4_lora(a, st))) != EP_OK) return rc;
+    return zero_pad(d, layout, y, (int64_t)out_dim * 2, st);
+}
+
+int ep_expert_gemm_bwd_x_lora(const ep_cfg_t* cfg, const ep_layout_t* layout, const ep_lora_t* lora, int32_t in_dim,
+                              int32_t out_dim, const uint16_t* grad_y, const uint16_t* w, const void* grad_u,
+                              uint16_t* grad_x, void* stream) {
+    Shape d;
+    int rc = derive(cfg, &d);
+    if (rc != EP_OK) return rc;
+    if ((rc = check_block(d, layout, in_dim, out_dim, 8)) != EP_OK) return rc;
+    if ((rc = check_lora(d, lora, true, false)) != EP_OK) return rc;
+    if (bad_buffer(grad_y, d.R * out_dim * 2, 16) || bad_buffer(w, 16, 16) ||
+        bad_buffer(grad_u, d.R * lora->rank * 4, 16) || bad_buffer(grad_x, d.R * in_dim * 2, 16))
+        return EP_EINVAL;
+    if ((rc = check_device()) != EP_OK) return rc;
+    hipStream_t st = static_cast<hipStream_t>(stream);
+    BlockArgs a = block_args(d, layout, lora, in_dim, out_dim, grad_u, grad_x);
+    a.e.gy = grad_y;
+    a.e.w = w;
+    if ((rc = expert_status(launch_gemm_bwd_x_lora(a, st))) != EP_OK) return rc;
+    return zero_pad(d, layout, grad_x, (int64_t)in_dim * 2, st);
+}
+
+int ep_lora_bwd_w(const ep_cfg_t* cfg, const ep_layout_t* layout, const ep_lora_t* lora, int32_t in_dim,
+                  int32_t out_dim, const uint16_t* x, const uint16_t* grad_y, const void* u, const void* grad_u,
+                  void* grad_a, void* grad_b, int32_t grad_type, void* stream) {
+    Shape d;
+    int rc = derive(cfg, &d);
+    if (rc != EP_OK) return rc;
+    if ((rc = check_block(d, layout, in_dim, out_dim, 8)) != EP_OK) return rc;
+    if ((rc = check_lora(d, lora, false, false)) != EP_OK) return rc;
+    if (grad_type != EP_GRAD_BF16 && grad_type != EP_GRAD_F32 && grad_type != EP_GRAD_F32_ADD) return EP_EINVAL;
+    if (bad_buffer(x, d.R * in_dim * 2, 16) || bad_buffer(grad_y, d.R * out_dim * 2, 16) ||
+        bad_buffer(u, d.R * lora->rank * 4, 16) || bad_buffer(grad_u, d.R * lora->rank * 4, 16) ||
+        bad_buffer(grad_a, 16, 16) || bad_buffer(grad_b, 16, 16))
+        return EP_EINVAL;
+    if ((rc = check_device()) != EP_OK) return rc;
+    BlockArgs a = block_args(d, layout, lora, in_dim, out_dim, u, nullptr);
+    a.e.x = x;
+    a.e.gy = grad_y;
+    a.e.grad_type = grad_type;
+    return expert_status(launch_lora_bwd_w(a, static_cast<const float*>(grad_u), grad_a, grad_b,
+                                           static_cast<hipStream_t>(stream)));
+}
+
+int ep_expert_gated(const ep_cfg_t* cfg, const ep_layout_t* layout, const ep_lora_t* lora, int32_t in_dim, int32_t inter,
+                    const uint16_t* x, const uint16_t* w, const float* probs, const void* ulora, uint16_t* act,
+                    void* stream) {
+    Shape d;
+    int rc = derive(cfg, &d);
+    if (rc != EP_OK) return rc;
+    if ((rc = check_gated(d, layout, lora, in_dim, inter, 8, ulora, probs)) != EP_OK) return rc;
+    if (bad_buffer(x, d.R * in_dim * 2, 16) || bad_buffer(w, 16, 16) || bad_buffer(act, d.R * inter * 2, 16))
+        return EP_EINVAL;
+    if ((rc = check_device()) != EP_OK) return rc;
+    hipStream_t st = static_cast<hipStream_t>(stream);
+    BlockArgs a = gated_args(d, layout, lora, in_dim, inter, ulora, probs, act);
+    a.e.x = x;
+    a.e.w = w;
+    if ((rc = expert_status(launch_gated(a, st))) != EP_OK) return rc;
+    return zero_pad(d, layout, act, (int64_t)inter * 2, st);
+}
+
+int ep_expert_gated_nvfp4(const ep_cfg_t* cfg, const ep_layout_t* layout, const ep_lora_t* lora, int32_t in_dim,
+                          int32_t inter, const uint16_t* x, const uint8_t* codes, const uint8_t* scales,
+                          const uint16_t* rowscale, const float* probs, const void* ulora, uint16_t* act, void* stream) {
+    Shape d;
+    int rc = derive(cfg, &d);
+    if (rc != EP_OK) return rc;
+    if ((rc = check_gated(d, layout, lora, in_dim, inter, 16, ulora, probs)) != EP_OK) return rc;
+    if ((int64_t)inter * in_dim >= int64_t(1) << 34) return EP_EINVAL;  // an expert's scales are reached by 32-bit offsets
+    if (bad_buffer(x, d.R * in_dim * 2, 16) || bad_buffer(codes, 16, 16) || bad_buffer(scales, 16, 16) ||
+        bad_buffer(rowscale, 8, 8) || bad_buffer(act, d.R * inter * 2, 16))
+        return EP_EINVAL;
+    if ((rc = check_device()) != EP_OK) return rc;
+    hipStream_t st = static_cast<hipStream_t>(stream);
+    BlockArgs a = gated_args(d, layout, lora, in_dim, inter, ulora, probs, act);
+    a.e.x = x;
+    a.e.codes = codes;
+    a.e.scales = scales;
+    a.e.rowscale = rowscale;
+    if ((rc = expert_status(launch_gated_nvfp4(a, st))) != EP_OK) return rc;
+    return zero_pad(d, layout, act, (int64_t)inter * 2, st);
+}
+
+int ep_expert_gated_bwd(const ep_cfg_t* cfg, const ep_layout_t* layout, const ep_lora_t* lora, int32_t in_dim,
+                        int32_t inter, const uint16_t* x, const uint16_t* w, const float* probs, const void* ulora,
+                        const uint16_t* grad_act, uint16_t* grad_h, uint16_t* act, float* grad_probs, void* workspace,
+                        int64_t workspace_bytes, void* stream) {
+    Shape d;
+    int rc = derive(cfg, &d);
+    if (rc != EP_OK) return rc;
+    if ((rc = check_gated(d, layout, lora, in_dim, inter, 8, ulora, probs)) != EP_OK) return rc;
+    if (bad_buffer(x, d.R * in_dim * 2, 16) || bad_buffer(w, 16, 16) || bad_buffer(grad_act, d.R * inter * 2, 16) ||
+        bad_buffer(grad_h, d.R * inter * 4, 16) || misaligned(act, 16))
+        return EP_EINVAL;
+    if (grad_probs != nullptr) {
+        const int64_t need = (int64_t)d.T * d.K * ((inter + EP_GATED_PART - 1) / EP_GATED_PART) * 4;
+        if (misaligned(grad_probs, 4) || workspace_bytes < need || bad_buffer(workspace, need, 16)) return EP_EINVAL;
+        if (bad_buffer(layout->token_row, (int64_t)d.T * d.Kp * 4, 4)) return EP_EINVAL;
+    }
+    if ((rc = check_device()) != EP_OK) return rc;
+    hipStream_t st = static_cast<hipStream_t>(stream);
+    BlockArgs a = gated_args(d, layout, lora, in_dim, inter, ulora, probs, act);
+    a.e.x = x;
+    a.e.w = w;
+    a.grad_act = grad_act;
+    a.grad_h = grad_h;
+    a.grad_probs = grad_probs;
+    a.parts = grad_probs != nullptr ? static_cast<float*>(workspace) : nullptr;
+    if ((rc = expert_status(launch_gated_bwd(a, st))) != EP_OK) return rc;
+    if (act != nullptr && (rc = zero_pad(d, layout, act, (int64_t)inter * 2, st)) != EP_OK) return rc;
+    return zero_pad(d, layout, grad_h, (int64_t)inter * 4, st);
 }
 
 }  // extern "C"

@@ -420,6 +420,41 @@ hipError_t launch_expert_gemm_bwd_x(const ExpertArgs& a, hipStream_t stream);
 hipError_t launch_expert_gemm_bwd_w(const ExpertArgs& a, hipStream_t stream);
 hipError_t launch_expert_gemm_nvfp4(const ExpertArgs& a, hipStream_t stream);
 
+struct LoraArgs {                // low-rank adapters (ep_lora_t)
+    const int32_t* token_adapter;  // [T]
+    const uint16_t* a;             // [n, E + shared, rank, in]
+    const uint16_t* b;             // [n, E + shared, out, rank]
+    const float* scale;            // [n] or nullptr: 1
+    int32_t n, rank;               // rank 0: no adapters
+};
+
+struct BlockArgs {               // the gated block, and the products with adapters
+    ExpertArgs e;                // e.out: act, y or grad_x; gated: e.on = 2 * I
+    LoraArgs l;
+    const float* u;              // [R, rank]: of the rows (input's gradient: grad_u)
+    const int32_t* src_info;     // [R, 2]
+    const int32_t* token_row;    // [T, K'] (grad_probs)
+    const float* probs;          // [T, K] or nullptr: weight 1
+    const uint16_t* grad_act;    // gated backward: [R, I]
+    uint16_t* grad_h;            //   [R, 2I]
+    float* parts;                //   [T, K, ceil(I / kGatedPart)] or nullptr
+    float* grad_probs;           //   [T, K] or nullptr
+    int32_t T, K, Kp, I;
+};
+constexpr int kGatedPart = EP_GATED_PART;  // columns of act in one part of a weight's gradient
+hipError_t launch_gated(const BlockArgs& a, hipStream_t stream);
+hipError_t launch_gated_nvfp4(const BlockArgs& a, hipStream_t stream);
+hipError_t launch_gated_bwd(const BlockArgs& a, hipStream_t stream);
+hipError_t launch_gemm_lora(const BlockArgs& a, hipStream_t stream);
+hipError_t launch_gemm_nvfp4_lora(const BlockArgs& a, hipStream_t stream);
+hipError_t launch_gemm_bwd_x_lora(const BlockArgs& a, hipStream_t stream);
+
+// u [R, rank] = scale A x (ep_lora_down), or scale B^T grad_y (ep_lora_bwd_u; e.gy).
+hipError_t launch_lora_down(const BlockArgs& a, float* u, hipStream_t stream);
+hipError_t launch_lora_bwd_u(const BlockArgs& a, float* grad_u, hipStream_t stream);
+// The adapters' gradients, of e.grad_type, from e.x, e.gy, a.u and grad_u.
+hipError_t launch_lora_bwd_w(const BlockArgs& a, const float* grad_u, void* grad_a, void* grad_b, hipStream_t stream);
+
 // Zero the payload bytes of every pad row ([count, align_up(count)) of each
 // group, below capacity).  row_bytes = bytes of one row of `base`.
 hipError_t launch_zero_pad_rows(void* base, int64_t row_bytes, const ep_layout_t& L, int32_t S,

@@ -55,6 +55,13 @@ __device__ __forceinline__ void load_to_lds(const void* base, int32_t bytes, con
 }
 #pragma clang diagnostic pop
 
+// Results of matrix instructions kept in accumulation registers from here on.
+__device__ __forceinline__ void in_agprs(f32x4& v) {
+#ifdef __HIP_DEVICE_COMPILE__
+    asm volatile("" : "+a"(v));
+#endif
+}
+
 // A group's rows in the receive buffers, whatever the layout holds: [first,
 // first + rows) lies inside [0, R).
 struct GroupRows {

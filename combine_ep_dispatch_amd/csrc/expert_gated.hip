@@ -1,0 +1,134 @@
+// The experts' gated block in one kernel, bf16 weights (gate rows, then up rows):
+//   g = x[r] . w[e, i, :],  u = x[r] . w[e, I + i, :]
+//   act[r, i] = w_r silu(g) u,   silu(g) = g s,   s = 1 / (1 + exp(-g))
+// and its backward pass, which makes g and u again from x and w:
+//   grad_h[r, i] = w_r ga u s (1 + g (1 - s)),   grad_h[r, I + i] = w_r ga g s
+//   grad_probs[t, k] = sum_i ga silu(g) u
+// g and u are not rounded between the product and the activation.  Low-rank
+// adapters, if any, add to g and u before it.
+#include "expert_loop.h"
+#include "gated_device.h"
+
+namespace epx {
+namespace {
+
+template <int KF, int KN>
+__device__ __forceinline__ void adapters_of(const BlockArgs& a, const RowTile& t, int32_t c0, int32_t wn, f32x4 (&acc)[KF][KN]) {
+    const int i = threadIdx.x % 16;
+    add_adapters<KF, KN>(a, t.first, t.rows, wn, [&](int f, int32_t ad, int32_t c) {
+        const int32_t col = c0 + f / 2 * 16 + i;  // of act
+        const int64_t expert = (int64_t)ad * (a.e.E + a.e.shared) + t.expert;
+        if (col >= a.I) return bf16x8{};
+        return *reinterpret_cast<const bf16x8*>(a.l.b + (expert * a.e.on + f % 2 * a.I + col) * a.l.rank + c * 8);
+    }, acc);
+}
+
+// BACKWARD: grad_h and the weights' gradients from grad_act (and act again, if wanted).
+template <bool BACKWARD, bool LORA>
+__global__ __launch_bounds__(kLoopThreads) __attribute__((amdgpu_waves_per_eu(1, 1))) void k_gated(BlockArgs a, int32_t ftiles) {
+    __shared__ __align__(1024) uint16_t lds[kLoopLds / 2];
+    int32_t ft;
+    const RowTile t = find_row_tile<kLoopThreads, kTileN>(
+        a.e, reinterpret_cast<int32_t*>(lds), [&](int32_t rt, int32_t& f) { return xcd_tile(rt, ftiles, f); }, ft);
+    if (t.expert < 0) return;
+    __syncthreads();  // the words that named the tile become step 0
+    const int lane = threadIdx.x & (kWave - 1), i = lane % 16, q = lane / 16;
+    const int32_t a0 = ft * (kTileF / 2), I = a.I;
+    GatedOperand fo;
+    fo.init(a.e.w + (int64_t)t.expert * a.e.on * a.e.in, a0, I, a.e.in);
+    by_rows(t.rows, [&](auto nt) {
+        constexpr int NT = decltype(nt)::value, KF = Shape<NT>::kF, KN = Shape<NT>::kN;
+        const int wf = Shape<NT>::wf(), wn = Shape<NT>::wn();
+        RowsOperand<NT, kLoopWaves> no;
+        no.init(a.e.x + t.first * a.e.in, t.rows, a.e.in, a.e.in);
+        f32x4 acc[KF][KN] = {};
+        const int32_t c0 = a0 + wf / 2;  // the wave's first column of act
+        tile_loop<GatedOperand, RowsOperand<NT, kLoopWaves>, NT>(fo, no, lds, wf, wn, a.e.in, acc, [&] {
+            if constexpr (LORA) adapters_of(a, t, c0, wn, acc);
+        });
+        // acc[2 p][n][j], acc[2 p + 1][n][j]: g and u of column c0 + 16 p + 4 q + j, row wn + 16 n + i
+        uint16_t* const act = static_cast<uint16_t*>(a.e.out);
+#pragma unroll
+        for (int n = 0; n < KN; ++n) {
+            const int32_t row = wn + n * 16 + i;
+            const bool on = row < t.rows;
+            const int64_t r = t.first + row;
+            int64_t slot = -1;
+            const float w = on ? row_weight(a, r, slot) : 0.0f;
+            float sum = 0.0f;
+#pragma unroll
+            for (int p = 0; p < KF / 2; ++p) {
+                const int32_t c = c0 + p * 16 + q * 4;
+                if (!on || c >= I) continue;
+                const f32x4 g = acc[2 * p][n], u = acc[2 * p + 1][n];
+                float y[4], gg[4], gu[4];
+                v2u ga = {};
+                if constexpr (BACKWARD) ga = *reinterpret_cast<const v2u*>(a.grad_act + r * I + c);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const float s = fast_sigmoid(g[j]), silu = g[j] * s;
+                    y[j] = w * (silu * u[j]);
+                    if constexpr (BACKWARD) {
+                        const float d = j % 2 ? bf16_hi(ga[j / 2]) : bf16_lo(ga[j / 2]), wd = w * d;
+                        sum += d * (silu * u[j]);
+                        gg[j] = wd * u[j] * (s * (1.0f + g[j] * (1.0f - s)));
+                        gu[j] = wd * silu;
+                    }
+                }
+                if (act != nullptr)
+                    *reinterpret_cast<v2u*>(act + r * I + c) = v2u{pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3])};
+                if constexpr (BACKWARD) {
+                    uint16_t* const gh = a.grad_h + r * 2 * I + c;
+                    *reinterpret_cast<v2u*>(gh) = v2u{pack_bf16x2(gg[0], gg[1]), pack_bf16x2(gg[2], gg[3])};
+                    *reinterpret_cast<v2u*>(gh + I) = v2u{pack_bf16x2(gu[0], gu[1]), pack_bf16x2(gu[2], gu[3])};
+                }
+            }
+            if constexpr (BACKWARD) {
+                if (a.parts == nullptr) continue;
+                sum += __shfl_xor(sum, 16, kWave);
+                sum += __shfl_xor(sum, 32, kWave);
+                // the wave's columns are KF / 4 parts: the sum in the first, zeros in the others
+                const int32_t parts = (I + kGatedPart - 1) / kGatedPart, part = c0 / kGatedPart + q;
+                if (q < KF / 4 && slot >= 0 && part < parts) a.parts[slot * parts + part] = q == 0 ? sum : 0.0f;
+            }
+        }
+    });
+}
+
+// grad_probs[t, k]: the parts of the slot's row in order; 0 where the slot has none.
+__global__ __launch_bounds__(256) void k_gated_probs(BlockArgs a) {
+    const int64_t at = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    if (at >= (int64_t)a.T * a.K) return;
+    const int32_t row = a.token_row[at / a.K * a.Kp + at % a.K], parts = (a.I + kGatedPart - 1) / kGatedPart;
+    float sum = 0.0f;
+    if (row >= 0 && row < a.e.R)
+        for (int32_t p = 0; p < parts; ++p) sum += a.parts[at * parts + p];
+    a.grad_probs[at] = sum;
+}
+
+template <bool BACKWARD>
+hipError_t gated(const BlockArgs& a, hipStream_t stream) {
+    const int32_t ftiles = (a.I + kTileF / 2 - 1) / (kTileF / 2);
+    const int64_t blocks = (max_row_tiles(a.e, kTileN) * ftiles + 7) / 8 * 8;
+    if (blocks == 0) return hipSuccess;
+    if (const hipError_t e = check_grid(blocks, kLoopThreads)) return e;
+    if (a.l.rank > 0)
+        hipLaunchKernelGGL((k_gated<BACKWARD, true>), dim3((unsigned)blocks), dim3(kLoopThreads), 0, stream, a, ftiles);
+    else
+        hipLaunchKernelGGL((k_gated<BACKWARD, false>), dim3((unsigned)blocks), dim3(kLoopThreads), 0, stream, a, ftiles);
+    return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_gated(const BlockArgs& a, hipStream_t stream) { return gated<false>(a, stream); }
+
+hipError_t launch_gated_bwd(const BlockArgs& a, hipStream_t stream) {
+    if (const hipError_t e = gated<true>(a, stream)) return e;
+    const int64_t slots = (int64_t)a.T * a.K;
+    if (a.grad_probs == nullptr || slots == 0) return hipSuccess;
+    hipLaunchKernelGGL(k_gated_probs, dim3((unsigned)((slots + 255) / 256)), dim3(256), 0, stream, a);
+    return hipGetLastError();
+}
+
+}  // namespace epx

@@ -1,0 +1,328 @@
+// Low-rank adapters of many requests beside the experts' products.  Row r, of
+// expert e and of a token with adapter d:
+//   u[r] = s_d A[d, e] x[r]                     (k_lora_down)
+//   y[r] = w[e] x[r] + B[d, e] u[r]             (k_product, forward)
+// and the gradients, w fixed:
+//   gu[r] = s_d B[d, e]^T gy[r]                 (k_lora_down over B)
+//   gx[r] = w[e]^T gy[r] + A[d, e]^T gu[r]      (k_product, input's gradient)
+//   gA[d, e] = sum_r gu[r]^T x[r],  gB[d, e] = sum_r gy[r]^T u[r]   (k_lora_bwd_w)
+// The second product of an adapter is added to the first results of the experts'
+// own, before anything is rounded.
+#include "expert_loop.h"
+
+namespace epx {
+namespace {
+
+enum Product { kForward, kInputGrad };
+
+template <Product P>
+__global__ __launch_bounds__(kLoopThreads) __attribute__((amdgpu_waves_per_eu(1, 1))) void k_product(BlockArgs a, int32_t ftiles) {
+    using FOp = typename std::conditional<P == kForward, RowsOperand<kTileF, kLoopWaves>, ColsOperand<kTileF, kLoopWaves>>::type;
+    __shared__ __align__(1024) uint16_t lds[kLoopLds / 2];
+    int32_t ft;
+    const RowTile t = find_row_tile<kLoopThreads, kTileN>(
+        a.e, reinterpret_cast<int32_t*>(lds), [&](int32_t rt, int32_t& f) { return xcd_tile(rt, ftiles, f); }, ft);
+    if (t.expert < 0) return;
+    __syncthreads();  // the words that named the tile become step 0
+    const int lane = threadIdx.x & (kWave - 1), i = lane % 16, q = lane / 16;
+    const int32_t f0 = ft * kTileF, F = P == kForward ? a.e.on : a.e.in, L = P == kForward ? a.e.in : a.e.on;
+    const uint16_t* const we = a.e.w + (int64_t)t.expert * a.e.on * a.e.in;
+    FOp fo;
+    if constexpr (P == kForward)
+        fo.init(we + (int64_t)f0 * L, min(kTileF, F - f0), L, L);
+    else
+        fo.init(we + f0, F - f0, F, L, f0);
+    by_rows(t.rows, [&](auto nt) {
+        constexpr int NT = decltype(nt)::value, KF = Shape<NT>::kF, KN = Shape<NT>::kN;
+        const int wf = Shape<NT>::wf(), wn = Shape<NT>::wn();
+        RowsOperand<NT, kLoopWaves> no;
+        no.init((P == kForward ? a.e.x : a.e.gy) + t.first * L, t.rows, L, L);
+        f32x4 acc[KF][KN] = {};
+        tile_loop<FOp, RowsOperand<NT, kLoopWaves>, NT>(fo, no, lds, wf, wn, L, acc, [&] {
+            add_adapters<KF, KN>(a, t.first, t.rows, wn, [&](int f, int32_t ad, int32_t c) {
+                const int32_t fe = f0 + wf + f * 16 + i, rank = a.l.rank;
+                const int64_t pair = (int64_t)ad * (a.e.E + a.e.shared) + t.expert;
+                bf16x8 v = {};
+                if (fe >= F) return v;
+                if constexpr (P == kForward) {
+                    v = *reinterpret_cast<const bf16x8*>(a.l.b + (pair * F + fe) * rank + c * 8);
+                } else {
+                    const __bf16* const p = reinterpret_cast<const __bf16*>(a.l.a) + (pair * rank + c * 8) * F + fe;
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) v[k] = p[(int64_t)k * F];
+                }
+                return v;
+            }, acc);
+        });
+        // acc[f][n][j]: feature f0 + wf + 16 f + 4 q + j, row wn + 16 n + i
+#pragma unroll
+        for (int n = 0; n < KN; ++n) {
+            const int32_t row = wn + n * 16 + i;
+            if (row >= t.rows) continue;
+            uint16_t* const out = static_cast<uint16_t*>(a.e.out) + (t.first + row) * F;
+#pragma unroll
+            for (int f = 0; f < KF; ++f) {
+                const int32_t fe = f0 + wf + f * 16 + q * 4;
+                if (fe < F)
+                    *reinterpret_cast<v2u*>(out + fe) =
+                        v2u{pack_bf16x2(acc[f][n][0], acc[f][n][1]), pack_bf16x2(acc[f][n][2], acc[f][n][3])};
+            }
+        }
+    });
+}
+
+template <Product P>
+hipError_t product(const BlockArgs& a, hipStream_t stream) {
+    const int32_t F = P == kForward ? a.e.on : a.e.in, ftiles = (F + kTileF - 1) / kTileF;
+    const int64_t blocks = (max_row_tiles(a.e, kTileN) * ftiles + 7) / 8 * 8;
+    if (blocks == 0) return hipSuccess;
+    if (const hipError_t e = check_grid(blocks, kLoopThreads)) return e;
+    hipLaunchKernelGGL((k_product<P>), dim3((unsigned)blocks), dim3(kLoopThreads), 0, stream, a, ftiles);
+    return hipGetLastError();
+}
+
+constexpr int kDownWaves = 8;
+constexpr int kDownRows = 16;
+
+// u of 16 rows: each of 8 waves sums its share of L (64 values in turn, 16 a
+// quarter of the wave), and the workgroup adds the eight up in order.  The
+// workgroups of a tile (blockIdx.y) share its adapters: with few tiles, as in a
+// decode step, each adapter's weights are read by a workgroup of their own.
+// BWD: gu, from gy and B, whose values lie along the rank.
+template <bool BWD, int KP>
+__global__ __launch_bounds__(kDownWaves * kWave) void k_lora_down(BlockArgs a, uint16_t* u) {
+    constexpr int P = KP * 16;
+    __shared__ float part[kDownWaves][kDownRows][P + 1];
+    __shared__ int32_t scan[kDownWaves + 3];
+    int32_t none;
+    const RowTile t = find_row_tile<kDownWaves * kWave, kDownRows>(
+        a.e, scan, [&](int32_t rt, int32_t& f) { return xcd_tile(rt, 1, f); }, none);
+    if (t.expert < 0) return;
+    const int lane = threadIdx.x & (kWave - 1), w = uniform((int32_t)(threadIdx.x / kWave)), i = lane % 16, q = lane / 16;
+    const int32_t L = BWD ? a.e.on : a.e.in, rank = a.l.rank;
+    const uint16_t* const x = (BWD ? a.e.gy : a.e.x) + (t.first + i) * L;
+    int32_t ad[1] = {i < t.rows ? row_adapter(a, t.first + i) : -1};
+    // what this thread writes: value p of row r
+    constexpr int kThreads = kDownWaves * kWave, kMine = (kDownRows * P + kThreads - 1) / kThreads;
+    auto out = [&](int m, int& r, int& p) {
+        const int at = m * kThreads + threadIdx.x;
+        r = at / P;
+        p = at % P;
+        return r < t.rows && p < rank;
+    };
+    int32_t at = 0;
+    for (int32_t cur = next_adapter(ad, -1);; cur = next_adapter(ad, cur), ++at) {
+        if (cur == kNoAdapter) break;
+        if (at % gridDim.y != blockIdx.y) continue;
+        const int64_t pair = (int64_t)cur * (a.e.E + a.e.shared) + t.expert;
+        const uint16_t* const f = (BWD ? a.l.b : a.l.a) + pair * rank * L;
+        f32x4 acc[KP] = {};
+        for (int32_t l0 = w * 64; l0 < L; l0 += kDownWaves * 64) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int32_t l = l0 + q * 16 + h * 8;
+                bf16x8 xv = {}, fv[KP] = {};
+                if (l < L && ad[0] == cur) xv = *reinterpret_cast<const bf16x8*>(x + l);
+#pragma unroll
+                for (int k = 0; k < KP; ++k) {
+                    const int32_t p = k * 16 + i;
+                    if (l >= L || p >= rank) continue;
+                    if constexpr (BWD) {
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) fv[k][j] = reinterpret_cast<const __bf16*>(f)[(l + j) * (int64_t)rank + p];
+                    } else {
+                        fv[k] = *reinterpret_cast<const bf16x8*>(f + (int64_t)p * L + l);
+                    }
+                }
+#pragma unroll
+                for (int k = 0; k < KP; ++k) acc[k] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fv[k], xv, acc[k], 0, 0, 0);
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < KP; ++k)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) part[w][i][k * 16 + q * 4 + j] = acc[k][j];
+        __syncthreads();
+        const float s = a.l.scale != nullptr ? a.l.scale[cur] : 1.0f;
+#pragma unroll
+        for (int m = 0; m < kMine; ++m) {
+            int r, p;
+            if (!out(m, r, p)) continue;
+            if (row_adapter(a, t.first + r) != cur) continue;
+            float v = 0.0f;
+#pragma unroll
+            for (int k = 0; k < kDownWaves; ++k) v += part[k][r][p];
+            const uint32_t two = split_bf16(s * v);
+            uint16_t* const to = u + (t.first + r) * 2 * rank + p;
+            to[0] = (uint16_t)two;
+            to[rank] = (uint16_t)(two >> 16);
+        }
+        __syncthreads();
+    }
+    if (blockIdx.y != 0) return;
+    // rows without an adapter: zeros
+#pragma unroll
+    for (int m = 0; m < kMine; ++m) {
+        int r, p;
+        if (!out(m, r, p) || row_adapter(a, t.first + r) >= 0) continue;
+        uint16_t* const to = u + (t.first + r) * 2 * rank + p;
+        to[0] = to[rank] = 0;
+    }
+}
+
+template <bool BWD, int KP>
+hipError_t down(const BlockArgs& a, float* u, hipStream_t stream) {
+    const int64_t tiles = max_row_tiles(a.e, kDownRows), blocks = (tiles + 7) / 8 * 8;
+    if (blocks == 0) return hipSuccess;
+    const int share = tiles <= 512 ? (a.l.n < kDownRows ? a.l.n : kDownRows) : 1;
+    if (const hipError_t e = check_grid(blocks, kDownWaves * kWave)) return e;
+    hipLaunchKernelGGL((k_lora_down<BWD, KP>), dim3((unsigned)blocks, (unsigned)share), dim3(kDownWaves * kWave), 0, stream, a,
+                       reinterpret_cast<uint16_t*>(u));
+    return hipGetLastError();
+}
+
+template <bool BWD>
+hipError_t down_by_rank(const BlockArgs& a, float* u, hipStream_t stream) {
+    if (a.l.rank <= 16) return down<BWD, 1>(a, u, stream);
+    if (a.l.rank <= 32) return down<BWD, 2>(a, u, stream);
+    if (a.l.rank <= 64) return down<BWD, 4>(a, u, stream);
+    return down<BWD, 8>(a, u, stream);
+}
+
+constexpr int kGradThreads = 256, kGradRows = 64, kGradCols = 256;  // rows a step, columns of a tile
+constexpr int kList = 512;                                          // rows looked through at a time
+
+// Gradients of one adapter's weights of one expert, columns c0 on: sum over the
+// rows r of the expert whose tokens have the adapter of v[r]^T d[r], d = x (of
+// width in; result [rank, in]) or gy (out; result [out, rank]), v = gu or u.  The
+// rows are picked out in order, 64 a step; d's go through registers to LDS.
+template <int KP, bool OUT>
+__global__ __launch_bounds__(kGradThreads) void k_lora_bwd_w(BlockArgs a, const uint16_t* v, void* out, int32_t ctiles) {
+    using XOp = ColsOperand<kGradCols, 4>;
+    using VOp = ColsOperand<KP * 32, 4>;  // the rounded values, then the rests
+    constexpr int P = KP * 16;
+    __shared__ __align__(1024) uint16_t xs[kGradRows * kGradCols], vs[kGradRows * P * 2];
+    __shared__ int32_t list[kList + kGradRows], counts[5];
+    const int lane = threadIdx.x & (kWave - 1), w = uniform((int32_t)(threadIdx.x / kWave)), i = lane % 16, q = lane / 16;
+    const int32_t EX = a.e.E + a.e.shared, rank = a.l.rank, C = OUT ? a.e.on : a.e.in;
+    const int32_t ct = blockIdx.x % ctiles, pair = blockIdx.x / ctiles, ad = pair / EX, expert = pair % EX, c0 = ct * kGradCols;
+    const int32_t g = expert < a.e.E ? expert / a.e.E_loc * a.e.G + a.e.shared + expert % a.e.E_loc : a.e.src_seg * a.e.G;
+    const GroupRows rows = group_rows(a.e, g);
+    const uint16_t* const d = (OUT ? a.e.gy : a.e.x) + rows.first * C + c0;
+    const uint16_t* const vv = v + rows.first * 2 * rank;
+    f32x4 acc[4][KP] = {};
+    int32_t have = 0;  // rows in the list
+    for (int32_t r0 = 0; r0 < rows.rows || have > 0; r0 += kList) {
+        // append the next rows' matches
+        for (int32_t b = r0; b < min(r0 + kList, rows.rows); b += kGradThreads) {
+            const int32_t r = b + (int32_t)threadIdx.x;
+            const bool mine = r < rows.rows && row_adapter(a, rows.first + r) == ad;
+            const uint64_t m = __builtin_amdgcn_ballot_w64(mine);
+            if (lane == 0) counts[w] = __popcll(m);
+            __syncthreads();
+            int32_t at = have;
+            for (int k = 0; k < 4; ++k) {
+                if (k == w && mine) list[at + lanes_below(m)] = r;
+                at += counts[k];
+            }
+            have = at;
+            __syncthreads();
+        }
+        const bool last = r0 + kList >= rows.rows;
+        int32_t done = 0;
+        for (; have - done >= kGradRows || (last && done < have); done += kGradRows) {
+            const int32_t n = min(kGradRows, have - done);
+            // d: 64 rows of 32 chunks of 8 values, one a thread and turn
+#pragma unroll
+            for (int k = 0; k < kGradRows * kGradCols / 8 / kGradThreads; ++k) {
+                const int at = k * kGradThreads + threadIdx.x, r = at / 32, c = at % 32;
+                v4u o = {};
+                if (r < n && c0 + c * 8 < C) o = *reinterpret_cast<const v4u*>(d + (int64_t)list[done + r] * C + c * 8);
+                *reinterpret_cast<v4u*>(xs + r * kGradCols + (((c / 2) ^ XOp::swizzle(r)) * 2 + c % 2) * 8) = o;
+            }
+            // v: 64 rows of KP * 4 chunks
+#pragma unroll
+            for (int k = 0; k < KP; ++k) {
+                const int at = k * kGradThreads + threadIdx.x, r = at / (KP * 4), c = at % (KP * 4);
+                const int half = c / (KP * 2), p = c % (KP * 2) * 8;
+                v4u o = {};
+                if (r < n && p < rank) o = *reinterpret_cast<const v4u*>(vv + (int64_t)list[done + r] * 2 * rank + half * rank + p);
+                *reinterpret_cast<v4u*>(vs + r * P * 2 + (((c / 2) ^ VOp::swizzle(r)) * 2 + c % 2) * 8) = o;
+            }
+            __syncthreads();
+#pragma unroll
+            for (int kk = 0; kk < 2; ++kk) {
+                bf16x8 xf[4];
+#pragma unroll
+                for (int f = 0; f < 4; ++f) xf[f] = XOp::fragment(xs, w * 64 + f * 16, kk);
+#pragma unroll
+                for (int k = 0; k < 2 * KP; ++k) {
+                    const bf16x8 vf = VOp::fragment(vs, k * 16, kk);
+#pragma unroll
+                    for (int f = 0; f < 4; ++f) {
+                        f32x4& s = acc[f][k % KP];
+                        s = OUT ? __builtin_amdgcn_mfma_f32_16x16x32_bf16(vf, xf[f], s, 0, 0, 0)
+                                : __builtin_amdgcn_mfma_f32_16x16x32_bf16(xf[f], vf, s, 0, 0, 0);
+                    }
+                }
+            }
+            __syncthreads();
+        }
+        // what is left of the list moves to its front
+        const int32_t left = max(have - done, 0);
+        int32_t keep = 0;
+        if ((int32_t)threadIdx.x < left) keep = list[done + threadIdx.x];
+        __syncthreads();
+        if ((int32_t)threadIdx.x < left) list[threadIdx.x] = keep;
+        have = left;
+        __syncthreads();
+    }
+    // acc[f][k][j]: column c = c0 + 64 w + 16 f + .., value p = 16 k + .. of the rank;
+    // the four of a lane lie along the result's rows
+#pragma unroll
+    for (int f = 0; f < 4; ++f)
+#pragma unroll
+        for (int k = 0; k < KP; ++k) {
+            const int32_t c = c0 + w * 64 + f * 16 + (OUT ? i : q * 4), p = k * 16 + (OUT ? q * 4 : i);
+            if (c >= C || p >= rank) continue;
+            const int64_t at = (int64_t)pair * rank * C + (OUT ? (int64_t)c * rank + p : (int64_t)p * C + c);
+            const f32x4 s = acc[f][k];
+            if (a.e.grad_type == EP_GRAD_BF16) {
+                *reinterpret_cast<v2u*>(static_cast<uint16_t*>(out) + at) = v2u{pack_bf16x2(s[0], s[1]), pack_bf16x2(s[2], s[3])};
+            } else {
+                f32x4* const o = reinterpret_cast<f32x4*>(static_cast<float*>(out) + at);
+                *o = a.e.grad_type == EP_GRAD_F32_ADD ? *o + s : s;
+            }
+        }
+}
+
+template <int KP, bool OUT>
+hipError_t bwd_w(const BlockArgs& a, const float* v, void* out, hipStream_t stream) {
+    const int32_t ctiles = ((OUT ? a.e.on : a.e.in) + kGradCols - 1) / kGradCols;
+    const int64_t blocks = (int64_t)a.l.n * (a.e.E + a.e.shared) * ctiles;
+    if (const hipError_t e = check_grid(blocks, kGradThreads)) return e;
+    hipLaunchKernelGGL((k_lora_bwd_w<KP, OUT>), dim3((unsigned)blocks), dim3(kGradThreads), 0, stream, a,
+                       reinterpret_cast<const uint16_t*>(v), out, ctiles);
+    return hipGetLastError();
+}
+
+template <bool OUT>
+hipError_t bwd_w_by_rank(const BlockArgs& a, const float* v, void* out, hipStream_t stream) {
+    if (a.l.rank <= 16) return bwd_w<1, OUT>(a, v, out, stream);
+    if (a.l.rank <= 32) return bwd_w<2, OUT>(a, v, out, stream);
+    if (a.l.rank <= 64) return bwd_w<4, OUT>(a, v, out, stream);
+    return bwd_w<8, OUT>(a, v, out, stream);
+}
+
+}  // namespace
+
+hipError_t launch_gemm_lora(const BlockArgs& a, hipStream_t stream) { return product<kForward>(a, stream); }
+hipError_t launch_gemm_bwd_x_lora(const BlockArgs& a, hipStream_t stream) { return product<kInputGrad>(a, stream); }
+hipError_t launch_lora_down(const BlockArgs& a, float* u, hipStream_t stream) { return down_by_rank<false>(a, u, stream); }
+hipError_t launch_lora_bwd_u(const BlockArgs& a, float* u, hipStream_t stream) { return down_by_rank<true>(a, u, stream); }
+hipError_t launch_lora_bwd_w(const BlockArgs& a, const float* grad_u, void* grad_a, void* grad_b, hipStream_t stream) {
+    if (const hipError_t e = bwd_w_by_rank<false>(a, grad_u, grad_a, stream)) return e;
+    return bwd_w_by_rank<true>(a, a.u, grad_b, stream);
+}
+
+}  // namespace epx

@@ -1,0 +1,94 @@
+// What the kernels with low-rank adapters share: which adapter a row has, and
+// adding B u (or A^T u) to a wave's results in registers.
+#pragma once
+
+#include "expert_device.h"
+
+namespace epx {
+
+// The adapter of receive row r, -1 for none, whatever the layout and the ids hold.
+__device__ __forceinline__ int32_t row_adapter(const BlockArgs& a, int64_t r) {
+    const int32_t t = a.src_info[2 * r];
+    if (t < 0 || t >= a.T) return -1;
+    const int32_t ad = a.l.token_adapter[t];
+    return ad < 0 || ad >= a.l.n ? -1 : ad;
+}
+
+// The smallest of the adapters `ad` (COUNT of each of the 16 lanes i; the
+// quarters of the wave hold the same) past `last`, kNoAdapter if there is none.
+constexpr int32_t kNoAdapter = INT32_MAX;
+template <int COUNT>
+__device__ __forceinline__ int32_t next_adapter(const int32_t (&ad)[COUNT], int32_t last) {
+    int32_t v = kNoAdapter;
+#pragma unroll
+    for (int n = 0; n < COUNT; ++n) v = ad[n] > last ? min(v, ad[n]) : v;
+#pragma unroll
+    for (int o = 1; o < 16; o <<= 1) v = min(v, __shfl_xor(v, o, kWave));
+    return uniform(v);
+}
+
+// u (and grad_u) travel as two bf16 a value: row r of [R, rank] words holds the
+// rank values rounded to bf16, then what the rounding left.  Their sum has 16
+// significant bits, so that the products with u are as good as 32-bit ones next to
+// the result's 8; one bf16 alone would add a rounding of its own where the
+// adapters make most of the result.  An infinity leaves nothing (not NaN).
+__device__ __forceinline__ uint32_t split_bf16(float v) {  // rounded value low, rest high
+    const uint32_t hi = f32_to_bf16(v);
+    const float rest = __builtin_isinf(bf16_lo(hi)) ? 0.0f : v - bf16_lo(hi);
+    return hi | f32_to_bf16(rest) << 16;
+}
+
+// acc[f][n] += the adapters' part of a wave's results: 16 features a fragment f
+// by 16 rows a fragment n, summed over u rounded to bf16 and then over what the
+// rounding left (2 rank values).  weights(f, ad, c): this lane's 8 values [8 c, 8 c
+// + 8) of the rank of its feature of fragment f.  Every adapter that one of the rows
+// has is multiplied with all of them, and added to its own rows alone: nothing
+// that an adapter or another row holds, infinities and NaN included, reaches a row
+// that does not use it.
+template <int KF, int KN, typename Weights>
+__device__ __forceinline__ void add_adapters(const BlockArgs& a, int64_t first, int32_t rows, int32_t wn, Weights weights,
+                                             f32x4 (&acc)[KF][KN]) {
+    const int lane = threadIdx.x & (kWave - 1), i = lane % 16, q = lane / 16;
+    int32_t ad[KN];
+#pragma unroll
+    for (int n = 0; n < KN; ++n) ad[n] = wn + n * 16 + i < rows ? row_adapter(a, first + wn + n * 16 + i) : -1;
+    const int32_t chunks = a.l.rank / 4;  // of 8 halves: the rounded values', then the rests'
+    const uint16_t* const u = reinterpret_cast<const uint16_t*>(a.u) + (first + wn + i) * 2 * a.l.rank;
+    // Four fragments of features at a time: the selections need their results in
+    // vector registers, and all 256 at once would not fit beside the operands.
+    constexpr int kBlock = KF < 4 ? KF : 4;
+#pragma unroll
+    for (int f0 = 0; f0 < KF; f0 += kBlock) {
+        for (int32_t cur = next_adapter(ad, -1); cur != kNoAdapter; cur = next_adapter(ad, cur)) {
+            for (int32_t c0 = 0; c0 < chunks; c0 += 4) {
+                const int32_t c = c0 + q;
+                const bool on = c < chunks;
+                bf16x8 uv[KN], wv[kBlock];
+#pragma unroll
+                for (int f = 0; f < kBlock; ++f) {
+                    wv[f] = bf16x8{};
+                    if (on) wv[f] = weights(f0 + f, cur, c < chunks / 2 ? c : c - chunks / 2);
+                }
+#pragma unroll
+                for (int n = 0; n < KN; ++n) {
+                    uv[n] = bf16x8{};
+                    if (on && ad[n] == cur) uv[n] = *reinterpret_cast<const bf16x8*>(u + n * 32 * a.l.rank + c * 8);
+                }
+#pragma unroll
+                for (int f = 0; f < kBlock; ++f)
+#pragma unroll
+                    for (int n = 0; n < KN; ++n) {
+                        const f32x4 s = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wv[f], uv[n], acc[f0 + f][n], 0, 0, 0);
+                        acc[f0 + f][n] = ad[n] == cur ? s : acc[f0 + f][n];
+                    }
+            }
+        }
+        // done with: into accumulation registers, out of the next block's way
+#pragma unroll
+        for (int f = 0; f < kBlock; ++f)
+#pragma unroll
+            for (int n = 0; n < KN; ++n) in_agprs(acc[f0 + f][n]);
+    }
+}
+
+}  // namespace epx

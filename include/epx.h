@@ -581,6 +581,123 @@ int ep_expert_gemm_nvfp4(const ep_cfg_t* cfg, const ep_layout_t* layout, int32_t
                          const uint16_t* x, const uint8_t* codes, const uint8_t* scales,
                          const uint16_t* rowscale, uint16_t* y, void* stream);
 
+/* ------------------------------------------------------------------------
+ * Low-rank adapters of many requests beside the experts' products: a row of
+ * expert e and of a token with adapter d has
+ *   u = scale[d] A[d, e] x,   y = w[e] x + B[d, e] u
+ * and a row of a token without one y = w[e] x.  ep_lora_down makes u; the
+ * products below take it and B.  Every adapter reaches its own rows alone,
+ * infinities and NaN in it included.
+ * ------------------------------------------------------------------------ */
+#define EP_MAX_LORA_RANK 128
+#define EP_MAX_ADAPTERS 65536
+
+typedef struct ep_lora_t {
+    const int32_t* token_adapter; /* int32 [T]: the adapter of each token; -1 and ids
+                                     outside [0, num_adapters): none                 */
+    const uint16_t* a;            /* bf16 [num_adapters, E + shared_expert, rank, in_dim]  */
+    const uint16_t* b;            /* bf16 [num_adapters, E + shared_expert, out_dim, rank] */
+    const float* scale;           /* float [num_adapters], or NULL: 1                */
+    int32_t num_adapters;         /* 1 .. EP_MAX_ADAPTERS                            */
+    int32_t rank;                 /* a multiple of 8 in [8, EP_MAX_LORA_RANK]        */
+    int32_t reserved0;            /* must be 0                                       */
+    int32_t reserved1;            /* must be 0                                       */
+} ep_lora_t;
+/* a, b and u are 16-byte aligned.  in_dim, out_dim and w are the product's they
+ * stand beside; a call checks and reads a, b and scale only as its formula names
+ * them.  All of these calls read counts, row_offsets, seg_base and src_info of the
+ * layout, with token_adapter as it was for ep_lora_down. */
+
+/*
+ * u[r] = scale[d] A[d, e(r)] x[r] for every kept row (fp32 accumulation), zeros
+ * for those without an adapter.
+ *   x  bf16 [R, in_dim]
+ *   u  4-byte words [R, rank]; row r holds the rank values rounded to bf16, then
+ *      rank bf16 of what the rounding left: their sum has 16 significant bits.
+ */
+int ep_lora_down(const ep_cfg_t* cfg, const ep_layout_t* layout, const ep_lora_t* lora, int32_t in_dim,
+                 const uint16_t* x, void* u, void* stream);
+
+/* ep_expert_gemm with the adapters' part:
+ *   y[r, n] = bf16_rne( sum_h x[r, h] w[e(r), n, h] + sum_p B[d, e(r), n, p] u[r, p] ) */
+int ep_expert_gemm_lora(const ep_cfg_t* cfg, const ep_layout_t* layout, const ep_lora_t* lora, int32_t in_dim,
+                        int32_t out_dim, const uint16_t* x, const uint16_t* w, const void* u, uint16_t* y, void* stream);
+
+/* ep_expert_gemm_nvfp4 with the adapters' part (in bf16 beside the 4-bit weights). */
+int ep_expert_gemm_nvfp4_lora(const ep_cfg_t* cfg, const ep_layout_t* layout, const ep_lora_t* lora, int32_t in_dim,
+                              int32_t out_dim, const uint16_t* x, const uint8_t* codes, const uint8_t* scales,
+                              const uint16_t* rowscale, const void* u, uint16_t* y, void* stream);
+
+/* grad_u[r] = scale[d] B[d, e(r)]^T grad_y[r], held as u is; zeros for rows
+ * without an adapter. */
+int ep_lora_bwd_u(const ep_cfg_t* cfg, const ep_layout_t* layout, const ep_lora_t* lora, int32_t out_dim,
+                  const uint16_t* grad_y, void* grad_u, void* stream);
+
+/* ep_expert_gemm_bwd_x with the adapters' part:
+ *   grad_x[r, h] = bf16_rne( sum_n grad_y[r, n] w[e(r), n, h] + sum_p A[d, e(r), p, h] grad_u[r, p] ) */
+int ep_expert_gemm_bwd_x_lora(const ep_cfg_t* cfg, const ep_layout_t* layout, const ep_lora_t* lora, int32_t in_dim,
+                              int32_t out_dim, const uint16_t* grad_y, const uint16_t* w, const void* grad_u,
+                              uint16_t* grad_x, void* stream);
+
+/*
+ * The adapters' gradients, over the rows r of expert e whose tokens have adapter d:
+ *   grad_a[d, e, p, h] = sum_r grad_u[r, p] x[r, h]     [num_adapters, E + shared, rank, in_dim]
+ *   grad_b[d, e, n, p] = sum_r grad_y[r, n] u[r, p]     [num_adapters, E + shared, out_dim, rank]
+ * both of grad_type (EP_GRAD_*: bf16, float, float added to), zeros where no row
+ * is.  Sums in row order: results repeat bit for bit.  (scale is part of u and
+ * grad_u; a and b of lora are not read.)  Returns EP_EINVAL past one grid of 2^32
+ * work-items: 2^24 tiles of 256 columns over all adapters and experts.
+ */
+int ep_lora_bwd_w(const ep_cfg_t* cfg, const ep_layout_t* layout, const ep_lora_t* lora, int32_t in_dim,
+                  int32_t out_dim, const uint16_t* x, const uint16_t* grad_y, const void* u, const void* grad_u,
+                  void* grad_a, void* grad_b, int32_t grad_type, void* stream);
+
+/*
+ * The gated block in one kernel: both projections, the activation and the
+ * routing weight (ep_expert_gemm over the stacked weights and ep_swiglu, without
+ * h in between: g and u below are not rounded).
+ *   g = sum_h x[r, h] w[e(r), i, h],  u = sum_h x[r, h] w[e(r), inter + i, h]
+ *   act[r, i] = bf16_rne( w_r * (silu(g) * u) )
+ *   x     bf16 [R, in_dim];  w  bf16 [E + shared_expert, 2*inter, in_dim] (gate rows, then up rows)
+ *   probs float [T, K] or NULL (w_r = 1; 1 in the shared slot as well);  act  bf16 [R, inter]
+ *   lora  NULL, or adapters beside the stacked weights (B [.., 2*inter, rank]), added to g
+ *         and u before the activation; ulora: ep_lora_down's of x (NULL without)
+ * in_dim and inter: multiples of 8 in [8, EP_MAX_EXPERT_DIM].  Reads counts,
+ * row_offsets, seg_base and src_info of the layout.
+ */
+int ep_expert_gated(const ep_cfg_t* cfg, const ep_layout_t* layout, const ep_lora_t* lora, int32_t in_dim, int32_t inter,
+                    const uint16_t* x, const uint16_t* w, const float* probs, const void* ulora, uint16_t* act,
+                    void* stream);
+
+/* The same over 4-bit weights, as in ep_expert_gemm_nvfp4 with out_dim 2*inter
+ * (in_dim a multiple of 16, inter * in_dim < 2^34). */
+int ep_expert_gated_nvfp4(const ep_cfg_t* cfg, const ep_layout_t* layout, const ep_lora_t* lora, int32_t in_dim,
+                          int32_t inter, const uint16_t* x, const uint8_t* codes, const uint8_t* scales,
+                          const uint16_t* rowscale, const float* probs, const void* ulora, uint16_t* act, void* stream);
+
+/* Columns of act whose share of grad_probs is one part of the workspace. */
+#define EP_GATED_PART 32
+
+/*
+ * Backward of ep_expert_gated, which makes g and u again (neither is kept
+ * between the passes): with s = 1 / (1 + exp(-g)) and ga the row of grad_act, in fp32,
+ *   grad_h[r, i]         = bf16_rne( w_r ga u s (1 + g (1 - s)) )
+ *   grad_h[r, inter + i] = bf16_rne( w_r ga g s )
+ *   grad_probs[t, k]     = sum_i ga silu(g) u   (k < K; 0 for masked, invalid and dropped
+ *                          slots; float [T, K], or NULL to leave it out)
+ *   act                  as the forward pass, or NULL to leave it out
+ * and, from grad_h, the gradients of x and w by ep_expert_gemm_bwd_x and
+ * ep_expert_gemm_bwd_w (of the adapters by ep_lora_bwd_u and ep_lora_bwd_w).
+ *   grad_act bf16 [R, inter];  grad_h bf16 [R, 2*inter]
+ *   workspace: with grad_probs, at least T * K * ceil(inter / EP_GATED_PART) * 4
+ *              bytes, 16-byte aligned, of any content; not shared by calls that may
+ *              run at the same time.  Else NULL.
+ */
+int ep_expert_gated_bwd(const ep_cfg_t* cfg, const ep_layout_t* layout, const ep_lora_t* lora, int32_t in_dim,
+                        int32_t inter, const uint16_t* x, const uint16_t* w, const float* probs, const void* ulora,
+                        const uint16_t* grad_act, uint16_t* grad_h, uint16_t* act, float* grad_probs, void* workspace,
+                        int64_t workspace_bytes, void* stream);
+
 /* Static description of a status code. */
 const char* ep_strerror(int status);
 
