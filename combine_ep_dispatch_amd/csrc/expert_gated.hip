@@ -39,11 +39,11 @@ __global__ __launch_bounds__(kLoopThreads) __attribute__((amdgpu_waves_per_eu(1,
     by_rows(t.rows, [&](auto nt) {
         constexpr int NT = decltype(nt)::value, KF = Shape<NT>::kF, KN = Shape<NT>::kN;
         const int wf = Shape<NT>::wf(), wn = Shape<NT>::wn();
-        RowsOperand<NT, kLoopWaves> no;
+        LoopRows<NT> no;
         no.init(a.e.x + t.first * a.e.in, t.rows, a.e.in, a.e.in);
         f32x4 acc[KF][KN] = {};
         const int32_t c0 = a0 + wf / 2;  // the wave's first column of act
-        tile_loop<GatedOperand, RowsOperand<NT, kLoopWaves>, NT>(fo, no, lds, wf, wn, a.e.in, acc, [&] {
+        tile_loop<GatedOperand, LoopRows<NT>, NT>(fo, no, lds, wf, wn, a.e.in, acc, [&] {
             if constexpr (LORA) adapters_of(a, t, c0, wn, acc);
         });
         // acc[2 p][n][j], acc[2 p + 1][n][j]: g and u of column c0 + 16 p + 4 q + j, row wn + 16 n + i

@@ -14,30 +14,96 @@ constexpr int kLoopThreads = kLoopWaves * kWave;
 constexpr int kTileF = 256, kTileN = 256;  // features (of both projections, where gated) and rows of a tile
 constexpr int kLoopLds = 160 * 1024;       // all of it: one workgroup a CU
 
+// A load of 16 bytes a lane to LDS from `to` on (16 l for lane l), as load_to_lds,
+// from a descriptor that no vector instruction writes from settled() on: without
+// the wait states that one would need before every load.
+__device__ __forceinline__ void load16(i32x4 rs, uint32_t to, int32_t voff) {
+#ifdef __HIP_DEVICE_COMPILE__
+#pragma clang diagnostic push
+#pragma clang diagnostic ignored "-Winline-asm"
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(to), "v"(voff), "s"(rs)
+                 : "memory", "m0");
+#pragma clang diagnostic pop
+#endif
+}
+
+__device__ __forceinline__ i32x4 descriptor(const void* base, int32_t bytes) {
+    const uint64_t p = reinterpret_cast<uint64_t>(base);
+    return {(int32_t)uniform((uint32_t)p), (int32_t)uniform((uint32_t)(p >> 32) & 0xFFFFu), uniform(bytes), kBufferWord3};
+}
+
+// rs, whose words were written 5 wait states ago at least.
+__device__ __forceinline__ i32x4 settled(i32x4 rs) {
+#ifdef __HIP_DEVICE_COMPILE__
+    asm volatile("s_nop 4" : "+s"(rs));
+#endif
+    return rs;
+}
+
+// The operands as expert_tile.h lays them out, with what a load computes kept to
+// one addition: at(l0) is what the loads of a step have in common.
+template <int BM>
+struct LoopRows : RowsOperand<BM, kLoopWaves> {
+    using Base = RowsOperand<BM, kLoopWaves>;
+    i32x4 rs;
+    struct At {
+        int32_t off[2];  // of even and odd loads
+    };
+    __device__ __forceinline__ void init(const uint16_t* p, int32_t rows, int32_t pitch, int32_t l) {
+        Base::init(p, rows, pitch, l);
+        rs = settled(descriptor(p, this->records));
+    }
+    __device__ __forceinline__ At at(int32_t l0) const {
+        At a;
+#pragma unroll
+        for (int k = 0; k < 2; ++k) a.off[k] = l0 + this->chunk[k] * 8 < this->len ? l0 * 2 : kOutside;
+        return a;
+    }
+    __device__ __forceinline__ void load(uint32_t to, const At& a, int j) const {
+        load16(rs, to + j * 1024, (int32_t)((uint32_t)this->voff[j] + (uint32_t)a.off[j % 2]));
+    }
+    // Where a lane's values of half a step are in the operand's LDS tile, from row m0
+    // on, and the fragment 16 f rows further.
+    static __device__ __forceinline__ int32_t lane_at(int m0, int half) {
+        const int lane = threadIdx.x & (kWave - 1), i = lane % 16, q = lane / 16;
+        return (m0 + i) * kStepL + ((half * 4 + q) ^ (i / 2)) * 8;
+    }
+    static __device__ __forceinline__ bf16x8 fragment_at(const uint16_t* p, int f, int, int) {
+        return *reinterpret_cast<const bf16x8*>(p + f * 16 * kStepL);
+    }
+};
+
 // The gated block's feature operand: 16 rows of the gate and 16 of the up
 // projection in turn, so that a lane of a wave has both of a column of act.
-struct GatedOperand : RowsOperand<kTileF, kLoopWaves> {
-    const uint16_t* up;
+struct GatedOperand : LoopRows<kTileF> {
+    i32x4 up;
 
     // p: the expert's weights; a0: first column of act; inter: their number
     __device__ __forceinline__ void init(const uint16_t* p, int32_t a0, int32_t inter, int32_t l) {
         const int lane = threadIdx.x & (kWave - 1), w = uniform((int32_t)(threadIdx.x / kWave));
-        base = p + (int64_t)a0 * l;
-        up = base + (int64_t)inter * l;
-        ld = len = l;
-        records = uniform(min(kTileF / 2, inter - a0) * l * 2);
-        chunk[0] = (lane % 8) ^ (lane / 16);
-        chunk[1] = chunk[0] ^ 4;
+        const uint16_t* const gate = p + (int64_t)a0 * l;
+        LoopRows<kTileF>::init(gate, min(kTileF / 2, inter - a0), l, l);
+        up = settled(descriptor(gate + (int64_t)inter * l, records));
 #pragma unroll
         for (int j = 0; j < kLoads; ++j) {
             const int at = w * kLoads + j;  // 8 rows of LDS: half of a gate's or an up's 16
             voff[j] = (at / 4 * 16 + at % 2 * 8 + lane / 8) * l * 2 + chunk[j % 2] * 16;
         }
     }
-    __device__ __forceinline__ void load(uint16_t* lds, int32_t l0, int j) const {
-        const int w = uniform((int32_t)(threadIdx.x / kWave));
-        load_to_lds<16>(j / 2 % 2 ? up : base, records, lds + (w * kLoads + j) * 512,
-                        l0 + chunk[j % 2] * 8 < len ? voff[j] + l0 * 2 : kOutside);
+    __device__ __forceinline__ void load(uint32_t to, const At& a, int j) const {
+        load16(j / 2 % 2 ? up : rs, to + j * 1024, (int32_t)((uint32_t)voff[j] + (uint32_t)a.off[j % 2]));
+    }
+};
+
+struct LoopCols : ColsOperand<kTileF, kLoopWaves> {
+    struct At {
+        i32x4 rs;
+    };
+    __device__ __forceinline__ At at(int32_t l0) const { return {settled(descriptor(base + (int64_t)l0 * ld, records(l0)))}; }
+    __device__ __forceinline__ void load(uint32_t to, const At& a, int j) const { load16(a.rs, to + j * 1024, voff[j]); }
+    static __device__ __forceinline__ int32_t lane_at(int, int) { return 0; }
+    static __device__ __forceinline__ bf16x8 fragment_at(const uint16_t* p, int f, int m0, int half) {
+        return fragment(p, m0 + f * 16, half);
     }
 };
 
@@ -55,24 +121,31 @@ __device__ __forceinline__ void tile_loop(const FOp& fo, const NOp& no, uint16_t
     constexpr int kAheadF = kUnits ? 2 : kRing - 1, kAheadN = kUnits ? 1 : kRing - 1;
     constexpr int kFL = FOp::kLoads, kNL = NOp::kLoads;
     static_assert(kUnits ? kRing == 5 : kRing >= 3, "");
+    const int w = uniform((int32_t)(threadIdx.x / kWave));
+    const uint32_t base = uniform((uint32_t)(uintptr_t)(EPX_LDS const void*)lds);
     auto ring = [](int32_t v) { return v >= kRing ? v - kRing : v; };
-    auto f_at = [&](int32_t slot) { return lds + slot * kBuffer; };
-    auto n_at = [&](int32_t slot) { return kUnits ? lds + ring(slot + 1) * kBuffer : lds + slot * kBuffer + kUnit; };
-    auto load_f = [&](int32_t s, int32_t slot, int j0, int j1) {
+    // element of LDS where a step's operands begin, by the step's slot
+    auto f_at = [&](int32_t slot) { return slot * kBuffer; };
+    auto n_at = [&](int32_t slot) { return kUnits ? ring(slot + 1) * kBuffer : slot * kBuffer + kUnit; };
+    auto f_to = [&](int32_t slot) { return base + f_at(slot) * 2 + w * kFL * 1024; };
+    auto n_to = [&](int32_t slot) { return base + n_at(slot) * 2 + w * kNL * 1024; };
+    auto load_f = [&](int32_t s, int32_t slot) {
+        const auto a = fo.at(s * kStepL);
 #pragma unroll
-        for (int j = j0; j < j1; ++j) fo.load(f_at(slot), s * kStepL, j);
+        for (int j = 0; j < kFL; ++j) fo.load(f_to(slot), a, j);
     };
-    auto load_n = [&](int32_t s, int32_t slot, int j0, int j1) {
+    auto load_n = [&](int32_t s, int32_t slot) {
+        const auto a = no.at(s * kStepL);
 #pragma unroll
-        for (int j = j0; j < j1; ++j) no.load(n_at(slot), s * kStepL, j);
+        for (int j = 0; j < kNL; ++j) no.load(n_to(slot), a, j);
     };
     constexpr int kStride = kUnits ? 2 : 1;  // slots of a step
 #pragma unroll
     for (int s = 0; s < kAheadF; ++s) {
-        if (s < kAheadN) load_n(s, s * kStride, 0, kNL);
-        load_f(s, s * kStride, 0, kFL);
+        if (s < kAheadN) load_n(s, s * kStride);
+        load_f(s, s * kStride);
     }
-    load_n(kAheadN, kAheadN * kStride, 0, kNL);
+    load_n(kAheadN, kAheadN * kStride);
     meanwhile();
     // 256 results in accumulation registers, the operands in the other 256: left
     // to itself the compiler moves results between the two in every step
@@ -86,48 +159,50 @@ __device__ __forceinline__ void tile_loop(const FOp& fo, const NOp& no, uint16_t
     lds_barrier();
     constexpr int kReads = KF + KN;  // of half a step
     bf16x8 fa[2][KF], fb[2][KN];
-    auto read = [&](int half, int32_t slot, int r) {
+    const uint16_t* const lane_f[2] = {lds + FOp::lane_at(wf, 0), lds + FOp::lane_at(wf, 1)};
+    const uint16_t* const lane_n[2] = {lds + NOp::lane_at(wn, 0), lds + NOp::lane_at(wn, 1)};
+    auto read = [&](int half, const uint16_t* f, const uint16_t* n, int r) {
         if (r < KN)
-            fb[half][r] = NOp::fragment(n_at(slot), wn + r * 16, half);
+            fb[half][r] = NOp::fragment_at(n, r, wn, half);
         else
-            fa[half][r - KN] = FOp::fragment(f_at(slot), wf + (r - KN) * 16, half);
+            fa[half][r - KN] = FOp::fragment_at(f, r - KN, wf, half);
     };
 #pragma unroll
-    for (int r = 0; r < kReads; ++r) read(0, 0, r);
+    for (int r = 0; r < kReads; ++r) read(0, lane_f[0] + f_at(0), lane_n[0] + n_at(0), r);
     // Each half of a step multiplies the fragments that the half before read, and
     // reads the next one's: first the second half's, then, behind the barrier, the
     // next step's first.  By that barrier every wave has read all of this step,
-    // whose buffers are filled from then on.
-    constexpr int kSpread = KF - 1;  // the reads end before the last products: they have returned by the barrier
+    // whose buffers are filled from then on.  Loads and reads go one by one between
+    // the matrix instructions, each of which leaves time to issue three others.
+    constexpr int kProducts = KF * KN;
+    constexpr int kReadGap = (kProducts - 1) / kReads < 3 ? (kProducts - 1) / kReads : 3;
+    static_assert(kReadGap >= 1, "");
     const int32_t steps = (len + kStepL - 1) / kStepL;
     int32_t slot = 0;
-    for (int32_t s = 0; s < steps; ++s) {
-        const int32_t ahead = ring(slot + (kUnits ? 4 : kRing - 1)), after = ring(slot + kStride);
+    auto half_step = [&](int half, int32_t from, const auto& op, const auto& at, uint32_t to, auto loads) {
+        constexpr int kLoads = decltype(loads)::value;
+        const uint16_t *const f_from = lane_f[half ^ 1] + f_at(from), *const n_from = lane_n[half ^ 1] + n_at(from);
 #pragma unroll
-        for (int f = 0; f < KF; ++f) {
+        for (int k = 0; k < kProducts; ++k) {
+            const int f = k / KN, n = k % KN;
             __builtin_amdgcn_sched_barrier(0);
-            load_f(s + kAheadF, ahead, f * kFL / KF, (f + 1) * kFL / KF);
-#pragma unroll
-            for (int r = min(f, kSpread) * kReads / kSpread; r < min(f + 1, kSpread) * kReads / kSpread; ++r) read(1, slot, r);
-#pragma unroll
-            for (int n = 0; n < KN; ++n)
-                acc[f][n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fa[0][f], fb[0][n], acc[f][n], 0, 0, 0);
+            acc[f][n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fa[half][f], fb[half][n], acc[f][n], 0, 0, 0);
+            __builtin_amdgcn_sched_barrier(0);
+            if (k % kReadGap == 0 && k / kReadGap < kReads) read(half ^ 1, f_from, n_from, k / kReadGap);
+            if ((k + 1) * kLoads / kProducts > k * kLoads / kProducts) op.load(to, at, k * kLoads / kProducts);
         }
         __builtin_amdgcn_sched_barrier(0);
+    };
+    for (int32_t s = 0; s < steps; ++s) {
+        const int32_t after = ring(slot + kStride);
+        half_step(0, slot, fo, fo.at((s + kAheadF) * kStepL), f_to(ring(slot + (kUnits ? 4 : kRing - 1))),
+                  std::integral_constant<int, kFL>{});
         // the next step has landed, in every wave
         asm volatile("s_waitcnt vmcnt(%0)" ::"n"(kUnits ? kFL : (kRing - 2) * (kFL + kNL)) : "memory");
         lds_barrier();
-        const int32_t freed = kUnits ? ring(slot + 4) : slot;  // its N unit is this step's F unit
-#pragma unroll
-        for (int f = 0; f < KF; ++f) {
-            __builtin_amdgcn_sched_barrier(0);
-            load_n(s + 1 + kAheadN, freed, f * kNL / KF, (f + 1) * kNL / KF);
-#pragma unroll
-            for (int r = min(f, kSpread) * kReads / kSpread; r < min(f + 1, kSpread) * kReads / kSpread; ++r) read(0, after, r);
-#pragma unroll
-            for (int n = 0; n < KN; ++n)
-                acc[f][n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fa[1][f], fb[1][n], acc[f][n], 0, 0, 0);
-        }
+        // of the freed units, N's of the step after the next takes this step's F's
+        half_step(1, after, no, no.at((s + 1 + kAheadN) * kStepL), n_to(kUnits ? ring(slot + 4) : slot),
+                  std::integral_constant<int, kNL>{});
         slot = after;
     }
     // No load may land in LDS that belongs to another workgroup by then.

@@ -17,7 +17,7 @@ enum Product { kForward, kInputGrad };
 
 template <Product P>
 __global__ __launch_bounds__(kLoopThreads) __attribute__((amdgpu_waves_per_eu(1, 1))) void k_product(BlockArgs a, int32_t ftiles) {
-    using FOp = typename std::conditional<P == kForward, RowsOperand<kTileF, kLoopWaves>, ColsOperand<kTileF, kLoopWaves>>::type;
+    using FOp = typename std::conditional<P == kForward, LoopRows<kTileF>, LoopCols>::type;
     __shared__ __align__(1024) uint16_t lds[kLoopLds / 2];
     int32_t ft;
     const RowTile t = find_row_tile<kLoopThreads, kTileN>(
@@ -35,10 +35,10 @@ __global__ __launch_bounds__(kLoopThreads) __attribute__((amdgpu_waves_per_eu(1,
     by_rows(t.rows, [&](auto nt) {
         constexpr int NT = decltype(nt)::value, KF = Shape<NT>::kF, KN = Shape<NT>::kN;
         const int wf = Shape<NT>::wf(), wn = Shape<NT>::wn();
-        RowsOperand<NT, kLoopWaves> no;
+        LoopRows<NT> no;
         no.init((P == kForward ? a.e.x : a.e.gy) + t.first * L, t.rows, L, L);
         f32x4 acc[KF][KN] = {};
-        tile_loop<FOp, RowsOperand<NT, kLoopWaves>, NT>(fo, no, lds, wf, wn, L, acc, [&] {
+        tile_loop<FOp, LoopRows<NT>, NT>(fo, no, lds, wf, wn, L, acc, [&] {
             add_adapters<KF, KN>(a, t.first, t.rows, wn, [&](int f, int32_t ad, int32_t c) {
                 const int32_t fe = f0 + wf + f * 16 + i, rank = a.l.rank;
                 const int64_t pair = (int64_t)ad * (a.e.E + a.e.shared) + t.expert;
