@@ -3,6 +3,7 @@
 #pragma once
 
 #include <type_traits>
+#include <utility>
 
 #include "expert_tile.h"
 #include "lora_device.h"
@@ -14,18 +15,34 @@ constexpr int kLoopThreads = kLoopWaves * kWave;
 constexpr int kTileF = 256, kTileN = 256;  // features (of both projections, where gated) and rows of a tile
 constexpr int kLoopLds = 160 * 1024;       // all of it: one workgroup a CU
 
-// A load of 16 bytes a lane to LDS from `to` on (16 l for lane l), as load_to_lds,
-// from a descriptor that no vector instruction writes from settled() on: without
-// the wait states that one would need before every load.
-__device__ __forceinline__ void load16(i32x4 rs, uint32_t to, int32_t voff) {
-#ifdef __HIP_DEVICE_COMPILE__
+// A load of 16 bytes a lane to LDS (16 l for lane l), as load_to_lds, in two parts
+// that other instructions go between: where to, in m0, and the load, at least one
+// wait state later.  Its descriptor is one that no vector instruction writes from
+// settled() on: it needs no wait states of its own.  Nothing the compiler puts
+// between the two uses m0.
 #pragma clang diagnostic push
 #pragma clang diagnostic ignored "-Winline-asm"
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(to), "v"(voff), "s"(rs)
-                 : "memory", "m0");
-#pragma clang diagnostic pop
+template <int OFF>
+__device__ __forceinline__ void aim16(uint32_t to) {
+#ifdef __HIP_DEVICE_COMPILE__
+    asm volatile("s_add_u32 m0, %0, %1" ::"s"(to), "n"(OFF) : "memory", "m0", "scc");
 #endif
 }
+__device__ __forceinline__ void load16(i32x4 rs, int32_t voff) {
+#ifdef __HIP_DEVICE_COMPILE__
+    asm volatile("buffer_load_dwordx4 %0, %1, 0 offen lds" ::"v"(voff), "s"(rs) : "memory");
+#endif
+}
+// Both at once.
+template <int OFF>
+__device__ __forceinline__ void aim_and_load16(uint32_t to, i32x4 rs, int32_t voff) {
+#ifdef __HIP_DEVICE_COMPILE__
+    asm volatile("s_add_u32 m0, %0, %1\n\ts_nop 0\n\tbuffer_load_dwordx4 %2, %3, 0 offen lds" ::"s"(to), "n"(OFF), "v"(voff),
+                 "s"(rs)
+                 : "memory", "m0", "scc");
+#endif
+}
+#pragma clang diagnostic pop
 
 __device__ __forceinline__ i32x4 descriptor(const void* base, int32_t bytes) {
     const uint64_t p = reinterpret_cast<uint64_t>(base);
@@ -59,9 +76,10 @@ struct LoopRows : RowsOperand<BM, kLoopWaves> {
         for (int k = 0; k < 2; ++k) a.off[k] = l0 + this->chunk[k] * 8 < this->len ? l0 * 2 : kOutside;
         return a;
     }
-    __device__ __forceinline__ void load(uint32_t to, const At& a, int j) const {
-        load16(rs, to + j * 1024, (int32_t)((uint32_t)this->voff[j] + (uint32_t)a.off[j % 2]));
+    __device__ __forceinline__ int32_t offset(const At& a, int j) const {
+        return (int32_t)((uint32_t)this->voff[j] + (uint32_t)a.off[j % 2]);
     }
+    __device__ __forceinline__ i32x4 source(const At&, int) const { return rs; }
     // Where a lane's values of half a step are in the operand's LDS tile, from row m0
     // on, and the fragment 16 f rows further.
     static __device__ __forceinline__ int32_t lane_at(int m0, int half) {
@@ -90,9 +108,7 @@ struct GatedOperand : LoopRows<kTileF> {
             voff[j] = (at / 4 * 16 + at % 2 * 8 + lane / 8) * l * 2 + chunk[j % 2] * 16;
         }
     }
-    __device__ __forceinline__ void load(uint32_t to, const At& a, int j) const {
-        load16(j / 2 % 2 ? up : rs, to + j * 1024, (int32_t)((uint32_t)voff[j] + (uint32_t)a.off[j % 2]));
-    }
+    __device__ __forceinline__ i32x4 source(const At&, int j) const { return j / 2 % 2 ? up : rs; }
 };
 
 struct LoopCols : ColsOperand<kTileF, kLoopWaves> {
@@ -100,12 +116,26 @@ struct LoopCols : ColsOperand<kTileF, kLoopWaves> {
         i32x4 rs;
     };
     __device__ __forceinline__ At at(int32_t l0) const { return {settled(descriptor(base + (int64_t)l0 * ld, records(l0)))}; }
-    __device__ __forceinline__ void load(uint32_t to, const At& a, int j) const { load16(a.rs, to + j * 1024, voff[j]); }
+    __device__ __forceinline__ int32_t offset(const At&, int j) const { return voff[j]; }
+    __device__ __forceinline__ i32x4 source(const At& a, int) const { return a.rs; }
     static __device__ __forceinline__ int32_t lane_at(int, int) { return 0; }
     static __device__ __forceinline__ bf16x8 fragment_at(const uint16_t* p, int f, int m0, int half) {
         return fragment(p, m0 + f * 16, half);
     }
 };
+
+// A wave's loads of an operand's step from l0 on, to its part of LDS.
+template <typename Op, int... J>
+__device__ __forceinline__ void load_step(const Op& op, uint32_t to, int32_t l0, std::integer_sequence<int, J...>) {
+    const auto a = op.at(l0);
+    (aim_and_load16<J * 1024>(to, op.source(a, J), op.offset(a, J)), ...);
+}
+
+// f(integral_constant<int, 0>), f(integral_constant<int, 1>), ...
+template <typename F, int... K>
+__device__ __forceinline__ void each(F f, std::integer_sequence<int, K...>) {
+    (f(std::integral_constant<int, K>{}), ...);
+}
 
 // A wave's KF x KN fragments of 16 features by 16 rows, from feature wf and row
 // wn of the tile on, summed over L and added to acc.  LDS holds NT rows a step.
@@ -129,16 +159,8 @@ __device__ __forceinline__ void tile_loop(const FOp& fo, const NOp& no, uint16_t
     auto n_at = [&](int32_t slot) { return kUnits ? ring(slot + 1) * kBuffer : slot * kBuffer + kUnit; };
     auto f_to = [&](int32_t slot) { return base + f_at(slot) * 2 + w * kFL * 1024; };
     auto n_to = [&](int32_t slot) { return base + n_at(slot) * 2 + w * kNL * 1024; };
-    auto load_f = [&](int32_t s, int32_t slot) {
-        const auto a = fo.at(s * kStepL);
-#pragma unroll
-        for (int j = 0; j < kFL; ++j) fo.load(f_to(slot), a, j);
-    };
-    auto load_n = [&](int32_t s, int32_t slot) {
-        const auto a = no.at(s * kStepL);
-#pragma unroll
-        for (int j = 0; j < kNL; ++j) no.load(n_to(slot), a, j);
-    };
+    auto load_f = [&](int32_t s, int32_t slot) { load_step(fo, f_to(slot), s * kStepL, std::make_integer_sequence<int, kFL>{}); };
+    auto load_n = [&](int32_t s, int32_t slot) { load_step(no, n_to(slot), s * kStepL, std::make_integer_sequence<int, kNL>{}); };
     constexpr int kStride = kUnits ? 2 : 1;  // slots of a step
 #pragma unroll
     for (int s = 0; s < kAheadF; ++s) {
@@ -179,29 +201,38 @@ __device__ __forceinline__ void tile_loop(const FOp& fo, const NOp& no, uint16_t
     static_assert(kReadGap >= 1, "");
     const int32_t steps = (len + kStepL - 1) / kStepL;
     int32_t slot = 0;
-    auto half_step = [&](int half, int32_t from, const auto& op, const auto& at, uint32_t to, auto loads) {
-        constexpr int kLoads = decltype(loads)::value;
+    auto half_step = [&](auto half_, int32_t from, const auto& op, const auto& at, uint32_t to, auto loads) {
+        constexpr int half = decltype(half_)::value, kLoads = decltype(loads)::value, kGap = kProducts / kLoads;
+        static_assert(kGap >= 1, "");
         const uint16_t *const f_from = lane_f[half ^ 1] + f_at(from), *const n_from = lane_n[half ^ 1] + n_at(from);
-#pragma unroll
-        for (int k = 0; k < kProducts; ++k) {
-            const int f = k / KN, n = k % KN;
+        int32_t voff = 0;
+        each([&](auto k_) {
+            constexpr int k = decltype(k_)::value, f = k / KN, n = k % KN, j = k / kGap;
             __builtin_amdgcn_sched_barrier(0);
             acc[f][n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fa[half][f], fb[half][n], acc[f][n], 0, 0, 0);
             __builtin_amdgcn_sched_barrier(0);
-            if (k % kReadGap == 0 && k / kReadGap < kReads) read(half ^ 1, f_from, n_from, k / kReadGap);
-            if ((k + 1) * kLoads / kProducts > k * kLoads / kProducts) op.load(to, at, k * kLoads / kProducts);
-        }
+            if constexpr (k % kReadGap == 0 && k / kReadGap < kReads) read(half ^ 1, f_from, n_from, k / kReadGap);
+            if constexpr (j < kLoads && kGap == 1) {
+                aim_and_load16<j * 1024>(to, op.source(at, j), op.offset(at, j));
+            } else if constexpr (j < kLoads && k % kGap == 0) {
+                voff = op.offset(at, j);
+                aim16<j * 1024>(to);
+            }
+            if constexpr (j < kLoads && kGap > 1 && k % kGap == 1) load16(op.source(at, j), voff);
+        }, std::make_integer_sequence<int, kProducts>{});
         __builtin_amdgcn_sched_barrier(0);
     };
+    using First = std::integral_constant<int, 0>;
+    using Second = std::integral_constant<int, 1>;
     for (int32_t s = 0; s < steps; ++s) {
         const int32_t after = ring(slot + kStride);
-        half_step(0, slot, fo, fo.at((s + kAheadF) * kStepL), f_to(ring(slot + (kUnits ? 4 : kRing - 1))),
+        half_step(First{}, slot, fo, fo.at((s + kAheadF) * kStepL), f_to(ring(slot + (kUnits ? 4 : kRing - 1))),
                   std::integral_constant<int, kFL>{});
         // the next step has landed, in every wave
         asm volatile("s_waitcnt vmcnt(%0)" ::"n"(kUnits ? kFL : (kRing - 2) * (kFL + kNL)) : "memory");
         lds_barrier();
         // of the freed units, N's of the step after the next takes this step's F's
-        half_step(1, after, no, no.at((s + 1 + kAheadN) * kStepL), n_to(kUnits ? ring(slot + 4) : slot),
+        half_step(Second{}, after, no, no.at((s + 1 + kAheadN) * kStepL), n_to(kUnits ? ring(slot + 4) : slot),
                   std::integral_constant<int, kNL>{});
         slot = after;
     }
