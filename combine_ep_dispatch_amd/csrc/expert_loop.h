@@ -57,29 +57,43 @@ __device__ __forceinline__ i32x4 settled(i32x4 rs) {
     return rs;
 }
 
-// The operands as expert_tile.h lays them out, with what a load computes kept to
-// one addition: at(l0) is what the loads of a step have in common.
+// bytes further: the base by scalar additions.
+__device__ __forceinline__ void move_on(i32x4& rs, int64_t bytes) {
+    const uint64_t p = ((uint64_t)(uint32_t)rs[1] << 32 | (uint32_t)rs[0]) + bytes;
+    rs[0] = (int32_t)(uint32_t)p;
+    rs[1] = (int32_t)(uint32_t)(p >> 32);
+}
+
+// The operands as expert_tile.h lays them out, loaded step after step: a lane's
+// offsets stay, the descriptors move on.  (A vector instruction between two matrix
+// instructions costs about 9 cycles: with an addition for each load the loop took
+// 272 000 instead of 256 000.)
 template <int BM>
 struct LoopRows : RowsOperand<BM, kLoopWaves> {
     using Base = RowsOperand<BM, kLoopWaves>;
     i32x4 rs;
-    struct At {
-        int32_t off[2];  // of even and odd loads
-    };
+    int32_t left;  // values of L from the next step on
+
     __device__ __forceinline__ void init(const uint16_t* p, int32_t rows, int32_t pitch, int32_t l) {
         Base::init(p, rows, pitch, l);
         rs = settled(descriptor(p, this->records));
+        left = l;
+        if (left < kStepL) trim();
     }
-    __device__ __forceinline__ At at(int32_t l0) const {
-        At a;
+    // The last step, in part: chunks past its end are outside.  Behind it everything is.
+    __device__ __forceinline__ void trim() {
+        if (left <= 0) rs[2] = 0;
 #pragma unroll
-        for (int k = 0; k < 2; ++k) a.off[k] = l0 + this->chunk[k] * 8 < this->len ? l0 * 2 : kOutside;
-        return a;
+        for (int j = 0; j < Base::kLoads; ++j)
+            if (this->chunk[j % 2] * 8 >= left) this->voff[j] = kOutside;
     }
-    __device__ __forceinline__ int32_t offset(const At& a, int j) const {
-        return (int32_t)((uint32_t)this->voff[j] + (uint32_t)a.off[j % 2]);
+    __device__ __forceinline__ void advance() {
+        move_on(rs, kStepL * 2);
+        rs[2] -= kStepL * 2;
+        left -= kStepL;
+        if (left < kStepL) trim();
     }
-    __device__ __forceinline__ i32x4 source(const At&, int) const { return rs; }
+    __device__ __forceinline__ i32x4 source(int) const { return rs; }
     // Where a lane's values of half a step are in the operand's LDS tile, from row m0
     // on, and the fragment 16 f rows further.
     static __device__ __forceinline__ int32_t lane_at(int m0, int half) {
@@ -100,35 +114,53 @@ struct GatedOperand : LoopRows<kTileF> {
     __device__ __forceinline__ void init(const uint16_t* p, int32_t a0, int32_t inter, int32_t l) {
         const int lane = threadIdx.x & (kWave - 1), w = uniform((int32_t)(threadIdx.x / kWave));
         const uint16_t* const gate = p + (int64_t)a0 * l;
-        LoopRows<kTileF>::init(gate, min(kTileF / 2, inter - a0), l, l);
+        Base::init(gate, min(kTileF / 2, inter - a0), l, l);
+        rs = settled(descriptor(gate, records));
         up = settled(descriptor(gate + (int64_t)inter * l, records));
 #pragma unroll
         for (int j = 0; j < kLoads; ++j) {
             const int at = w * kLoads + j;  // 8 rows of LDS: half of a gate's or an up's 16
             voff[j] = (at / 4 * 16 + at % 2 * 8 + lane / 8) * l * 2 + chunk[j % 2] * 16;
         }
+        left = l;
+        if (left < kStepL) trim();
     }
-    __device__ __forceinline__ i32x4 source(const At&, int j) const { return j / 2 % 2 ? up : rs; }
+    __device__ __forceinline__ void advance() {
+        LoopRows<kTileF>::advance();
+        move_on(up, kStepL * 2);
+        up[2] = rs[2];
+    }
+    __device__ __forceinline__ i32x4 source(int j) const { return j / 2 % 2 ? up : rs; }
 };
 
 struct LoopCols : ColsOperand<kTileF, kLoopWaves> {
-    struct At {
-        i32x4 rs;
-    };
-    __device__ __forceinline__ At at(int32_t l0) const { return {settled(descriptor(base + (int64_t)l0 * ld, records(l0)))}; }
-    __device__ __forceinline__ int32_t offset(const At&, int j) const { return voff[j]; }
-    __device__ __forceinline__ i32x4 source(const At& a, int) const { return a.rs; }
+    using Base = ColsOperand<kTileF, kLoopWaves>;
+    i32x4 rs;
+    int32_t l0;  // the next step's first row
+
+    __device__ __forceinline__ void init(const uint16_t* p, int32_t cols, int32_t pitch, int32_t l, int32_t m0) {
+        Base::init(p, cols, pitch, l, m0);
+        rs = settled(descriptor(p, records(0)));
+        l0 = 0;
+    }
+    __device__ __forceinline__ void advance() {
+        move_on(rs, (int64_t)kStepL * ld * 2);
+        l0 += kStepL;
+        const int32_t rows = min(len - l0, kStepL);
+        rs[2] = rows > 0 ? rows * ld * 2 - cut : 0;
+    }
+    __device__ __forceinline__ i32x4 source(int) const { return rs; }
     static __device__ __forceinline__ int32_t lane_at(int, int) { return 0; }
     static __device__ __forceinline__ bf16x8 fragment_at(const uint16_t* p, int f, int m0, int half) {
         return fragment(p, m0 + f * 16, half);
     }
 };
 
-// A wave's loads of an operand's step from l0 on, to its part of LDS.
+// A wave's loads of an operand's next step, to its part of LDS.
 template <typename Op, int... J>
-__device__ __forceinline__ void load_step(const Op& op, uint32_t to, int32_t l0, std::integer_sequence<int, J...>) {
-    const auto a = op.at(l0);
-    (aim_and_load16<J * 1024>(to, op.source(a, J), op.offset(a, J)), ...);
+__device__ __forceinline__ void load_step(Op& op, uint32_t to, std::integer_sequence<int, J...>) {
+    (aim_and_load16<J * 1024>(to, op.source(J), op.voff[J]), ...);
+    op.advance();
 }
 
 // f(integral_constant<int, 0>), f(integral_constant<int, 1>), ...
@@ -141,7 +173,7 @@ __device__ __forceinline__ void each(F f, std::integer_sequence<int, K...>) {
 // wn of the tile on, summed over L and added to acc.  LDS holds NT rows a step.
 // meanwhile() runs behind the first loads, which are under way meanwhile.
 template <typename FOp, typename NOp, int NT, int KF, int KN, typename Meanwhile>
-__device__ __forceinline__ void tile_loop(const FOp& fo, const NOp& no, uint16_t* lds, int wf, int wn, int32_t len,
+__device__ __forceinline__ void tile_loop(FOp fo, NOp no, uint16_t* lds, int wf, int wn, int32_t len,
                                           f32x4 (&acc)[KF][KN], Meanwhile meanwhile) {
     // LDS is a ring of whole steps of both operands; with 256 rows, of which two
     // steps and a half fit, of units of one operand's step, F's and N's in turn.
@@ -159,15 +191,15 @@ __device__ __forceinline__ void tile_loop(const FOp& fo, const NOp& no, uint16_t
     auto n_at = [&](int32_t slot) { return kUnits ? ring(slot + 1) * kBuffer : slot * kBuffer + kUnit; };
     auto f_to = [&](int32_t slot) { return base + f_at(slot) * 2 + w * kFL * 1024; };
     auto n_to = [&](int32_t slot) { return base + n_at(slot) * 2 + w * kNL * 1024; };
-    auto load_f = [&](int32_t s, int32_t slot) { load_step(fo, f_to(slot), s * kStepL, std::make_integer_sequence<int, kFL>{}); };
-    auto load_n = [&](int32_t s, int32_t slot) { load_step(no, n_to(slot), s * kStepL, std::make_integer_sequence<int, kNL>{}); };
+    auto load_f = [&](int32_t slot) { load_step(fo, f_to(slot), std::make_integer_sequence<int, kFL>{}); };
+    auto load_n = [&](int32_t slot) { load_step(no, n_to(slot), std::make_integer_sequence<int, kNL>{}); };
     constexpr int kStride = kUnits ? 2 : 1;  // slots of a step
 #pragma unroll
     for (int s = 0; s < kAheadF; ++s) {
-        if (s < kAheadN) load_n(s, s * kStride);
-        load_f(s, s * kStride);
+        if (s < kAheadN) load_n(s * kStride);
+        load_f(s * kStride);
     }
-    load_n(kAheadN, kAheadN * kStride);
+    load_n(kAheadN * kStride);
     meanwhile();
     // 256 results in accumulation registers, the operands in the other 256: left
     // to itself the compiler moves results between the two in every step
@@ -201,11 +233,10 @@ __device__ __forceinline__ void tile_loop(const FOp& fo, const NOp& no, uint16_t
     static_assert(kReadGap >= 1, "");
     const int32_t steps = (len + kStepL - 1) / kStepL;
     int32_t slot = 0;
-    auto half_step = [&](auto half_, int32_t from, const auto& op, const auto& at, uint32_t to, auto loads) {
+    auto half_step = [&](auto half_, int32_t from, auto& op, uint32_t to, auto loads) {
         constexpr int half = decltype(half_)::value, kLoads = decltype(loads)::value, kGap = kProducts / kLoads;
         static_assert(kGap >= 1, "");
         const uint16_t *const f_from = lane_f[half ^ 1] + f_at(from), *const n_from = lane_n[half ^ 1] + n_at(from);
-        int32_t voff = 0;
         each([&](auto k_) {
             constexpr int k = decltype(k_)::value, f = k / KN, n = k % KN, j = k / kGap;
             __builtin_amdgcn_sched_barrier(0);
@@ -213,26 +244,27 @@ __device__ __forceinline__ void tile_loop(const FOp& fo, const NOp& no, uint16_t
             __builtin_amdgcn_sched_barrier(0);
             if constexpr (k % kReadGap == 0 && k / kReadGap < kReads) read(half ^ 1, f_from, n_from, k / kReadGap);
             if constexpr (j < kLoads && kGap == 1) {
-                aim_and_load16<j * 1024>(to, op.source(at, j), op.offset(at, j));
+                aim_and_load16<j * 1024>(to, op.source(j), op.voff[j]);
             } else if constexpr (j < kLoads && k % kGap == 0) {
-                voff = op.offset(at, j);
                 aim16<j * 1024>(to);
+            } else if constexpr (j < kLoads && k % kGap == 1) {
+                load16(op.source(j), op.voff[j]);
             }
-            if constexpr (j < kLoads && kGap > 1 && k % kGap == 1) load16(op.source(at, j), voff);
         }, std::make_integer_sequence<int, kProducts>{});
         __builtin_amdgcn_sched_barrier(0);
+        op.advance();
     };
     using First = std::integral_constant<int, 0>;
     using Second = std::integral_constant<int, 1>;
     for (int32_t s = 0; s < steps; ++s) {
         const int32_t after = ring(slot + kStride);
-        half_step(First{}, slot, fo, fo.at((s + kAheadF) * kStepL), f_to(ring(slot + (kUnits ? 4 : kRing - 1))),
+        half_step(First{}, slot, fo, f_to(ring(slot + (kUnits ? 4 : kRing - 1))),
                   std::integral_constant<int, kFL>{});
         // the next step has landed, in every wave
         asm volatile("s_waitcnt vmcnt(%0)" ::"n"(kUnits ? kFL : (kRing - 2) * (kFL + kNL)) : "memory");
         lds_barrier();
         // of the freed units, N's of the step after the next takes this step's F's
-        half_step(Second{}, after, no, no.at((s + 1 + kAheadN) * kStepL), n_to(kUnits ? ring(slot + 4) : slot),
+        half_step(Second{}, after, no, n_to(kUnits ? ring(slot + 4) : slot),
                   std::integral_constant<int, kNL>{});
         slot = after;
     }
