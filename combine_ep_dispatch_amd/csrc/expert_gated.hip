@@ -13,7 +13,7 @@ namespace epx {
 namespace {
 
 template <int KF, int KN>
-__device__ __forceinline__ void adapters_of(const BlockArgs& a, const RowTile& t, int32_t c0, int32_t wn, f32x4 (&acc)[KF][KN]) {
+__device__ __forceinline__ void adapters_of(const BlockArgs& a, const LoopTile& t, int32_t c0, int32_t wn, f32x4 (&acc)[KF][KN]) {
     const int i = threadIdx.x % 16;
     add_adapters<KF, KN>(a, t.first, t.rows, wn, [&](int f, int32_t ad, int32_t c) {
         const int32_t col = c0 + f / 2 * 16 + i;  // of act
@@ -27,25 +27,27 @@ __device__ __forceinline__ void adapters_of(const BlockArgs& a, const RowTile& t
 template <bool BACKWARD, bool LORA>
 __global__ __launch_bounds__(kLoopThreads) __attribute__((amdgpu_waves_per_eu(1, 1))) void k_gated(BlockArgs a, int32_t ftiles) {
     __shared__ __align__(1024) uint16_t lds[kLoopLds / 2];
-    int32_t ft;
-    const RowTile t = find_row_tile<kLoopThreads, kTileN>(
-        a.e, reinterpret_cast<int32_t*>(lds), [&](int32_t rt, int32_t& f) { return xcd_tile(rt, ftiles, f); }, ft);
-    if (t.expert < 0) return;
-    __syncthreads();  // the words that named the tile become step 0
     const int lane = threadIdx.x & (kWave - 1), i = lane % 16, q = lane / 16;
-    const int32_t a0 = ft * (kTileF / 2), I = a.I;
+    const int32_t I = a.I, in = a.e.in;
     GatedOperand fo;
-    fo.init(a.e.w + (int64_t)t.expert * a.e.on * a.e.in, a0, I, a.e.in);
-    by_rows(t.rows, [&](auto nt) {
-        constexpr int NT = decltype(nt)::value, KF = Shape<NT>::kF, KN = Shape<NT>::kN;
-        const int wf = Shape<NT>::wf(), wn = Shape<NT>::wn();
-        LoopRows<NT> no;
-        no.init(a.e.x + t.first * a.e.in, t.rows, a.e.in, a.e.in);
-        f32x4 acc[KF][KN] = {};
-        const int32_t c0 = a0 + wf / 2;  // the wave's first column of act
-        tile_loop<GatedOperand, LoopRows<NT>, NT>(fo, no, lds, wf, wn, a.e.in, acc, [&] {
-            if constexpr (LORA) adapters_of(a, t, c0, wn, acc);
-        });
+    fo.init(in);
+    auto start_f = [&](GatedOperand& op, const LoopTile& t) {
+        const int32_t c0 = t.ft * (kTileF / 2);
+        const bool on = t.expert >= 0;
+        op.start(on ? a.e.w + ((int64_t)t.expert * a.e.on + c0) * in : a.e.w, on ? I : 0, on ? I - c0 : 0);
+    };
+    auto start_n = [&](LoopRows<kTileN>& op, const LoopTile& t) {
+        op.start(a.e.x + t.first * in, t.expert >= 0 ? t.rows : 0);
+    };
+    auto begin = [&](auto nt, const LoopTile& t, auto& acc) {
+        using S = Shape<decltype(nt)::value>;
+        if constexpr (LORA) adapters_of<S::kF, S::kN>(a, t, t.ft * (kTileF / 2) + S::wf() / 2, S::wn(), acc);
+    };
+    run_tiles(a.e, ftiles, in, lds, fo, start_f, start_n, begin, [&](auto nt, const LoopTile& t, auto& acc) {
+        using S = Shape<decltype(nt)::value>;
+        constexpr int KF = S::kF, KN = S::kN;
+        const int wn = S::wn();
+        const int32_t c0 = t.ft * (kTileF / 2) + S::wf() / 2;  // the wave's first column of act
         // acc[2 p][n][j], acc[2 p + 1][n][j]: g and u of column c0 + 16 p + 4 q + j, row wn + 16 n + i
         uint16_t* const act = static_cast<uint16_t*>(a.e.out);
 #pragma unroll
@@ -109,13 +111,13 @@ __global__ __launch_bounds__(256) void k_gated_probs(BlockArgs a) {
 template <bool BACKWARD>
 hipError_t gated(const BlockArgs& a, hipStream_t stream) {
     const int32_t ftiles = (a.I + kTileF / 2 - 1) / (kTileF / 2);
-    const int64_t blocks = (max_row_tiles(a.e, kTileN) * ftiles + 7) / 8 * 8;
+    unsigned blocks;
+    if (const hipError_t e = loop_blocks(a.e, ftiles, blocks)) return e;
     if (blocks == 0) return hipSuccess;
-    if (const hipError_t e = check_grid(blocks, kLoopThreads)) return e;
     if (a.l.rank > 0)
-        hipLaunchKernelGGL((k_gated<BACKWARD, true>), dim3((unsigned)blocks), dim3(kLoopThreads), 0, stream, a, ftiles);
+        hipLaunchKernelGGL((k_gated<BACKWARD, true>), dim3(blocks), dim3(kLoopThreads), 0, stream, a, ftiles);
     else
-        hipLaunchKernelGGL((k_gated<BACKWARD, false>), dim3((unsigned)blocks), dim3(kLoopThreads), 0, stream, a, ftiles);
+        hipLaunchKernelGGL((k_gated<BACKWARD, false>), dim3(blocks), dim3(kLoopThreads), 0, stream, a, ftiles);
     return hipGetLastError();
 }
 

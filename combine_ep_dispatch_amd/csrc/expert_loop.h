@@ -1,5 +1,6 @@
 // Tiles of 256 features by up to 256 rows whose product ends in an epilogue of
-// its own: the gated block and the products with adapters.
+// its own: the gated block and the products with adapters.  A workgroup of 4 waves
+// a CU takes tile after tile; the loads run on from one to the next.
 #pragma once
 
 #include <type_traits>
@@ -13,7 +14,99 @@ namespace epx {
 constexpr int kLoopWaves = 4;
 constexpr int kLoopThreads = kLoopWaves * kWave;
 constexpr int kTileF = 256, kTileN = 256;  // features (of both projections, where gated) and rows of a tile
+constexpr int kFewRows = 128;              // tiles of up to as many rows come last
 constexpr int kLoopLds = 160 * 1024;       // all of it: one workgroup a CU
+constexpr int kCus = 256;
+
+struct LoopTile {
+    int32_t expert;  // -1: no such tile
+    int32_t rows;    // of the tile, 1..kTileN
+    int32_t ft;      // its feature tile
+    int64_t first;   // its first receive row
+};
+
+// The tiles that a workgroup takes in turn.  Every wave keeps, for the run of
+// groups that each lane looks after, how many row tiles come before and up to it:
+// those of more than kFewRows rows, and the rest, which are taken last, so that the
+// CUs end together (1024 rows an expert on average: 8 of the ones and 1 of the
+// others a CU).  No memory but the layout's is used.  Of both kinds each XCD
+// takes an eighth, in blocks of 4 row tiles by all feature tiles, whose operands
+// the workgroups that run together share in its L2.
+struct LoopTiles {
+    int32_t before[2], upto[2];  // of this lane's groups
+    int32_t total[2], ftiles, per;
+
+    static __device__ __forceinline__ int32_t tiles_of(int32_t rows, int kind) {
+        const int32_t rest = rows % kTileN;
+        return kind == 0 ? rows / kTileN + (rest > kFewRows) : rest > 0 && rest <= kFewRows;
+    }
+    __device__ __forceinline__ void init(const ExpertArgs& a, int32_t f) {
+        const int lane = threadIdx.x & (kWave - 1);
+        ftiles = f;
+        per = (a.NG + kWave - 1) / kWave;
+        int32_t mine[2] = {0, 0};
+        for (int g = lane * per; g < min((lane + 1) * per, a.NG); ++g) {
+            const int32_t rows = group_rows(a, g).rows;
+            mine[0] += tiles_of(rows, 0);
+            mine[1] += tiles_of(rows, 1);
+        }
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            upto[k] = wave_inclusive_sum(mine[k]);
+            before[k] = upto[k] - mine[k];
+            total[k] = __builtin_amdgcn_readlane(upto[k], kWave - 1);
+        }
+    }
+    // The n-th tile of this workgroup.
+    __device__ __forceinline__ LoopTile get(const ExpertArgs& a, int32_t n) const {
+        const int32_t x = (int32_t)(blockIdx.x % 8);
+        int32_t at = uniform((int32_t)(blockIdx.x / 8 + (uint32_t)n * (gridDim.x / 8)));
+        LoopTile t = {-1, 1, 0, 0};
+#pragma unroll
+        for (int kind = 0; kind < 2; ++kind) {
+            const int32_t tiles = total[kind] * ftiles, share = (tiles + 7) / 8;
+            const int32_t mine = max(min(share, tiles - x * share), 0);
+            if (at >= mine) {
+                at -= mine;
+                continue;
+            }
+            const int32_t all = x * share + at, block = all / (4 * ftiles), r0 = block * 4, height = min(4, total[kind] - r0);
+            const int32_t in = all - block * 4 * ftiles, want = r0 + in % height;
+            t.ft = in / height;
+            const bool owner = want >= before[kind] && want < upto[kind];
+            int32_t expert = 0, rows = 0, first = 0;
+            if (owner) {
+                const int lane = threadIdx.x & (kWave - 1);
+                int32_t b = before[kind];
+                for (int g = lane * per; g < min((lane + 1) * per, a.NG); ++g) {
+                    const GroupRows r = group_rows(a, g);
+                    const int32_t c = tiles_of(r.rows, kind);
+                    if (want < b + c) {
+                        const int32_t skip = kind == 0 ? (want - b) * kTileN : r.rows / kTileN * kTileN;
+                        expert = group_expert(a, g);
+                        rows = min(kTileN, r.rows - skip);
+                        first = (int32_t)(r.first + skip);
+                        break;
+                    }
+                    b += c;
+                }
+            }
+            const int l = __builtin_ctzll(__builtin_amdgcn_ballot_w64(owner) | 1ull << 63);
+            t.expert = __builtin_amdgcn_readlane(expert, l);
+            t.rows = __builtin_amdgcn_readlane(rows, l);
+            t.first = __builtin_amdgcn_readlane(first, l);
+            break;
+        }
+        return {uniform(t.expert), uniform(t.rows), uniform(t.ft), uniform((int32_t)t.first)};
+    }
+};
+
+// Workgroups of a launch, and whether the tiles can be counted in 32 bits.
+inline hipError_t loop_blocks(const ExpertArgs& a, int32_t ftiles, unsigned& blocks) {
+    const int64_t tiles = max_row_tiles(a, kTileN) * ftiles;
+    blocks = (unsigned)((tiles < kCus ? tiles : kCus) + 7) / 8 * 8;
+    return tiles >= int64_t(1) << 31 ? hipErrorInvalidConfiguration : hipSuccess;
+}
 
 // A load of 16 bytes a lane to LDS (16 l for lane l), as load_to_lds, in two parts
 // that other instructions go between: where to, in m0, and the load, at least one
@@ -49,8 +142,10 @@ __device__ __forceinline__ i32x4 descriptor(const void* base, int32_t bytes) {
     return {(int32_t)uniform((uint32_t)p), (int32_t)uniform((uint32_t)(p >> 32) & 0xFFFFu), uniform(bytes), kBufferWord3};
 }
 
-// rs, whose words were written 5 wait states ago at least.
+// rs in scalar registers, written 5 wait states ago at least.
 __device__ __forceinline__ i32x4 settled(i32x4 rs) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) rs[k] = uniform(rs[k]);
 #ifdef __HIP_DEVICE_COMPILE__
     asm volatile("s_nop 4" : "+s"(rs));
 #endif
@@ -65,34 +160,34 @@ __device__ __forceinline__ void move_on(i32x4& rs, int64_t bytes) {
 }
 
 // The operands as expert_tile.h lays them out, loaded step after step: a lane's
-// offsets stay, the descriptors move on.  (A vector instruction between two matrix
-// instructions costs about 9 cycles: with an addition for each load the loop took
-// 272 000 instead of 256 000.)
+// offsets stay, the descriptors move on (advance()).  start() sets an operand to a
+// tile's first step; ready(s) comes before the loads of step s wherever that may be
+// one that L ends in, or one behind it, which loads zeros.
 template <int BM>
 struct LoopRows : RowsOperand<BM, kLoopWaves> {
     using Base = RowsOperand<BM, kLoopWaves>;
     i32x4 rs;
-    int32_t left;  // values of L from the next step on
 
-    __device__ __forceinline__ void init(const uint16_t* p, int32_t rows, int32_t pitch, int32_t l) {
-        Base::init(p, rows, pitch, l);
-        rs = settled(descriptor(p, this->records));
-        left = l;
-        if (left < kStepL) trim();
+    __device__ __forceinline__ void offsets() { Base::init(nullptr, 0, this->ld, this->len); }
+    __device__ __forceinline__ void init(int32_t l) { Base::init(nullptr, 0, l, l); }
+    __device__ __forceinline__ void start(const uint16_t* p, int32_t rows) {
+        rs = settled(descriptor(p, rows * this->ld * 2));
     }
-    // The last step, in part: chunks past its end are outside.  Behind it everything is.
-    __device__ __forceinline__ void trim() {
-        if (left <= 0) rs[2] = 0;
+    __device__ __forceinline__ void trim(int32_t s) {
 #pragma unroll
         for (int j = 0; j < Base::kLoads; ++j)
-            if (this->chunk[j % 2] * 8 >= left) this->voff[j] = kOutside;
+            this->voff[j] = s * kStepL + this->chunk[j % 2] * 8 >= this->len ? kOutside : this->voff[j];
+    }
+    __device__ __forceinline__ void ready(int32_t s, bool ragged) {
+        if (!ragged) return;
+        offsets();
+        trim(s);
     }
     __device__ __forceinline__ void advance() {
         move_on(rs, kStepL * 2);
-        rs[2] -= kStepL * 2;
-        left -= kStepL;
-        if (left < kStepL) trim();
+        rs[2] -= min(rs[2], kStepL * 2);
     }
+    __device__ __forceinline__ void settle() { rs = settled(rs); }
     __device__ __forceinline__ i32x4 source(int) const { return rs; }
     // Where a lane's values of half a step are in the operand's LDS tile, from row m0
     // on, and the fragment 16 f rows further.
@@ -110,25 +205,37 @@ struct LoopRows : RowsOperand<BM, kLoopWaves> {
 struct GatedOperand : LoopRows<kTileF> {
     i32x4 up;
 
-    // p: the expert's weights; a0: first column of act; inter: their number
-    __device__ __forceinline__ void init(const uint16_t* p, int32_t a0, int32_t inter, int32_t l) {
+    __device__ __forceinline__ void offsets() {
         const int lane = threadIdx.x & (kWave - 1), w = uniform((int32_t)(threadIdx.x / kWave));
-        const uint16_t* const gate = p + (int64_t)a0 * l;
-        Base::init(gate, min(kTileF / 2, inter - a0), l, l);
-        rs = settled(descriptor(gate, records));
-        up = settled(descriptor(gate + (int64_t)inter * l, records));
 #pragma unroll
         for (int j = 0; j < kLoads; ++j) {
             const int at = w * kLoads + j;  // 8 rows of LDS: half of a gate's or an up's 16
-            voff[j] = (at / 4 * 16 + at % 2 * 8 + lane / 8) * l * 2 + chunk[j % 2] * 16;
+            voff[j] = (at / 4 * 16 + at % 2 * 8 + lane / 8) * ld * 2 + chunk[j % 2] * 16;
         }
-        left = l;
-        if (left < kStepL) trim();
+    }
+    __device__ __forceinline__ void init(int32_t l) {
+        Base::init(nullptr, 0, l, l);
+        offsets();
+    }
+    // gate: the tile's first row of the gate projection; inter rows behind it the up's; cols: rows left of each
+    __device__ __forceinline__ void start(const uint16_t* gate, int32_t inter, int32_t cols) {
+        const int32_t bytes = min(kTileF / 2, cols) * ld * 2;
+        rs = settled(descriptor(gate, bytes));
+        up = settled(descriptor(gate + (int64_t)inter * ld, bytes));
+    }
+    __device__ __forceinline__ void ready(int32_t s, bool ragged) {
+        if (!ragged) return;
+        offsets();
+        trim(s);
     }
     __device__ __forceinline__ void advance() {
         LoopRows<kTileF>::advance();
         move_on(up, kStepL * 2);
         up[2] = rs[2];
+    }
+    __device__ __forceinline__ void settle() {
+        rs = settled(rs);
+        up = settled(up);
     }
     __device__ __forceinline__ i32x4 source(int j) const { return j / 2 % 2 ? up : rs; }
 };
@@ -136,18 +243,18 @@ struct GatedOperand : LoopRows<kTileF> {
 struct LoopCols : ColsOperand<kTileF, kLoopWaves> {
     using Base = ColsOperand<kTileF, kLoopWaves>;
     i32x4 rs;
-    int32_t l0;  // the next step's first row
 
-    __device__ __forceinline__ void init(const uint16_t* p, int32_t cols, int32_t pitch, int32_t l, int32_t m0) {
-        Base::init(p, cols, pitch, l, m0);
+    // p: the weights' column f0; cols: columns from it on; pitch, rows: the weights'
+    __device__ __forceinline__ void start(const uint16_t* p, int32_t f0, int32_t cols, int32_t pitch, int32_t rows) {
+        Base::init(p, cols, pitch, rows, f0);
         rs = settled(descriptor(p, records(0)));
-        l0 = 0;
     }
-    __device__ __forceinline__ void advance() {
-        move_on(rs, (int64_t)kStepL * ld * 2);
-        l0 += kStepL;
-        const int32_t rows = min(len - l0, kStepL);
-        rs[2] = rows > 0 ? rows * ld * 2 - cut : 0;
+    __device__ __forceinline__ void ready(int32_t s, bool) { rs[2] = records(s * kStepL); }
+    __device__ __forceinline__ void advance() { move_on(rs, (int64_t)kStepL * ld * 2); }
+    __device__ __forceinline__ void settle() {
+        rs = settled(rs);
+        len = uniform(len);
+        cut = uniform(cut);
     }
     __device__ __forceinline__ i32x4 source(int) const { return rs; }
     static __device__ __forceinline__ int32_t lane_at(int, int) { return 0; }
@@ -156,124 +263,23 @@ struct LoopCols : ColsOperand<kTileF, kLoopWaves> {
     }
 };
 
-// A wave's loads of an operand's next step, to its part of LDS.
-template <typename Op, int... J>
-__device__ __forceinline__ void load_step(Op& op, uint32_t to, std::integer_sequence<int, J...>) {
-    (aim_and_load16<J * 1024>(to, op.source(J), op.voff[J]), ...);
-    op.advance();
-}
-
 // f(integral_constant<int, 0>), f(integral_constant<int, 1>), ...
 template <typename F, int... K>
 __device__ __forceinline__ void each(F f, std::integer_sequence<int, K...>) {
     (f(std::integral_constant<int, K>{}), ...);
 }
 
-// A wave's KF x KN fragments of 16 features by 16 rows, from feature wf and row
-// wn of the tile on, summed over L and added to acc.  LDS holds NT rows a step.
-// meanwhile() runs behind the first loads, which are under way meanwhile.
-template <typename FOp, typename NOp, int NT, int KF, int KN, typename Meanwhile>
-__device__ __forceinline__ void tile_loop(FOp fo, NOp no, uint16_t* lds, int wf, int wn, int32_t len,
-                                          f32x4 (&acc)[KF][KN], Meanwhile meanwhile) {
-    // LDS is a ring of whole steps of both operands; with 256 rows, of which two
-    // steps and a half fit, of units of one operand's step, F's and N's in turn.
-    constexpr bool kUnits = NT == kTileF;
-    constexpr int kUnit = kTileF * kStepL, kBuffer = kUnits ? kUnit : (kTileF + NT) * kStepL;
-    constexpr int kRing = kLoopLds / 2 / kBuffer;
-    constexpr int kAheadF = kUnits ? 2 : kRing - 1, kAheadN = kUnits ? 1 : kRing - 1;
-    constexpr int kFL = FOp::kLoads, kNL = NOp::kLoads;
-    static_assert(kUnits ? kRing == 5 : kRing >= 3, "");
-    const int w = uniform((int32_t)(threadIdx.x / kWave));
-    const uint32_t base = uniform((uint32_t)(uintptr_t)(EPX_LDS const void*)lds);
-    auto ring = [](int32_t v) { return v >= kRing ? v - kRing : v; };
-    // element of LDS where a step's operands begin, by the step's slot
-    auto f_at = [&](int32_t slot) { return slot * kBuffer; };
-    auto n_at = [&](int32_t slot) { return kUnits ? ring(slot + 1) * kBuffer : slot * kBuffer + kUnit; };
-    auto f_to = [&](int32_t slot) { return base + f_at(slot) * 2 + w * kFL * 1024; };
-    auto n_to = [&](int32_t slot) { return base + n_at(slot) * 2 + w * kNL * 1024; };
-    auto load_f = [&](int32_t slot) { load_step(fo, f_to(slot), std::make_integer_sequence<int, kFL>{}); };
-    auto load_n = [&](int32_t slot) { load_step(no, n_to(slot), std::make_integer_sequence<int, kNL>{}); };
-    constexpr int kStride = kUnits ? 2 : 1;  // slots of a step
-#pragma unroll
-    for (int s = 0; s < kAheadF; ++s) {
-        if (s < kAheadN) load_n(s * kStride);
-        load_f(s * kStride);
-    }
-    load_n(kAheadN * kStride);
-    meanwhile();
-    // 256 results in accumulation registers, the operands in the other 256: left
-    // to itself the compiler moves results between the two in every step
-#pragma unroll
-    for (int f = 0; f < KF; ++f)
-#pragma unroll
-        for (int n = 0; n < KN; ++n) in_agprs(acc[f][n]);
-    // Step 0 has landed when only what was issued behind it is outstanding
-    // (loads return in order, and past the end they still count and write zeros).
-    asm volatile("s_waitcnt vmcnt(%0)" ::"n"((kAheadF - 1) * kFL + kAheadN * kNL) : "memory");
-    lds_barrier();
-    constexpr int kReads = KF + KN;  // of half a step
-    bf16x8 fa[2][KF], fb[2][KN];
-    const uint16_t* const lane_f[2] = {lds + FOp::lane_at(wf, 0), lds + FOp::lane_at(wf, 1)};
-    const uint16_t* const lane_n[2] = {lds + NOp::lane_at(wn, 0), lds + NOp::lane_at(wn, 1)};
-    auto read = [&](int half, const uint16_t* f, const uint16_t* n, int r) {
-        if (r < KN)
-            fb[half][r] = NOp::fragment_at(n, r, wn, half);
-        else
-            fa[half][r - KN] = FOp::fragment_at(f, r - KN, wf, half);
-    };
-#pragma unroll
-    for (int r = 0; r < kReads; ++r) read(0, lane_f[0] + f_at(0), lane_n[0] + n_at(0), r);
-    // Each half of a step multiplies the fragments that the half before read, and
-    // reads the next one's: first the second half's, then, behind the barrier, the
-    // next step's first.  By that barrier every wave has read all of this step,
-    // whose buffers are filled from then on.  Loads and reads go one by one between
-    // the matrix instructions, each of which leaves time to issue three others.
-    constexpr int kProducts = KF * KN;
-    constexpr int kReadGap = (kProducts - 1) / kReads < 3 ? (kProducts - 1) / kReads : 3;
-    static_assert(kReadGap >= 1, "");
-    const int32_t steps = (len + kStepL - 1) / kStepL;
-    int32_t slot = 0;
-    auto half_step = [&](auto half_, int32_t from, auto& op, uint32_t to, auto loads) {
-        constexpr int half = decltype(half_)::value, kLoads = decltype(loads)::value, kGap = kProducts / kLoads;
-        static_assert(kGap >= 1, "");
-        const uint16_t *const f_from = lane_f[half ^ 1] + f_at(from), *const n_from = lane_n[half ^ 1] + n_at(from);
-        each([&](auto k_) {
-            constexpr int k = decltype(k_)::value, f = k / KN, n = k % KN, j = k / kGap;
-            __builtin_amdgcn_sched_barrier(0);
-            acc[f][n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fa[half][f], fb[half][n], acc[f][n], 0, 0, 0);
-            __builtin_amdgcn_sched_barrier(0);
-            if constexpr (k % kReadGap == 0 && k / kReadGap < kReads) read(half ^ 1, f_from, n_from, k / kReadGap);
-            if constexpr (j < kLoads && kGap == 1) {
-                aim_and_load16<j * 1024>(to, op.source(j), op.voff[j]);
-            } else if constexpr (j < kLoads && k % kGap == 0) {
-                aim16<j * 1024>(to);
-            } else if constexpr (j < kLoads && k % kGap == 1) {
-                load16(op.source(j), op.voff[j]);
-            }
-        }, std::make_integer_sequence<int, kProducts>{});
-        __builtin_amdgcn_sched_barrier(0);
-        op.advance();
-    };
-    using First = std::integral_constant<int, 0>;
-    using Second = std::integral_constant<int, 1>;
-    for (int32_t s = 0; s < steps; ++s) {
-        const int32_t after = ring(slot + kStride);
-        half_step(First{}, slot, fo, f_to(ring(slot + (kUnits ? 4 : kRing - 1))),
-                  std::integral_constant<int, kFL>{});
-        // the next step has landed, in every wave
-        asm volatile("s_waitcnt vmcnt(%0)" ::"n"(kUnits ? kFL : (kRing - 2) * (kFL + kNL)) : "memory");
-        lds_barrier();
-        // of the freed units, N's of the step after the next takes this step's F's
-        half_step(Second{}, after, no, n_to(kUnits ? ring(slot + 4) : slot),
-                  std::integral_constant<int, kNL>{});
-        slot = after;
-    }
-    // No load may land in LDS that belongs to another workgroup by then.
-    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-}
+// What a tile's rows ask for: the 4 waves take 128 features by 128 rows each, or,
+// of at most 128 rows, 64 by all.
+template <int NT>
+struct Shape {
+    static constexpr int kWavesN = NT == kTileN ? 2 : 1;
+    static constexpr int kF = kTileF / (kLoopWaves / kWavesN) / 16, kN = NT / kWavesN / 16;
+    // first feature and row of this wave
+    static __device__ __forceinline__ int wf() { return uniform((int32_t)(threadIdx.x / kWave)) / kWavesN * kF * 16; }
+    static __device__ __forceinline__ int wn() { return uniform((int32_t)(threadIdx.x / kWave)) % kWavesN * kN * 16; }
+};
 
-// Results of one row tile, with the shape that its rows ask for: the 4 waves
-// take 128 features by 128 rows each, or, of at most 128 rows, 64 by all.
 template <typename Go>
 __device__ __forceinline__ void by_rows(int32_t rows, Go go) {
     if (rows > 128)
@@ -286,13 +292,142 @@ __device__ __forceinline__ void by_rows(int32_t rows, Go go) {
         go(std::integral_constant<int, 32>{});
 }
 
-template <int NT>
-struct Shape {
-    static constexpr int kWavesN = NT == kTileN ? 2 : 1;
-    static constexpr int kF = kTileF / (kLoopWaves / kWavesN) / 16, kN = NT / kWavesN / 16;
-    // first feature and row of this wave
-    static __device__ __forceinline__ int wf() { return uniform((int32_t)(threadIdx.x / kWave)) / kWavesN * kF * 16; }
-    static __device__ __forceinline__ int wn() { return uniform((int32_t)(threadIdx.x / kWave)) % kWavesN * kN * 16; }
-};
+// All tiles of this workgroup.  start_f(fo, tile) and start_n(no, tile) set the
+// operands to a tile; begin(shape, tile, acc) may add to the results beforehand;
+// end(shape, tile, acc) takes them: acc[f][n], 16 features by 16 rows each, from
+// feature Shape::wf() and row Shape::wn() of the tile on.
+//
+// LDS is a ring of five units of 32 KiB, a step of one operand each, F's and N's in
+// turn: two steps and a half.  Step s's are units 2 s and 2 s + 1 (mod 5).
+template <typename FOp, typename StartF, typename StartN, typename Begin, typename End>
+__device__ __forceinline__ void run_tiles(const ExpertArgs& a, int32_t ftiles, int32_t len, uint16_t* lds, FOp& fo,
+                                          StartF start_f, StartN start_n, Begin begin, End end) {
+    using NOp = LoopRows<kTileN>;
+    constexpr int kUnit = kTileF * kStepL, kRing = 5, kLoads = FOp::kLoads;
+    static_assert(kLoopLds / 2 == kRing * kUnit && kTileN == kTileF && NOp::kLoads == kLoads, "");
+    LoopTiles tiles;
+    tiles.init(a, ftiles);
+    LoopTile t = tiles.get(a, 0), next;
+    if (t.expert < 0) return;
+    const int w = uniform((int32_t)(threadIdx.x / kWave));
+    const uint32_t base = uniform((uint32_t)(uintptr_t)(EPX_LDS const void*)lds) + w * (kLoads * 1024);
+    auto ring = [](int32_t v) { return v >= kRing ? v - kRing : v; };
+    auto to = [&](int32_t unit) { return base + unit * (kUnit * 2); };
+    // The loads are two steps ahead: with three steps a tile at least they reach the next one's, no further.
+    const int32_t steps = max((len + kStepL - 1) / kStepL, 3);
+    const bool ragged = len != steps * kStepL;
+    NOp no;
+    no.init(len);
+    start_f(fo, t);
+    start_n(no, t);
+    auto load = [&](auto& op, int32_t unit) {
+        each([&](auto j_) {
+            constexpr int j = decltype(j_)::value;
+            aim_and_load16<j * 1024>(to(unit), op.source(j), op.voff[j]);
+        }, std::make_integer_sequence<int, kLoads>{});
+        op.advance();
+    };
+    no.ready(0, ragged);
+    fo.ready(0, ragged);
+    load(no, 1);
+    load(fo, 0);
+    no.ready(1, ragged);
+    fo.ready(1, ragged);
+    load(fo, 2);
+    load(no, 3);
+    // Step 0 has landed when only what was issued behind it is outstanding: loads
+    // return in order, and out of range they still count and write zeros.
+    asm volatile("s_waitcnt vmcnt(%0)" ::"n"(2 * kLoads) : "memory");
+    lds_barrier();
+    int32_t unit = 0;  // of the step's F
+    for (int32_t n = 1;; ++n) {
+        next = tiles.get(a, n);
+        by_rows(t.rows, [&](auto nt) {
+            constexpr int NT = decltype(nt)::value, KF = Shape<NT>::kF, KN = Shape<NT>::kN;
+            const int wf = Shape<NT>::wf(), wn = Shape<NT>::wn();
+            // The compiler takes what comes out of the previous tile's branches for
+            // different from lane to lane.
+            unit = uniform(unit);
+            fo.settle();
+            no.settle();
+            f32x4 acc[KF][KN] = {};
+            begin(nt, t, acc);
+            // 256 results in accumulation registers, the operands in the other 256: left
+            // to itself the compiler moves results between the two in every step
+#pragma unroll
+            for (int f = 0; f < KF; ++f)
+#pragma unroll
+                for (int n = 0; n < KN; ++n) in_agprs(acc[f][n]);
+            constexpr int kReads = KF + KN;  // of half a step
+            bf16x8 fa[2][KF], fb[2][KN];
+            const uint16_t* const lane_f[2] = {lds + FOp::lane_at(wf, 0), lds + FOp::lane_at(wf, 1)};
+            const uint16_t* const lane_n[2] = {lds + NOp::lane_at(wn, 0), lds + NOp::lane_at(wn, 1)};
+            auto read = [&](int half, const uint16_t* f, const uint16_t* n, int r) {
+                if (r < KN)
+                    fb[half][r] = NOp::fragment_at(n, r, wn, half);
+                else
+                    fa[half][r - KN] = FOp::fragment_at(f, r - KN, wf, half);
+            };
+            // The step's first half; behind the previous tile's last barrier it has landed.
+#pragma unroll
+            for (int r = 0; r < kReads; ++r) read(0, lane_f[0] + unit * kUnit, lane_n[0] + ring(unit + 1) * kUnit, r);
+            // Each half of a step multiplies the fragments that the half before read, and
+            // reads the next one's: first the second half's, then, behind the barrier, the
+            // next step's first.  By that barrier every wave has read all of this step,
+            // whose units are filled from then on.  Loads and reads go one by one between
+            // the matrix instructions, each of which leaves time to issue three others.
+            constexpr int kProducts = KF * KN, kGap = kProducts / kLoads;
+            constexpr int kReadGap = (kProducts - 1) / kReads < 3 ? (kProducts - 1) / kReads : 3;
+            static_assert(kReadGap >= 1 && kGap >= 1, "");
+            auto half_step = [&](auto half_, int32_t from, auto& op, int32_t into) {
+                constexpr int half = decltype(half_)::value;
+                const uint16_t *const f_from = lane_f[half ^ 1] + from * kUnit, *const n_from = lane_n[half ^ 1] + ring(from + 1) * kUnit;
+                const uint32_t at = to(into);
+                each([&](auto k_) {
+                    constexpr int k = decltype(k_)::value, f = k / KN, n = k % KN, j = k / kGap;
+                    __builtin_amdgcn_sched_barrier(0);
+                    acc[f][n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fa[half][f], fb[half][n], acc[f][n], 0, 0, 0);
+                    __builtin_amdgcn_sched_barrier(0);
+                    if constexpr (k % kReadGap == 0 && k / kReadGap < kReads) read(half ^ 1, f_from, n_from, k / kReadGap);
+                    if constexpr (j < kLoads && kGap == 1) {
+                        aim_and_load16<j * 1024>(at, op.source(j), op.voff[j]);
+                    } else if constexpr (j < kLoads && k % kGap == 0) {
+                        aim16<j * 1024>(at);
+                    } else if constexpr (j < kLoads && k % kGap == 1) {
+                        load16(op.source(j), op.voff[j]);
+                    }
+                }, std::make_integer_sequence<int, kProducts>{});
+                __builtin_amdgcn_sched_barrier(0);
+                op.advance();
+            };
+            // A step loads the one two behind it: the steps whose loads L neither begins
+            // nor ends with; the one that loads the last; two that load the next tile's.
+#pragma nounroll
+            for (int part = 0; part < 4; ++part) {
+                if (part == 2) {
+                    start_f(fo, next);
+                    start_n(no, next);
+                }
+                const int32_t ahead = part == 0 ? 2 : part == 1 ? steps - 1 : part - 2;
+                fo.ready(ahead, ragged);
+                no.ready(ahead, ragged);
+                for (int32_t s = part == 0 ? steps - 3 : 1; s > 0; --s) {
+                    const int32_t after = ring(unit + 2), free = ring(unit + 4);
+                    half_step(std::integral_constant<int, 0>{}, unit, fo, free);  // F of the step after the next
+                    // the next step has landed, in every wave, but for that F
+                    asm volatile("s_waitcnt vmcnt(%0)" ::"n"(kLoads) : "memory");
+                    lds_barrier();
+                    half_step(std::integral_constant<int, 1>{}, after, no, unit);  // its N, where this step's F was
+                    unit = after;
+                }
+            }
+            end(nt, t, acc);
+        });
+        t = next;
+        if (t.expert < 0) break;
+    }
+    // No load may land in LDS that belongs to another workgroup by then.
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+}
 
 }  // namespace epx

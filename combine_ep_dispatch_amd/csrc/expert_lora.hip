@@ -19,41 +19,45 @@ template <Product P>
 __global__ __launch_bounds__(kLoopThreads) __attribute__((amdgpu_waves_per_eu(1, 1))) void k_product(BlockArgs a, int32_t ftiles) {
     using FOp = typename std::conditional<P == kForward, LoopRows<kTileF>, LoopCols>::type;
     __shared__ __align__(1024) uint16_t lds[kLoopLds / 2];
-    int32_t ft;
-    const RowTile t = find_row_tile<kLoopThreads, kTileN>(
-        a.e, reinterpret_cast<int32_t*>(lds), [&](int32_t rt, int32_t& f) { return xcd_tile(rt, ftiles, f); }, ft);
-    if (t.expert < 0) return;
-    __syncthreads();  // the words that named the tile become step 0
     const int lane = threadIdx.x & (kWave - 1), i = lane % 16, q = lane / 16;
-    const int32_t f0 = ft * kTileF, F = P == kForward ? a.e.on : a.e.in, L = P == kForward ? a.e.in : a.e.on;
-    const uint16_t* const we = a.e.w + (int64_t)t.expert * a.e.on * a.e.in;
+    const int32_t F = P == kForward ? a.e.on : a.e.in, L = P == kForward ? a.e.in : a.e.on;
     FOp fo;
-    if constexpr (P == kForward)
-        fo.init(we + (int64_t)f0 * L, min(kTileF, F - f0), L, L);
-    else
-        fo.init(we + f0, F - f0, F, L, f0);
-    by_rows(t.rows, [&](auto nt) {
-        constexpr int NT = decltype(nt)::value, KF = Shape<NT>::kF, KN = Shape<NT>::kN;
-        const int wf = Shape<NT>::wf(), wn = Shape<NT>::wn();
-        LoopRows<NT> no;
-        no.init((P == kForward ? a.e.x : a.e.gy) + t.first * L, t.rows, L, L);
-        f32x4 acc[KF][KN] = {};
-        tile_loop<FOp, LoopRows<NT>, NT>(fo, no, lds, wf, wn, L, acc, [&] {
-            add_adapters<KF, KN>(a, t.first, t.rows, wn, [&](int f, int32_t ad, int32_t c) {
-                const int32_t fe = f0 + wf + f * 16 + i, rank = a.l.rank;
-                const int64_t pair = (int64_t)ad * (a.e.E + a.e.shared) + t.expert;
-                bf16x8 v = {};
-                if (fe >= F) return v;
-                if constexpr (P == kForward) {
-                    v = *reinterpret_cast<const bf16x8*>(a.l.b + (pair * F + fe) * rank + c * 8);
-                } else {
-                    const __bf16* const p = reinterpret_cast<const __bf16*>(a.l.a) + (pair * rank + c * 8) * F + fe;
+    if constexpr (P == kForward) fo.init(L);
+    auto start_f = [&](FOp& op, const LoopTile& t) {
+        const int32_t f0 = t.ft * kTileF;
+        const bool on = t.expert >= 0;
+        const uint16_t* const we = a.e.w + (on ? (int64_t)t.expert * a.e.on * a.e.in : 0);
+        if constexpr (P == kForward)
+            op.start(we + (int64_t)f0 * L, on ? min(kTileF, F - f0) : 0);
+        else
+            op.start(we + f0, f0, F - f0, F, on ? L : 0);
+    };
+    auto start_n = [&](LoopRows<kTileN>& op, const LoopTile& t) {
+        op.start((P == kForward ? a.e.x : a.e.gy) + t.first * L, t.expert >= 0 ? t.rows : 0);
+    };
+    auto begin = [&](auto nt, const LoopTile& t, auto& acc) {
+        using S = Shape<decltype(nt)::value>;
+        const int32_t f0 = t.ft * kTileF + S::wf();
+        add_adapters<S::kF, S::kN>(a, t.first, t.rows, S::wn(), [&](int f, int32_t ad, int32_t c) {
+            const int32_t fe = f0 + f * 16 + i, rank = a.l.rank;
+            const int64_t pair = (int64_t)ad * (a.e.E + a.e.shared) + t.expert;
+            bf16x8 v = {};
+            if (fe >= F) return v;
+            if constexpr (P == kForward) {
+                v = *reinterpret_cast<const bf16x8*>(a.l.b + (pair * F + fe) * rank + c * 8);
+            } else {
+                const __bf16* const p = reinterpret_cast<const __bf16*>(a.l.a) + (pair * rank + c * 8) * F + fe;
 #pragma unroll
-                    for (int k = 0; k < 8; ++k) v[k] = p[(int64_t)k * F];
-                }
-                return v;
-            }, acc);
-        });
+                for (int k = 0; k < 8; ++k) v[k] = p[(int64_t)k * F];
+            }
+            return v;
+        }, acc);
+    };
+    run_tiles(a.e, ftiles, L, lds, fo, start_f, start_n, begin, [&](auto nt, const LoopTile& t, auto& acc) {
+        using S = Shape<decltype(nt)::value>;
+        constexpr int KF = S::kF, KN = S::kN;
+        const int wn = S::wn(), wf = S::wf();
+        const int32_t f0 = t.ft * kTileF;
         // acc[f][n][j]: feature f0 + wf + 16 f + 4 q + j, row wn + 16 n + i
 #pragma unroll
         for (int n = 0; n < KN; ++n) {
@@ -74,10 +78,10 @@ __global__ __launch_bounds__(kLoopThreads) __attribute__((amdgpu_waves_per_eu(1,
 template <Product P>
 hipError_t product(const BlockArgs& a, hipStream_t stream) {
     const int32_t F = P == kForward ? a.e.on : a.e.in, ftiles = (F + kTileF - 1) / kTileF;
-    const int64_t blocks = (max_row_tiles(a.e, kTileN) * ftiles + 7) / 8 * 8;
+    unsigned blocks;
+    if (const hipError_t e = loop_blocks(a.e, ftiles, blocks)) return e;
     if (blocks == 0) return hipSuccess;
-    if (const hipError_t e = check_grid(blocks, kLoopThreads)) return e;
-    hipLaunchKernelGGL((k_product<P>), dim3((unsigned)blocks), dim3(kLoopThreads), 0, stream, a, ftiles);
+    hipLaunchKernelGGL((k_product<P>), dim3(blocks), dim3(kLoopThreads), 0, stream, a, ftiles);
     return hipGetLastError();
 }
 
