@@ -36,7 +36,7 @@ __global__ __launch_bounds__(kLoopThreads) __attribute__((amdgpu_waves_per_eu(1,
         const bool on = t.expert >= 0;
         op.start(on ? a.e.w + ((int64_t)t.expert * a.e.on + c0) * in : a.e.w, on ? I : 0, on ? I - c0 : 0);
     };
-    auto start_n = [&](LoopRows<kTileN>& op, const LoopTile& t) {
+    auto start_n = [&](auto& op, const LoopTile& t) {
         op.start(a.e.x + t.first * in, t.expert >= 0 ? t.rows : 0);
     };
     auto begin = [&](auto nt, const LoopTile& t, auto& acc) {

@@ -14,7 +14,6 @@ namespace epx {
 constexpr int kLoopWaves = 4;
 constexpr int kLoopThreads = kLoopWaves * kWave;
 constexpr int kTileF = 256, kTileN = 256;  // features (of both projections, where gated) and rows of a tile
-constexpr int kFewRows = 128;              // tiles of up to as many rows come last
 constexpr int kLoopLds = 160 * 1024;       // all of it: one workgroup a CU
 constexpr int kCus = 256;
 
@@ -25,79 +24,96 @@ struct LoopTile {
     int64_t first;   // its first receive row
 };
 
-// The tiles that a workgroup takes in turn.  Every wave keeps, for the run of
-// groups that each lane looks after, how many row tiles come before and up to it:
-// those of more than kFewRows rows, and the rest, which are taken last, so that the
-// CUs end together (1024 rows an expert on average: 8 of the ones and 1 of the
-// others a CU).  No memory but the layout's is used.  Of both kinds each XCD
-// takes an eighth, in blocks of 4 row tiles by all feature tiles, whose operands
-// the workgroups that run together share in its L2.
-struct LoopTiles {
-    int32_t before[2], upto[2];  // of this lane's groups
-    int32_t total[2], ftiles, per;
+// Tiles come in three kinds, by their rows; each kind fills LDS in its own way.
+constexpr int kKinds = 3;
+constexpr int kKindRows[kKinds] = {kTileN, 128, 32};  // at most
 
-    static __device__ __forceinline__ int32_t tiles_of(int32_t rows, int kind) {
+// The tiles that a workgroup takes in turn, kind after kind.  A group is cut into
+// as few tiles as can be, of one height: 896 rows are 4 of 224.  From five tiles on
+// they are full ones and what is left over, if that is at most half of one, which
+// then reads the weights once more.  32 experts of 4096 x 7168, us for one height and
+// for full tiles and the rest: 896 rows 1290 and 1450, 1040 rows 1645 and 1645, 996
+// to 1060 rows (a training step's) 1605 and 1510, where one height is 9 tiles a CU and
+// the other 8 and a rest.  Every wave
+// keeps, for the run of groups that each lane looks after, how many row tiles of
+// each kind come before and up to it; no memory but the layout's is used.  Of each
+// kind each XCD takes an eighth, in blocks of 4 row tiles by all feature tiles, whose
+// operands the workgroups that run together share in its L2, and hands them out in
+// turn.
+struct LoopTiles {
+    int32_t before[kKinds], upto[kKinds];  // of this lane's groups
+    int32_t total[kKinds], ftiles, per;
+
+    // Rows of a group that become a tile of their own, behind its full ones.
+    static __device__ __forceinline__ int32_t left_over(int32_t rows) {
         const int32_t rest = rows % kTileN;
-        return kind == 0 ? rows / kTileN + (rest > kFewRows) : rest > 0 && rest <= kFewRows;
+        return rows <= kKindRows[1] ? rows : rows > 4 * kTileN && rest <= kKindRows[1] ? rest : 0;
+    }
+    static __device__ __forceinline__ int32_t tiles_of(int32_t rows, int kind) {
+        const int32_t rest = left_over(rows);
+        if (kind == 0) return (rows - rest + kTileN - 1) / kTileN;
+        return kind == 1 ? rest > kKindRows[2] : rest > 0 && rest <= kKindRows[2];
     }
     __device__ __forceinline__ void init(const ExpertArgs& a, int32_t f) {
         const int lane = threadIdx.x & (kWave - 1);
         ftiles = f;
         per = (a.NG + kWave - 1) / kWave;
-        int32_t mine[2] = {0, 0};
+        int32_t mine[kKinds] = {};
         for (int g = lane * per; g < min((lane + 1) * per, a.NG); ++g) {
             const int32_t rows = group_rows(a, g).rows;
-            mine[0] += tiles_of(rows, 0);
-            mine[1] += tiles_of(rows, 1);
+#pragma unroll
+            for (int k = 0; k < kKinds; ++k) mine[k] += tiles_of(rows, k);
         }
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
+        for (int k = 0; k < kKinds; ++k) {
             upto[k] = wave_inclusive_sum(mine[k]);
             before[k] = upto[k] - mine[k];
             total[k] = __builtin_amdgcn_readlane(upto[k], kWave - 1);
         }
     }
-    // The n-th tile of this workgroup.
+    // How many tiles of a kind this workgroup's XCD takes, and the first of them.
+    __device__ __forceinline__ int32_t share(int kind, int32_t& from) const {
+        const int32_t tiles = total[kind] * ftiles, each = (tiles + 7) / 8;
+        from = (int32_t)(blockIdx.x % 8) * each;
+        return max(min(each, tiles - from), 0);
+    }
+    // The n-th tile of the kind of this workgroup: its turns go on from one kind to
+    // the next, so that all workgroups get as many tiles, give or take one.
+    template <int KIND>
     __device__ __forceinline__ LoopTile get(const ExpertArgs& a, int32_t n) const {
-        const int32_t x = (int32_t)(blockIdx.x % 8);
-        int32_t at = uniform((int32_t)(blockIdx.x / 8 + (uint32_t)n * (gridDim.x / 8)));
-        LoopTile t = {-1, 1, 0, 0};
+        const int32_t turns = uniform((int32_t)(gridDim.x / 8));
+        int32_t from = 0, before_us = 0;
 #pragma unroll
-        for (int kind = 0; kind < 2; ++kind) {
-            const int32_t tiles = total[kind] * ftiles, share = (tiles + 7) / 8;
-            const int32_t mine = max(min(share, tiles - x * share), 0);
-            if (at >= mine) {
-                at -= mine;
-                continue;
-            }
-            const int32_t all = x * share + at, block = all / (4 * ftiles), r0 = block * 4, height = min(4, total[kind] - r0);
-            const int32_t in = all - block * 4 * ftiles, want = r0 + in % height;
-            t.ft = in / height;
-            const bool owner = want >= before[kind] && want < upto[kind];
-            int32_t expert = 0, rows = 0, first = 0;
-            if (owner) {
-                const int lane = threadIdx.x & (kWave - 1);
-                int32_t b = before[kind];
-                for (int g = lane * per; g < min((lane + 1) * per, a.NG); ++g) {
-                    const GroupRows r = group_rows(a, g);
-                    const int32_t c = tiles_of(r.rows, kind);
-                    if (want < b + c) {
-                        const int32_t skip = kind == 0 ? (want - b) * kTileN : r.rows / kTileN * kTileN;
-                        expert = group_expert(a, g);
-                        rows = min(kTileN, r.rows - skip);
-                        first = (int32_t)(r.first + skip);
-                        break;
-                    }
-                    b += c;
+        for (int k = 0; k < KIND; ++k) before_us += share(k, from);
+        const int32_t mine = share(KIND, from);
+        int32_t at = uniform((int32_t)(blockIdx.x / 8)) - before_us % turns;
+        at = uniform((at < 0 ? at + turns : at) + n * turns);
+        if (at >= mine) return {-1, 1, 0, 0};
+        const int32_t all = from + at, block = all / (4 * ftiles), r0 = block * 4, height = min(4, total[KIND] - r0);
+        const int32_t in = all - block * 4 * ftiles, want = r0 + in % height, ft = in / height;
+        const bool owner = want >= before[KIND] && want < upto[KIND];
+        int32_t expert = 0, rows = 0, first = 0;
+        if (owner) {
+            const int lane = threadIdx.x & (kWave - 1);
+            int32_t b = before[KIND];
+            for (int g = lane * per; g < min((lane + 1) * per, a.NG); ++g) {
+                const GroupRows r = group_rows(a, g);
+                const int32_t c = tiles_of(r.rows, KIND);
+                if (want < b + c) {
+                    const int32_t rest = left_over(r.rows), cut = r.rows - rest;  // cut: in tiles of one height
+                    const int32_t height = KIND == 0 ? ((cut + c - 1) / c + 15) / 16 * 16 : rest;
+                    const int32_t skip = KIND == 0 ? (want - b) * height : cut;
+                    expert = group_expert(a, g);
+                    rows = KIND == 0 ? min(height, cut - skip) : rest;
+                    first = (int32_t)(r.first + skip);
+                    break;
                 }
+                b += c;
             }
-            const int l = __builtin_ctzll(__builtin_amdgcn_ballot_w64(owner) | 1ull << 63);
-            t.expert = __builtin_amdgcn_readlane(expert, l);
-            t.rows = __builtin_amdgcn_readlane(rows, l);
-            t.first = __builtin_amdgcn_readlane(first, l);
-            break;
         }
-        return {uniform(t.expert), uniform(t.rows), uniform(t.ft), uniform((int32_t)t.first)};
+        const int l = __builtin_ctzll(__builtin_amdgcn_ballot_w64(owner) | 1ull << 63);
+        return {__builtin_amdgcn_readlane(expert, l), __builtin_amdgcn_readlane(rows, l), uniform(ft),
+                __builtin_amdgcn_readlane(first, l)};
     }
 };
 
@@ -269,85 +285,99 @@ __device__ __forceinline__ void each(F f, std::integer_sequence<int, K...>) {
     (f(std::integral_constant<int, K>{}), ...);
 }
 
-// What a tile's rows ask for: the 4 waves take 128 features by 128 rows each, or,
-// of at most 128 rows, 64 by all.
+// What a tile's rows ask for: the 4 waves take 128 features by half of the rows
+// each, or, of at most 128 rows, 64 by all.
 template <int NT>
 struct Shape {
-    static constexpr int kWavesN = NT == kTileN ? 2 : 1;
+    static constexpr int kWavesN = NT > 128 ? 2 : 1;
     static constexpr int kF = kTileF / (kLoopWaves / kWavesN) / 16, kN = NT / kWavesN / 16;
     // first feature and row of this wave
     static __device__ __forceinline__ int wf() { return uniform((int32_t)(threadIdx.x / kWave)) / kWavesN * kF * 16; }
     static __device__ __forceinline__ int wn() { return uniform((int32_t)(threadIdx.x / kWave)) % kWavesN * kN * 16; }
 };
 
-template <typename Go>
+template <int KIND, typename Go>
 __device__ __forceinline__ void by_rows(int32_t rows, Go go) {
-    if (rows > 128)
-        go(std::integral_constant<int, 256>{});
-    else if (rows > 64)
-        go(std::integral_constant<int, 128>{});
-    else if (rows > 32)
-        go(std::integral_constant<int, 64>{});
-    else
+    if constexpr (KIND == 0) {
+        if (rows > 224)
+            go(std::integral_constant<int, 256>{});
+        else if (rows > 192)
+            go(std::integral_constant<int, 224>{});
+        else if (rows > 160)
+            go(std::integral_constant<int, 192>{});
+        else
+            go(std::integral_constant<int, 160>{});
+    } else if constexpr (KIND == 2) {
         go(std::integral_constant<int, 32>{});
+    } else if (rows > 64) {
+        go(std::integral_constant<int, 128>{});
+    } else {
+        go(std::integral_constant<int, 64>{});
+    }
 }
 
-// All tiles of this workgroup.  start_f(fo, tile) and start_n(no, tile) set the
-// operands to a tile; begin(shape, tile, acc) may add to the results beforehand;
-// end(shape, tile, acc) takes them: acc[f][n], 16 features by 16 rows each, from
-// feature Shape::wf() and row Shape::wn() of the tile on.
+// This workgroup's tiles of a kind.  start_f(fo, tile) and start_n(no, tile) set the operands to a tile; begin(shape, tile, acc) may add to the
+// results beforehand; end(shape, tile, acc) takes them: acc[f][n], 16 features by 16
+// rows each, from feature Shape::wf() and row Shape::wn() of the tile on.
 //
-// LDS is a ring of five units of 32 KiB, a step of one operand each, F's and N's in
-// turn: two steps and a half.  Step s's are units 2 s and 2 s + 1 (mod 5).
-template <typename FOp, typename StartF, typename StartN, typename Begin, typename End>
-__device__ __forceinline__ void run_tiles(const ExpertArgs& a, int32_t ftiles, int32_t len, uint16_t* lds, FOp& fo,
-                                          StartF start_f, StartN start_n, Begin begin, End end) {
-    using NOp = LoopRows<kTileN>;
-    constexpr int kUnit = kTileF * kStepL, kRing = 5, kLoads = FOp::kLoads;
-    static_assert(kLoopLds / 2 == kRing * kUnit && kTileN == kTileF && NOp::kLoads == kLoads, "");
-    LoopTiles tiles;
-    tiles.init(a, ftiles);
-    LoopTile t = tiles.get(a, 0), next;
+// LDS is a ring: of whole steps, three for tiles of up to 128 rows and four for up
+// to 32; of full tiles, whose steps are 64 KiB, of five units of 32 KiB, a step of
+// one operand each, F's and N's in turn (step s's are units 2 s and 2 s + 1).  A step
+// loads the one kAhead behind it into what the step before it has left.
+template <int KIND, typename FOp, typename StartF, typename StartN, typename Begin, typename End>
+__device__ __forceinline__ void run_kind(const ExpertArgs& a, const LoopTiles& tiles, int32_t len, uint16_t* lds,
+                                         FOp& fo, StartF start_f, StartN start_n, Begin begin, End end) {
+    constexpr bool kUnits = KIND == 0;
+    constexpr int kRows = kKindRows[KIND];
+    using NOp = LoopRows<kRows>;
+    constexpr int kUnit = kTileF * kStepL, kSlot = kUnits ? kUnit : (kTileF + kRows) * kStepL;
+    constexpr int kRing = kLoopLds / 2 / kSlot, kStride = kUnits ? 2 : 1, kAhead = kUnits ? 2 : kRing - 1;
+    constexpr int kFL = FOp::kLoads, kNL = NOp::kLoads;
+    static_assert(kUnits ? kRing == 5 : kRing >= 3, "");
+    LoopTile t = tiles.get<KIND>(a, 0), next;
     if (t.expert < 0) return;
     const int w = uniform((int32_t)(threadIdx.x / kWave));
-    const uint32_t base = uniform((uint32_t)(uintptr_t)(EPX_LDS const void*)lds) + w * (kLoads * 1024);
+    const uint32_t base = uniform((uint32_t)(uintptr_t)(EPX_LDS const void*)lds);
     auto ring = [](int32_t v) { return v >= kRing ? v - kRing : v; };
-    auto to = [&](int32_t unit) { return base + unit * (kUnit * 2); };
-    // The loads are two steps ahead: with three steps a tile at least they reach the next one's, no further.
-    const int32_t steps = max((len + kStepL - 1) / kStepL, 3);
+    // element of LDS where a step's operands begin, by its slot
+    auto f_at = [](int32_t slot) { return slot * kSlot; };
+    auto n_at = [&](int32_t slot) { return kUnits ? ring(slot + 1) * kSlot : slot * kSlot + kUnit; };
+    auto f_to = [&](int32_t slot) { return base + f_at(slot) * 2 + w * kFL * 1024; };
+    auto n_to = [&](int32_t slot) { return base + n_at(slot) * 2 + w * kNL * 1024; };
+    // With more steps a tile than kAhead the loads reach into the next one, no further.
+    const int32_t steps = max((len + kStepL - 1) / kStepL, kAhead + 1);
     const bool ragged = len != steps * kStepL;
     NOp no;
     no.init(len);
     start_f(fo, t);
     start_n(no, t);
-    auto load = [&](auto& op, int32_t unit) {
+    auto load = [&](auto& op, uint32_t to, auto loads) {
         each([&](auto j_) {
             constexpr int j = decltype(j_)::value;
-            aim_and_load16<j * 1024>(to(unit), op.source(j), op.voff[j]);
-        }, std::make_integer_sequence<int, kLoads>{});
+            aim_and_load16<j * 1024>(to, op.source(j), op.voff[j]);
+        }, std::make_integer_sequence<int, decltype(loads)::value>{});
         op.advance();
     };
-    no.ready(0, ragged);
-    fo.ready(0, ragged);
-    load(no, 1);
-    load(fo, 0);
-    no.ready(1, ragged);
-    fo.ready(1, ragged);
-    load(fo, 2);
-    load(no, 3);
+#pragma unroll
+    for (int s = 0; s < kAhead; ++s) {
+        fo.ready(s, ragged);
+        no.ready(s, ragged);
+        load(fo, f_to(s * kStride), std::integral_constant<int, kFL>{});
+        load(no, n_to(s * kStride), std::integral_constant<int, kNL>{});
+    }
     // Step 0 has landed when only what was issued behind it is outstanding: loads
     // return in order, and out of range they still count and write zeros.
-    asm volatile("s_waitcnt vmcnt(%0)" ::"n"(2 * kLoads) : "memory");
+    asm volatile("s_waitcnt vmcnt(%0)" ::"n"((kAhead - 1) * (kFL + kNL)) : "memory");
     lds_barrier();
-    int32_t unit = 0;  // of the step's F
+    int32_t slot = 0;
     for (int32_t n = 1;; ++n) {
-        next = tiles.get(a, n);
-        by_rows(t.rows, [&](auto nt) {
+        next = tiles.get<KIND>(a, n);
+        by_rows<KIND>(t.rows, [&](auto nt) {
             constexpr int NT = decltype(nt)::value, KF = Shape<NT>::kF, KN = Shape<NT>::kN;
             const int wf = Shape<NT>::wf(), wn = Shape<NT>::wn();
             // The compiler takes what comes out of the previous tile's branches for
             // different from lane to lane.
-            unit = uniform(unit);
+            slot = uniform(slot);
             fo.settle();
             no.settle();
             f32x4 acc[KF][KN] = {};
@@ -368,21 +398,21 @@ __device__ __forceinline__ void run_tiles(const ExpertArgs& a, int32_t ftiles, i
                 else
                     fa[half][r - KN] = FOp::fragment_at(f, r - KN, wf, half);
             };
-            // The step's first half; behind the previous tile's last barrier it has landed.
+            // The first step's first half; behind the previous tile's last barrier it has landed.
 #pragma unroll
-            for (int r = 0; r < kReads; ++r) read(0, lane_f[0] + unit * kUnit, lane_n[0] + ring(unit + 1) * kUnit, r);
+            for (int r = 0; r < kReads; ++r) read(0, lane_f[0] + f_at(slot), lane_n[0] + n_at(slot), r);
             // Each half of a step multiplies the fragments that the half before read, and
             // reads the next one's: first the second half's, then, behind the barrier, the
-            // next step's first.  By that barrier every wave has read all of this step,
-            // whose units are filled from then on.  Loads and reads go one by one between
-            // the matrix instructions, each of which leaves time to issue three others.
-            constexpr int kProducts = KF * KN, kGap = kProducts / kLoads;
+            // next step's first.  By that barrier every wave has read all of this step.
+            // Loads and reads go one by one between the matrix instructions, each of which
+            // leaves time to issue three others.
+            constexpr int kProducts = KF * KN;
             constexpr int kReadGap = (kProducts - 1) / kReads < 3 ? (kProducts - 1) / kReads : 3;
-            static_assert(kReadGap >= 1 && kGap >= 1, "");
-            auto half_step = [&](auto half_, int32_t from, auto& op, int32_t into) {
-                constexpr int half = decltype(half_)::value;
-                const uint16_t *const f_from = lane_f[half ^ 1] + from * kUnit, *const n_from = lane_n[half ^ 1] + ring(from + 1) * kUnit;
-                const uint32_t at = to(into);
+            static_assert(kReadGap >= 1, "");
+            auto half_step = [&](auto half_, int32_t from, auto& op, uint32_t to, auto loads) {
+                constexpr int half = decltype(half_)::value, kLoads = decltype(loads)::value, kGap = kProducts / kLoads;
+                static_assert(kGap >= 1, "");
+                const uint16_t *const f_from = lane_f[half ^ 1] + f_at(from), *const n_from = lane_n[half ^ 1] + n_at(from);
                 each([&](auto k_) {
                     constexpr int k = decltype(k_)::value, f = k / KN, n = k % KN, j = k / kGap;
                     __builtin_amdgcn_sched_barrier(0);
@@ -390,9 +420,9 @@ __device__ __forceinline__ void run_tiles(const ExpertArgs& a, int32_t ftiles, i
                     __builtin_amdgcn_sched_barrier(0);
                     if constexpr (k % kReadGap == 0 && k / kReadGap < kReads) read(half ^ 1, f_from, n_from, k / kReadGap);
                     if constexpr (j < kLoads && kGap == 1) {
-                        aim_and_load16<j * 1024>(at, op.source(j), op.voff[j]);
+                        aim_and_load16<j * 1024>(to, op.source(j), op.voff[j]);
                     } else if constexpr (j < kLoads && k % kGap == 0) {
-                        aim16<j * 1024>(at);
+                        aim16<j * 1024>(to);
                     } else if constexpr (j < kLoads && k % kGap == 1) {
                         load16(op.source(j), op.voff[j]);
                     }
@@ -400,25 +430,25 @@ __device__ __forceinline__ void run_tiles(const ExpertArgs& a, int32_t ftiles, i
                 __builtin_amdgcn_sched_barrier(0);
                 op.advance();
             };
-            // A step loads the one two behind it: the steps whose loads L neither begins
-            // nor ends with; the one that loads the last; two that load the next tile's.
+            // The steps whose loads L neither begins nor ends with; the one that loads the
+            // last; those that load the next tile's first.
 #pragma nounroll
-            for (int part = 0; part < 4; ++part) {
+            for (int part = 0; part < 2 + kAhead; ++part) {
                 if (part == 2) {
                     start_f(fo, next);
                     start_n(no, next);
                 }
-                const int32_t ahead = part == 0 ? 2 : part == 1 ? steps - 1 : part - 2;
+                const int32_t ahead = part == 0 ? kAhead : part == 1 ? steps - 1 : part - 2;
                 fo.ready(ahead, ragged);
                 no.ready(ahead, ragged);
-                for (int32_t s = part == 0 ? steps - 3 : 1; s > 0; --s) {
-                    const int32_t after = ring(unit + 2), free = ring(unit + 4);
-                    half_step(std::integral_constant<int, 0>{}, unit, fo, free);  // F of the step after the next
-                    // the next step has landed, in every wave, but for that F
-                    asm volatile("s_waitcnt vmcnt(%0)" ::"n"(kLoads) : "memory");
+                for (int32_t s = part == 0 ? steps - kAhead - 1 : 1; s > 0; --s) {
+                    const int32_t after = ring(slot + kStride), free = ring(slot + (kUnits ? 4 : kAhead));
+                    half_step(std::integral_constant<int, 0>{}, slot, fo, f_to(free), std::integral_constant<int, kFL>{});
+                    // the next step has landed, in every wave, when only later ones are outstanding
+                    asm volatile("s_waitcnt vmcnt(%0)" ::"n"((kAhead - 2) * (kFL + kNL) + kFL) : "memory");
                     lds_barrier();
-                    half_step(std::integral_constant<int, 1>{}, after, no, unit);  // its N, where this step's F was
-                    unit = after;
+                    half_step(std::integral_constant<int, 1>{}, after, no, n_to(free), std::integral_constant<int, kNL>{});
+                    slot = after;
                 }
             }
             end(nt, t, acc);
@@ -426,8 +456,19 @@ __device__ __forceinline__ void run_tiles(const ExpertArgs& a, int32_t ftiles, i
         t = next;
         if (t.expert < 0) break;
     }
-    // No load may land in LDS that belongs to another workgroup by then.
+    // No load may land in LDS that belongs to the next kind, or another workgroup, by then.
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+}
+
+// All tiles of this workgroup.
+template <typename FOp, typename StartF, typename StartN, typename Begin, typename End>
+__device__ __forceinline__ void run_tiles(const ExpertArgs& a, int32_t ftiles, int32_t len, uint16_t* lds, FOp& fo,
+                                          StartF start_f, StartN start_n, Begin begin, End end) {
+    LoopTiles tiles;
+    tiles.init(a, ftiles);
+    run_kind<0>(a, tiles, len, lds, fo, start_f, start_n, begin, end);
+    run_kind<1>(a, tiles, len, lds, fo, start_f, start_n, begin, end);
+    run_kind<2>(a, tiles, len, lds, fo, start_f, start_n, begin, end);
 }
 
 }  // namespace epx

@@ -32,7 +32,7 @@ __global__ __launch_bounds__(kLoopThreads) __attribute__((amdgpu_waves_per_eu(1,
         else
             op.start(we + f0, f0, F - f0, F, on ? L : 0);
     };
-    auto start_n = [&](LoopRows<kTileN>& op, const LoopTile& t) {
+    auto start_n = [&](auto& op, const LoopTile& t) {
         op.start((P == kForward ? a.e.x : a.e.gy) + t.first * L, t.expert >= 0 ? t.rows : 0);
     };
     auto begin = [&](auto nt, const LoopTile& t, auto& acc) {
