@@ -38,13 +38,25 @@ __device__ __forceinline__ uint32_t split_bf16(float v) {  // rounded value low,
     return hi | f32_to_bf16(rest) << 16;
 }
 
+// Whether one of the values is an infinity or NaN: all exponent bits set.
+__device__ __forceinline__ bool not_finite(const bf16x8 v) {
+    const v4u w = __builtin_bit_cast(v4u, v);
+    uint32_t carry = 0;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) carry |= (w[j] & 0x7F807F80u) + 0x00800080u;
+    return (carry & 0x80008000u) != 0;
+}
+
 // acc[f][n] += the adapters' part of a wave's results: 16 features a fragment f
 // by 16 rows a fragment n, summed over u rounded to bf16 and then over what the
-// rounding left (2 rank values).  weights(f, ad, c): this lane's 8 values [8 c, 8 c
-// + 8) of the rank of its feature of fragment f.  Every adapter that one of the rows
-// has is multiplied with all of them, and added to its own rows alone: nothing
-// that an adapter or another row holds, infinities and NaN included, reaches a row
-// that does not use it.
+// rounding left (2 rank values), 32 of them a step.  weights(f, ad, c): this lane's 8
+// values [8 c, 8 c + 8) of the rank of its feature of fragment f.  Every adapter that
+// one of the rows has is multiplied with all of them, with u zero in the rows of
+// others.  Steps whose weights hold an infinity or NaN come afterwards, and are added
+// to the adapter's own rows alone: nothing that an adapter or another row holds
+// reaches a row that does not use it.  (Selecting in every step moves all results
+// from accumulation to vector registers and back: 32 experts of 4096 x 7168, 4096
+// tokens of 8, rank 32, 2010 us.)
 template <int KF, int KN, typename Weights>
 __device__ __forceinline__ void add_adapters(const BlockArgs& a, int64_t first, int32_t rows, int32_t wn, Weights weights,
                                              f32x4 (&acc)[KF][KN]) {
@@ -52,28 +64,63 @@ __device__ __forceinline__ void add_adapters(const BlockArgs& a, int64_t first, 
     int32_t ad[KN];
 #pragma unroll
     for (int n = 0; n < KN; ++n) ad[n] = wn + n * 16 + i < rows ? row_adapter(a, first + wn + n * 16 + i) : -1;
-    const int32_t chunks = a.l.rank / 4;  // of 8 halves: the rounded values', then the rests'
+    const int32_t chunks = uniform(a.l.rank / 4);  // of 8 halves: the rounded values', then the rests'
     const uint16_t* const u = reinterpret_cast<const uint16_t*>(a.u) + (first + wn + i) * 2 * a.l.rank;
-    // Four fragments of features at a time: the selections need their results in
+    auto load_u = [&](bf16x8 (&v)[KN], int32_t cur, int32_t c) {
+#pragma unroll
+        for (int n = 0; n < KN; ++n) {
+            v[n] = bf16x8{};
+            if (c < chunks && ad[n] == cur) v[n] = *reinterpret_cast<const bf16x8*>(u + n * 32 * a.l.rank + c * 8);
+        }
+    };
+    auto load_w = [&](int f, int32_t cur, int32_t c) {
+        bf16x8 w = {};
+        if (c < chunks) w = weights(f, cur, c < chunks / 2 ? c : c - chunks / 2);
+        return w;
+    };
+    int32_t any_bad = 0;
+#pragma unroll
+    for (int f = 0; f < KF; ++f)
+#pragma unroll
+        for (int n = 0; n < KN; ++n) in_agprs(acc[f][n]);
+    for (int32_t cur = next_adapter(ad, -1); cur != kNoAdapter; cur = next_adapter(ad, cur)) {
+        for (int32_t c0 = 0; c0 < chunks; c0 += 4) {
+            bf16x8 wv[KF], uv[KN];
+#pragma unroll
+            for (int f = 0; f < KF; ++f) wv[f] = load_w(f, cur, c0 + q);
+            load_u(uv, cur, c0 + q);
+            bool bad = false;
+#pragma unroll
+            for (int f = 0; f < KF; ++f) bad |= not_finite(wv[f]);
+            if (__builtin_amdgcn_ballot_w64(bad) != 0) {
+                any_bad = 1;
+                continue;
+            }
+#pragma unroll
+            for (int f = 0; f < KF; ++f)
+#pragma unroll
+                for (int n = 0; n < KN; ++n) {
+                    acc[f][n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wv[f], uv[n], acc[f][n], 0, 0, 0);
+                    in_agprs(acc[f][n]);
+                }
+        }
+    }
+    if (uniform(any_bad) == 0) return;
+    // Few fragments of features at a time: the selections need their results in
     // vector registers, and all 256 at once would not fit beside the operands.
-    constexpr int kBlock = KF < 4 ? KF : 4;
+    constexpr int kBlock = KF < 2 ? KF : 2;
 #pragma unroll
     for (int f0 = 0; f0 < KF; f0 += kBlock) {
         for (int32_t cur = next_adapter(ad, -1); cur != kNoAdapter; cur = next_adapter(ad, cur)) {
             for (int32_t c0 = 0; c0 < chunks; c0 += 4) {
-                const int32_t c = c0 + q;
-                const bool on = c < chunks;
+                bool bad = false;
+#pragma unroll
+                for (int f = 0; f < KF; ++f) bad |= not_finite(load_w(f, cur, c0 + q));
+                if (__builtin_amdgcn_ballot_w64(bad) == 0) continue;
                 bf16x8 uv[KN], wv[kBlock];
+                load_u(uv, cur, c0 + q);
 #pragma unroll
-                for (int f = 0; f < kBlock; ++f) {
-                    wv[f] = bf16x8{};
-                    if (on) wv[f] = weights(f0 + f, cur, c < chunks / 2 ? c : c - chunks / 2);
-                }
-#pragma unroll
-                for (int n = 0; n < KN; ++n) {
-                    uv[n] = bf16x8{};
-                    if (on && ad[n] == cur) uv[n] = *reinterpret_cast<const bf16x8*>(u + n * 32 * a.l.rank + c * 8);
-                }
+                for (int f = 0; f < kBlock; ++f) wv[f] = load_w(f0 + f, cur, c0 + q);
 #pragma unroll
                 for (int f = 0; f < kBlock; ++f)
 #pragma unroll
