@@ -50,33 +50,41 @@ __global__ __launch_bounds__(kLoopThreads) __attribute__((amdgpu_waves_per_eu(1,
         const int32_t c0 = t.ft * (kTileF / 2) + S::wf() / 2;  // the wave's first column of act
         // acc[2 p][n][j], acc[2 p + 1][n][j]: g and u of column c0 + 16 p + 4 q + j, row wn + 16 n + i
         uint16_t* const act = static_cast<uint16_t*>(a.e.out);
+        float w[KN];
+        int32_t slot[KN];
+        auto row_of = [&](int n) { return t.first + min(wn + n * 16 + i, t.rows - 1); };
+        row_weights<KN>(a, row_of, w, slot);
+        v2u ga[BACKWARD ? KN : 1][KF / 2];
+        if constexpr (BACKWARD) {
+#pragma unroll
+            for (int n = 0; n < KN; ++n)
+#pragma unroll
+                for (int p = 0; p < KF / 2; ++p)
+                    ga[n][p] = *reinterpret_cast<const v2u*>(a.grad_act + row_of(n) * I + min(c0 + p * 16 + q * 4, I - 4));
+        }
 #pragma unroll
         for (int n = 0; n < KN; ++n) {
-            const int32_t row = wn + n * 16 + i;
-            const bool on = row < t.rows;
-            const int64_t r = t.first + row;
-            int64_t slot = -1;
-            const float w = on ? row_weight(a, r, slot) : 0.0f;
+            const int64_t r = row_of(n);
+            const bool on = wn + n * 16 + i < t.rows;
             float sum = 0.0f;
 #pragma unroll
             for (int p = 0; p < KF / 2; ++p) {
                 const int32_t c = c0 + p * 16 + q * 4;
-                if (!on || c >= I) continue;
+                const bool in = on && c < I;
                 const f32x4 g = acc[2 * p][n], u = acc[2 * p + 1][n];
                 float y[4], gg[4], gu[4];
-                v2u ga = {};
-                if constexpr (BACKWARD) ga = *reinterpret_cast<const v2u*>(a.grad_act + r * I + c);
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     const float s = fast_sigmoid(g[j]), silu = g[j] * s;
-                    y[j] = w * (silu * u[j]);
+                    y[j] = w[n] * (silu * u[j]);
                     if constexpr (BACKWARD) {
-                        const float d = j % 2 ? bf16_hi(ga[j / 2]) : bf16_lo(ga[j / 2]), wd = w * d;
-                        sum += d * (silu * u[j]);
+                        const float d = j % 2 ? bf16_hi(ga[n][p][j / 2]) : bf16_lo(ga[n][p][j / 2]), wd = w[n] * d;
+                        sum += in ? d * (silu * u[j]) : 0.0f;
                         gg[j] = wd * u[j] * (s * (1.0f + g[j] * (1.0f - s)));
                         gu[j] = wd * silu;
                     }
                 }
+                if (!in) continue;
                 if (act != nullptr)
                     *reinterpret_cast<v2u*>(act + r * I + c) = v2u{pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3])};
                 if constexpr (BACKWARD) {
@@ -91,7 +99,7 @@ __global__ __launch_bounds__(kLoopThreads) __attribute__((amdgpu_waves_per_eu(1,
                 sum += __shfl_xor(sum, 32, kWave);
                 // the wave's columns are KF / 4 parts: the sum in the first, zeros in the others
                 const int32_t parts = (I + kGatedPart - 1) / kGatedPart, part = c0 / kGatedPart + q;
-                if (q < KF / 4 && slot >= 0 && part < parts) a.parts[slot * parts + part] = q == 0 ? sum : 0.0f;
+                if (q < KF / 4 && on && slot[n] >= 0 && part < parts) a.parts[(int64_t)slot[n] * parts + part] = q == 0 ? sum : 0.0f;
             }
         }
     });

@@ -43,6 +43,7 @@ constexpr int kKindRows[kKinds] = {kTileN, 128, 32};  // at most
 struct LoopTiles {
     int32_t before[kKinds], upto[kKinds];  // of this lane's groups
     int32_t total[kKinds], ftiles, per;
+    int32_t rows_, first_;  // of this lane's only group, where it has one
 
     // Rows of a group that become a tile of their own, behind its full ones.
     static __device__ __forceinline__ int32_t left_over(int32_t rows) {
@@ -59,10 +60,13 @@ struct LoopTiles {
         ftiles = f;
         per = (a.NG + kWave - 1) / kWave;
         int32_t mine[kKinds] = {};
+        rows_ = first_ = 0;
         for (int g = lane * per; g < min((lane + 1) * per, a.NG); ++g) {
-            const int32_t rows = group_rows(a, g).rows;
+            const GroupRows r = group_rows(a, g);
+            rows_ = r.rows;
+            first_ = (int32_t)r.first;
 #pragma unroll
-            for (int k = 0; k < kKinds; ++k) mine[k] += tiles_of(rows, k);
+            for (int k = 0; k < kKinds; ++k) mine[k] += tiles_of(r.rows, k);
         }
 #pragma unroll
         for (int k = 0; k < kKinds; ++k) {
@@ -97,7 +101,7 @@ struct LoopTiles {
             const int lane = threadIdx.x & (kWave - 1);
             int32_t b = before[KIND];
             for (int g = lane * per; g < min((lane + 1) * per, a.NG); ++g) {
-                const GroupRows r = group_rows(a, g);
+                const GroupRows r = per == 1 ? GroupRows{first_, rows_} : group_rows(a, g);
                 const int32_t c = tiles_of(r.rows, KIND);
                 if (want < b + c) {
                     const int32_t rest = left_over(r.rows), cut = r.rows - rest;  // cut: in tiles of one height

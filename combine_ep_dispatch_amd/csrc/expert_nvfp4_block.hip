@@ -40,6 +40,9 @@ __global__ __launch_bounds__(WAVES * kWave) void k_nvfp4_block(BlockArgs a, int3
                 return *reinterpret_cast<const bf16x8*>(a.l.b + (pair * a.e.on + up(g, i) * features + fe) * a.l.rank + c * 8);
             }, acc);
         uint16_t* const out = static_cast<uint16_t*>(a.e.out);
+        float w[KN];
+        int32_t slot[KN];
+        if constexpr (GATED) row_weights<KN>(a, [&](int n) { return t.first + min(n * 16 + i, t.rows - 1); }, w, slot);
 #pragma unroll
         for (int n = 0; n < KN; ++n) {
             const int32_t r = n * 16 + i;
@@ -54,11 +57,9 @@ __global__ __launch_bounds__(WAVES * kWave) void k_nvfp4_block(BlockArgs a, int3
                 const int32_t fe = feature(0, q * 4);
                 if (fe >= features) continue;
                 if constexpr (KF == 2) upper = acc[KF - 1][n];
-                int64_t slot;
-                const float w = row_weight(a, t.first + r, slot);
                 float y[4];
 #pragma unroll
-                for (int j = 0; j < 4; ++j) y[j] = w * (acc[0][n][j] * fast_sigmoid(acc[0][n][j]) * upper[j]);
+                for (int j = 0; j < 4; ++j) y[j] = w[n] * (acc[0][n][j] * fast_sigmoid(acc[0][n][j]) * upper[j]);
                 *reinterpret_cast<v2u*>(out + (t.first + r) * features + fe) = v2u{pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3])};
             } else {
 #pragma unroll
