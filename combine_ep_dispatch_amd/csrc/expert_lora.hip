@@ -85,77 +85,112 @@ hipError_t product(const BlockArgs& a, hipStream_t stream) {
     return hipGetLastError();
 }
 
-constexpr int kDownWaves = 8;
-constexpr int kDownRows = 16;
+constexpr int kDownWaves = 4;
+constexpr int kDownThreads = kDownWaves * kWave;
 
-// u of 16 rows: each of 8 waves sums its share of L (64 values in turn, 16 a
-// quarter of the wave), and the workgroup adds the eight up in order.  The
-// workgroups of a tile (blockIdx.y) share its adapters: with few tiles, as in a
-// decode step, each adapter's weights are read by a workgroup of their own.
-// BWD: gu, from gy and B, whose values lie along the rank.
-template <bool BWD, int KP>
-__global__ __launch_bounds__(kDownWaves * kWave) void k_lora_down(BlockArgs a, uint16_t* u) {
-    constexpr int P = KP * 16;
-    __shared__ float part[kDownWaves][kDownRows][P + 1];
-    __shared__ int32_t scan[kDownWaves + 3];
+// The adapter's weights as a wave's operand: A, rank rows along L, or for gu B,
+// whose rows of rank values are L.  Past the rank: zeros.
+template <bool BWD, int P>
+struct AdapterOperand : std::conditional<BWD, ColsOperand<P, 1>, RowsOperand<P, 1>>::type {
+    using Base = typename std::conditional<BWD, ColsOperand<P, 1>, RowsOperand<P, 1>>::type;
+    __device__ __forceinline__ void start(const uint16_t* p, int32_t rank, int32_t l) {
+        if constexpr (BWD)
+            Base::init(p, rank, rank, l, 0);
+        else
+            Base::init(p, rank, l, l);
+    }
+};
+
+// u of NT rows, P >= rank.  Each of 4 waves by itself sums every fourth step of 64
+// values, kept under way kRing - 1 steps ahead in its own part of LDS; the workgroup
+// adds the four up in order.  The workgroups of a tile (blockIdx.y) share its
+// adapters: with few tiles, as in a decode step, each adapter's weights are read by
+// a workgroup of their own.  BWD: gu, from gy and B.
+template <bool BWD, int P, int NT>
+__global__ __launch_bounds__(kDownThreads) void k_lora_down(BlockArgs a, uint16_t* u) {
+    using Op = AdapterOperand<BWD, P>;
+    constexpr int kStep = (NT + P) * kStepL;  // elements of a wave's step
+    constexpr int kRing = NT + P <= 32 ? 4 : NT + P <= 96 ? 3 : 2;
+    constexpr int kFL = P / 8, kNL = NT / 8, KP = P / 16, KN = NT / 16;
+    constexpr int kPart = kDownWaves * NT * (P + 1) * 4, kLds = kDownWaves * kRing * kStep * 2;
+    static_assert(kPart <= kLds && kLds <= 160 * 1024 && (kRing - 1) * (kFL + kNL) < 64, "");
+    __shared__ __align__(1024) uint8_t lds[kLds];
+    __shared__ int32_t scan[kDownWaves + 3], ads[NT];
     int32_t none;
-    const RowTile t = find_row_tile<kDownWaves * kWave, kDownRows>(
+    const RowTile t = find_row_tile<kDownThreads, NT>(
         a.e, scan, [&](int32_t rt, int32_t& f) { return xcd_tile(rt, 1, f); }, none);
     if (t.expert < 0) return;
     const int lane = threadIdx.x & (kWave - 1), w = uniform((int32_t)(threadIdx.x / kWave)), i = lane % 16, q = lane / 16;
-    const int32_t L = BWD ? a.e.on : a.e.in, rank = a.l.rank;
-    const uint16_t* const x = (BWD ? a.e.gy : a.e.x) + (t.first + i) * L;
-    int32_t ad[1] = {i < t.rows ? row_adapter(a, t.first + i) : -1};
-    // what this thread writes: value p of row r
-    constexpr int kThreads = kDownWaves * kWave, kMine = (kDownRows * P + kThreads - 1) / kThreads;
-    auto out = [&](int m, int& r, int& p) {
-        const int at = m * kThreads + threadIdx.x;
-        r = at / P;
-        p = at % P;
-        return r < t.rows && p < rank;
-    };
+    const int32_t L = BWD ? a.e.on : a.e.in, rank = a.l.rank, steps = (L + kStepL - 1) / kStepL;
+    const uint16_t* const x = (BWD ? a.e.gy : a.e.x) + t.first * L;
+    if ((int32_t)threadIdx.x < NT) ads[threadIdx.x] = (int32_t)threadIdx.x < t.rows ? row_adapter(a, t.first + threadIdx.x) : -1;
+    __syncthreads();
+    int32_t ad[KN];
+#pragma unroll
+    for (int n = 0; n < KN; ++n) ad[n] = ads[n * 16 + i];
+    uint16_t* const mine = reinterpret_cast<uint16_t*>(lds) + w * kRing * kStep;
+    float* const part = reinterpret_cast<float*>(lds);
+    RowsOperand<NT, 1> no;
     int32_t at = 0;
-    for (int32_t cur = next_adapter(ad, -1);; cur = next_adapter(ad, cur), ++at) {
-        if (cur == kNoAdapter) break;
-        if (at % gridDim.y != blockIdx.y) continue;
+    for (int32_t cur = next_adapter(ad, -1); cur != kNoAdapter; cur = next_adapter(ad, cur), ++at) {
+        if (at % (int32_t)gridDim.y != (int32_t)blockIdx.y) continue;
         const int64_t pair = (int64_t)cur * (a.e.E + a.e.shared) + t.expert;
-        const uint16_t* const f = (BWD ? a.l.b : a.l.a) + pair * rank * L;
-        f32x4 acc[KP] = {};
-        for (int32_t l0 = w * 64; l0 < L; l0 += kDownWaves * 64) {
+        Op fo;
+        fo.start((BWD ? a.l.b : a.l.a) + pair * rank * L, rank, L);
+        no.init(x, t.rows, L, L);
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const int32_t l = l0 + q * 16 + h * 8;
-                bf16x8 xv = {}, fv[KP] = {};
-                if (l < L && ad[0] == cur) xv = *reinterpret_cast<const bf16x8*>(x + l);
+        for (int j = 0; j < kNL; ++j)  // rows of other adapters: zeros, and not read
+            no.voff[j] = ads[j * 8 + lane / 8] == cur ? no.voff[j] : kOutside;
+        auto load = [&](int32_t s, int slot) {
+            const int32_t l0 = uniform((s * kDownWaves + w) * kStepL);
 #pragma unroll
-                for (int k = 0; k < KP; ++k) {
-                    const int32_t p = k * 16 + i;
-                    if (l >= L || p >= rank) continue;
-                    if constexpr (BWD) {
+            for (int j = 0; j < kFL; ++j) fo.load(mine + slot * kStep, l0, j);
 #pragma unroll
-                        for (int j = 0; j < 8; ++j) fv[k][j] = reinterpret_cast<const __bf16*>(f)[(l + j) * (int64_t)rank + p];
-                    } else {
-                        fv[k] = *reinterpret_cast<const bf16x8*>(f + (int64_t)p * L + l);
-                    }
-                }
+            for (int j = 0; j < kNL; ++j) no.load(mine + slot * kStep + P * kStepL, l0, j);
+        };
+        f32x4 acc[KP][KN] = {};
 #pragma unroll
-                for (int k = 0; k < KP; ++k) acc[k] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fv[k], xv, acc[k], 0, 0, 0);
+        for (int s = 0; s < kRing - 1; ++s) load(s, s);
+        const int32_t turns = (steps - w + kDownWaves - 1) / kDownWaves;
+        int32_t slot = 0;
+        for (int32_t s = 0; s < turns; ++s) {
+            load(s + kRing - 1, slot == 0 ? kRing - 1 : slot - 1);
+            // this step has landed when only the later ones are outstanding
+            asm volatile("s_waitcnt vmcnt(%0)" ::"n"((kRing - 1) * (kFL + kNL)) : "memory");
+            const uint16_t *const lf = mine + slot * kStep, *const ln = lf + P * kStepL;
+#pragma unroll
+            for (int kk = 0; kk < 2; ++kk) {
+                bf16x8 fv[KP], nv[KN];
+#pragma unroll
+                for (int k = 0; k < KP; ++k) fv[k] = Op::fragment(lf, k * 16, kk);
+#pragma unroll
+                for (int n = 0; n < KN; ++n) nv[n] = RowsOperand<NT, 1>::fragment(ln, n * 16, kk);
+#pragma unroll
+                for (int k = 0; k < KP; ++k)
+#pragma unroll
+                    for (int n = 0; n < KN; ++n) acc[k][n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fv[k], nv[n], acc[k][n], 0, 0, 0);
             }
+            // what was read is in registers before the next step's loads overwrite it
+            asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+            slot = slot == kRing - 1 ? 0 : slot + 1;
         }
+        // no load of any wave may land among the parts
+        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+        __syncthreads();
 #pragma unroll
         for (int k = 0; k < KP; ++k)
 #pragma unroll
-            for (int j = 0; j < 4; ++j) part[w][i][k * 16 + q * 4 + j] = acc[k][j];
+            for (int n = 0; n < KN; ++n)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) part[(w * NT + n * 16 + i) * (P + 1) + k * 16 + q * 4 + j] = acc[k][n][j];
         __syncthreads();
         const float s = a.l.scale != nullptr ? a.l.scale[cur] : 1.0f;
-#pragma unroll
-        for (int m = 0; m < kMine; ++m) {
-            int r, p;
-            if (!out(m, r, p)) continue;
-            if (row_adapter(a, t.first + r) != cur) continue;
+        for (int at = threadIdx.x; at < NT * P; at += kDownThreads) {
+            const int r = at / P, p = at % P;
+            if (p >= rank || ads[r] != cur) continue;
             float v = 0.0f;
 #pragma unroll
-            for (int k = 0; k < kDownWaves; ++k) v += part[k][r][p];
+            for (int k = 0; k < kDownWaves; ++k) v += part[(k * NT + r) * (P + 1) + p];
             const uint32_t two = split_bf16(s * v);
             uint16_t* const to = u + (t.first + r) * 2 * rank + p;
             to[0] = (uint16_t)two;
@@ -165,32 +200,34 @@ __global__ __launch_bounds__(kDownWaves * kWave) void k_lora_down(BlockArgs a, u
     }
     if (blockIdx.y != 0) return;
     // rows without an adapter: zeros
-#pragma unroll
-    for (int m = 0; m < kMine; ++m) {
-        int r, p;
-        if (!out(m, r, p) || row_adapter(a, t.first + r) >= 0) continue;
+    for (int at = threadIdx.x; at < NT * P; at += kDownThreads) {
+        const int r = at / P, p = at % P;
+        if (p >= rank || r >= t.rows || ads[r] >= 0) continue;
         uint16_t* const to = u + (t.first + r) * 2 * rank + p;
         to[0] = to[rank] = 0;
     }
 }
 
-template <bool BWD, int KP>
+// Tiles of 64 rows, which read an adapter's weights a quarter as often, where they
+// are enough to fill the CUs; of 16, shared by their adapters' workgroups, for less.
+template <bool BWD, int P, int NT>
 hipError_t down(const BlockArgs& a, float* u, hipStream_t stream) {
-    const int64_t tiles = max_row_tiles(a.e, kDownRows), blocks = (tiles + 7) / 8 * 8;
+    const int64_t tiles = max_row_tiles(a.e, NT), blocks = (tiles + 7) / 8 * 8;
     if (blocks == 0) return hipSuccess;
-    const int share = tiles <= 512 ? (a.l.n < kDownRows ? a.l.n : kDownRows) : 1;
-    if (const hipError_t e = check_grid(blocks, kDownWaves * kWave)) return e;
-    hipLaunchKernelGGL((k_lora_down<BWD, KP>), dim3((unsigned)blocks, (unsigned)share), dim3(kDownWaves * kWave), 0, stream, a,
+    const int share = tiles <= 2 * kCus ? (a.l.n < NT ? a.l.n : NT) : 1;
+    if (const hipError_t e = check_grid(blocks, kDownThreads)) return e;
+    hipLaunchKernelGGL((k_lora_down<BWD, P, NT>), dim3((unsigned)blocks, (unsigned)share), dim3(kDownThreads), 0, stream, a,
                        reinterpret_cast<uint16_t*>(u));
     return hipGetLastError();
 }
 
 template <bool BWD>
-hipError_t down_by_rank(const BlockArgs& a, float* u, hipStream_t stream) {
-    if (a.l.rank <= 16) return down<BWD, 1>(a, u, stream);
-    if (a.l.rank <= 32) return down<BWD, 2>(a, u, stream);
-    if (a.l.rank <= 64) return down<BWD, 4>(a, u, stream);
-    return down<BWD, 8>(a, u, stream);
+hipError_t down_by_size(const BlockArgs& a, float* u, hipStream_t stream) {
+    const bool many = a.e.slots >= 64 * kCus;
+    if (a.l.rank <= 16) return many ? down<BWD, 16, 64>(a, u, stream) : down<BWD, 16, 16>(a, u, stream);
+    if (a.l.rank <= 32) return many ? down<BWD, 32, 64>(a, u, stream) : down<BWD, 32, 16>(a, u, stream);
+    if (a.l.rank <= 64) return many ? down<BWD, 64, 64>(a, u, stream) : down<BWD, 64, 16>(a, u, stream);
+    return down<BWD, 128, 16>(a, u, stream);
 }
 
 constexpr int kGradThreads = 256, kGradRows = 64, kGradCols = 256;  // rows a step, columns of a tile
@@ -322,8 +359,8 @@ hipError_t bwd_w_by_rank(const BlockArgs& a, const float* v, void* out, hipStrea
 
 hipError_t launch_gemm_lora(const BlockArgs& a, hipStream_t stream) { return product<kForward>(a, stream); }
 hipError_t launch_gemm_bwd_x_lora(const BlockArgs& a, hipStream_t stream) { return product<kInputGrad>(a, stream); }
-hipError_t launch_lora_down(const BlockArgs& a, float* u, hipStream_t stream) { return down_by_rank<false>(a, u, stream); }
-hipError_t launch_lora_bwd_u(const BlockArgs& a, float* u, hipStream_t stream) { return down_by_rank<true>(a, u, stream); }
+hipError_t launch_lora_down(const BlockArgs& a, float* u, hipStream_t stream) { return down_by_size<false>(a, u, stream); }
+hipError_t launch_lora_bwd_u(const BlockArgs& a, float* u, hipStream_t stream) { return down_by_size<true>(a, u, stream); }
 hipError_t launch_lora_bwd_w(const BlockArgs& a, const float* grad_u, void* grad_a, void* grad_b, hipStream_t stream) {
     if (const hipError_t e = bwd_w_by_rank<false>(a, grad_u, grad_a, stream)) return e;
     return bwd_w_by_rank<true>(a, a.u, grad_b, stream);

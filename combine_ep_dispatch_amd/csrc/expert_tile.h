@@ -11,6 +11,12 @@ typedef short s16x4 __attribute__((ext_vector_type(4)));
 
 constexpr int kStepL = 64;  // values of L a step: whole 128-byte lines of rows
 
+// The wave among the WAVES that share an operand; alone, each has its own.
+template <int WAVES>
+__device__ __forceinline__ int32_t wave_of() {
+    return WAVES == 1 ? 0 : uniform((int32_t)(threadIdx.x / kWave));
+}
+
 // One operand's step of BM x kStepL values, copied to LDS by the loads
 // themselves (16 bytes a lane, 1 KiB a wave and load, to consecutive LDS
 // addresses; the lanes pick their global addresses so that the LDS tile comes
@@ -27,7 +33,7 @@ struct RowsOperand {
 
     // rows: valid rows from base on; pitch: theirs; l: values of L
     __device__ __forceinline__ void init(const uint16_t* p, int32_t rows, int32_t pitch, int32_t l) {
-        const int lane = threadIdx.x & (kWave - 1), w = uniform((int32_t)(threadIdx.x / kWave));
+        const int lane = threadIdx.x & (kWave - 1), w = wave_of<WAVES>();
         base = p;
         ld = pitch;
         len = l;
@@ -39,7 +45,7 @@ struct RowsOperand {
             voff[j] = ((w * kLoads + j) * 8 + lane / 8) * ld * 2 + chunk[j % 2] * 16;
     }
     __device__ __forceinline__ void load(uint16_t* lds, int32_t l0, int j) const {
-        const int w = uniform((int32_t)(threadIdx.x / kWave));
+        const int w = wave_of<WAVES>();
         load_to_lds<16>(base, records, lds + (w * kLoads + j) * 512,
                         l0 + chunk[j % 2] * 8 < len ? voff[j] + l0 * 2 : kOutside);
     }
@@ -64,7 +70,7 @@ struct ColsOperand {
 
     // p: column m0 of the operand; cols: valid columns from p on; pitch: of rows; l: rows
     __device__ __forceinline__ void init(const uint16_t* p, int32_t cols, int32_t pitch, int32_t l, int32_t m0) {
-        const int lane = threadIdx.x & (kWave - 1), w = uniform((int32_t)(threadIdx.x / kWave));
+        const int lane = threadIdx.x & (kWave - 1), w = wave_of<WAVES>();
         base = p;
         ld = pitch;
         len = l;
@@ -83,7 +89,7 @@ struct ColsOperand {
         return uniform(rows > 0 ? rows * ld * 2 - cut : 0);
     }
     __device__ __forceinline__ void load(uint16_t* lds, int32_t l0, int j) const {
-        const int w = uniform((int32_t)(threadIdx.x / kWave));
+        const int w = wave_of<WAVES>();
         load_to_lds<16>(base + (int64_t)l0 * ld, records(l0), lds + (w * kLoads + j) * 512, voff[j]);
     }
     static __device__ __forceinline__ bf16x8 fragment(const uint16_t* lds, int m0, int kk) {
