@@ -27,6 +27,12 @@ The expert layer around the two, on the same layout:
     act = d.swiglu(h, probs)                 # weights applied to the rows; differentiable in both
     y = d.combine(d.linear(act, w2), None)
 
+d.gated(recv, w1, probs) is d.swiglu(d.linear(recv, w1), probs) in one kernel that
+keeps neither h nor act's inputs: its backward pass makes h again.  linear and gated
+take Adapters (low-rank, a token's own each) beside the weights, differentiable in
+rows, w, adapters.a and adapters.b (scale gets no gradient); weights that need no
+gradient cost none.
+
 A step can be captured into a graph, backward pass included, on leaves that no
 eager autograd graph still holds (torch does not support capturing beside one).
 
@@ -41,9 +47,11 @@ from typing import Optional
 
 import torch
 
-from . import (EpConfig, Layout, RouteConfig, ep_combine, ep_combine_bwd, ep_combine_bwd_probs, ep_dispatch,
-               ep_dispatch_bwd, ep_dispatch_layout, ep_dispatch_with_layout, ep_expert_gemm, ep_expert_gemm_bwd_w,
-               ep_expert_gemm_bwd_x, ep_query, ep_route, ep_route_bwd, ep_swiglu, ep_swiglu_bwd, workspace_for)
+from . import (Adapters, EpConfig, Layout, RouteConfig, ep_combine, ep_combine_bwd, ep_combine_bwd_probs, ep_dispatch,
+               ep_dispatch_bwd, ep_dispatch_layout, ep_dispatch_with_layout, ep_expert_gated, ep_expert_gated_bwd,
+               ep_expert_gemm, ep_expert_gemm_bwd_w, ep_expert_gemm_bwd_x, ep_expert_gemm_bwd_x_lora,
+               ep_expert_gemm_lora, ep_lora_bwd_u, ep_lora_bwd_w, ep_lora_down, ep_query, ep_route, ep_route_bwd,
+               ep_swiglu, ep_swiglu_bwd, gated_workspace_for, workspace_for)
 
 __all__ = ["EpDispatcher"]
 
@@ -207,6 +215,90 @@ class _Swiglu(torch.autograd.Function):
         return gh, gp, None, None
 
 
+def _u(cfg, rank: int, device) -> torch.Tensor:
+    return torch.empty(cfg.recv_rows, rank, dtype=torch.float32, device=device)
+
+
+def _product_grads(ctx, gy, x, w, adapters, u, wanted):
+    """The gradients of x, w, a and b of a product (with adapters, or None) from its
+    results' gradient, those that are wanted."""
+    cfg, layout = ctx.cfg, ctx.layout
+    gx = gw = ga = gb = gu = None
+    if adapters is not None and (wanted[0] or wanted[2] or wanted[3]):
+        gu = _u(cfg, adapters.rank, gy.device)
+        ep_lora_bwd_u(cfg, layout, gy, adapters, gu)
+    if wanted[0]:
+        gx = torch.zeros_like(x)
+        if adapters is None:
+            ep_expert_gemm_bwd_x(cfg, layout, gy, w, gx)
+        else:
+            ep_expert_gemm_bwd_x_lora(cfg, layout, gy, w, gx, adapters, gu)
+    if wanted[1]:
+        gw = torch.empty_like(w)
+        ep_expert_gemm_bwd_w(cfg, layout, gy, x, gw)
+    if wanted[2] or wanted[3]:
+        ga, gb = torch.empty_like(adapters.a), torch.empty_like(adapters.b)
+        ep_lora_bwd_w(cfg, layout, x, gy, adapters, u, gu, ga, gb)
+    return gx, gw, ga, gb
+
+
+class _LinearLora(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, w, a, b, token_adapter, scale, cfg, layout):
+        adapters, u = Adapters(token_adapter, a, b, scale), _u(cfg, a.shape[2], x.device)
+        y = torch.zeros(cfg.recv_rows, w.shape[1], dtype=torch.bfloat16, device=x.device)
+        ep_lora_down(cfg, layout, x, adapters, u)
+        ep_expert_gemm_lora(cfg, layout, x, w, y, adapters, u)
+        ctx.cfg, ctx.layout, ctx.rest = cfg, layout, (token_adapter, scale)
+        ctx.save_for_backward(x, w, a, b, u)
+        return y
+
+    @staticmethod
+    @_first_only
+    def backward(ctx, grad_y):
+        x, w, a, b, u = ctx.saved_tensors
+        adapters = Adapters(ctx.rest[0], a, b, ctx.rest[1])
+        grads = _product_grads(ctx, _rows(grad_y.to(torch.bfloat16)), x, w, adapters, u, ctx.needs_input_grad)
+        return (*grads, None, None, None, None)
+
+
+class _Gated(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, w, a, b, probs, token_adapter, scale, cfg, layout):
+        adapters = u = None
+        if a is not None:
+            adapters, u = Adapters(token_adapter, a, b, scale), _u(cfg, a.shape[2], x.device)
+            ep_lora_down(cfg, layout, x, adapters, u)
+        act = torch.zeros(cfg.recv_rows, w.shape[1] // 2, dtype=torch.bfloat16, device=x.device)
+        ep_expert_gated(cfg, layout, x, w, probs, act, adapters, u)
+        ctx.cfg, ctx.layout, ctx.rest = cfg, layout, (token_adapter, scale)
+        ctx.save_for_backward(x, w, a, b, probs, u)
+        return act
+
+    @staticmethod
+    @_first_only
+    def backward(ctx, grad_act):
+        x, w, a, b, probs, u = ctx.saved_tensors
+        cfg, layout = ctx.cfg, ctx.layout
+        adapters = None if a is None else Adapters(ctx.rest[0], a, b, ctx.rest[1])
+        ga = _rows(grad_act.to(torch.bfloat16))
+        gh = torch.zeros(cfg.recv_rows, w.shape[1], dtype=torch.bfloat16, device=x.device)
+        gp = ws = None
+        if probs is not None and ctx.needs_input_grad[4]:
+            gp = torch.empty(cfg.num_tokens, cfg.top_k, dtype=torch.float32, device=x.device)
+            ws = gated_workspace_for(cfg, ga.shape[1], x.device)
+        ep_expert_gated_bwd(cfg, layout, x, w, probs, ga, gh, grad_probs=gp, workspace=ws, adapters=adapters, u=u)
+        return (*_product_grads(ctx, gh, x, w, adapters, u, ctx.needs_input_grad), gp, None, None, None, None)
+
+
+def _parts(adapters: Optional[Adapters]):
+    """a, b, token_adapter and scale of adapters as the calls take them."""
+    if adapters is None:
+        return None, None, None, None
+    return (_rows(adapters.a), _rows(adapters.b), adapters.token_adapter.to(torch.int32).contiguous(),
+            None if adapters.scale is None else adapters.scale.detach().float().contiguous())
+
+
 class EpDispatcher:
     """Dispatch / combine with autograd for one configuration on one device."""
 
@@ -249,10 +341,21 @@ class EpDispatcher:
         float32 [T, K], differentiable in the logits."""
         return _Gate.apply(_rows(logits), bias, token_mask, self.cfg, route)
 
-    def linear(self, rows: torch.Tensor, w: torch.Tensor) -> torch.Tensor:
+    def linear(self, rows: torch.Tensor, w: torch.Tensor, adapters: Optional[Adapters] = None) -> torch.Tensor:
         """[R, in] bf16 receive rows times their experts' weights bf16
-        [E (+1 shared), out, in] -> [R, out]; rows no slot owns are zero."""
-        return _Linear.apply(_rows(rows), _rows(w), self.cfg, self.layout)
+        [E (+1 shared), out, in] (and their tokens' adapters) -> [R, out]; rows no
+        slot owns are zero."""
+        if adapters is None:
+            return _Linear.apply(_rows(rows), _rows(w), self.cfg, self.layout)
+        a, b, of, scale = _parts(adapters)
+        return _LinearLora.apply(_rows(rows), _rows(w), a, b, of, scale, self.cfg, self.layout)
+
+    def gated(self, rows: torch.Tensor, w: torch.Tensor, probs: Optional[torch.Tensor],
+              adapters: Optional[Adapters] = None) -> torch.Tensor:
+        """swiglu(linear(rows, w, adapters), probs) in one kernel: rows [R, in], w bf16
+        [E (+1 shared), 2*inter, in] (gate rows, then up rows) -> [R, inter]."""
+        a, b, of, scale = _parts(adapters)
+        return _Gated.apply(_rows(rows), _rows(w), a, b, _weights(probs), of, scale, self.cfg, self.layout)
 
     def swiglu(self, h: torch.Tensor, probs: Optional[torch.Tensor]) -> torch.Tensor:
         """[R, 2*inter] bf16 (gate, then up) -> [R, inter], each row times its

@@ -492,3 +492,242 @@ def test_operands_that_end_with_their_memory(G, name, n_in):  # noqa: F811
     got = block_calls(G, d, *map(at_the_end, (x, ga, w)), list(map(at_the_end, q)), lora, rank, inter)
     for k, v in got.items():
         assert torch.equal(v, want[k]), k
+
+
+# ---------------------------------------------------------------------------
+# Together
+# ---------------------------------------------------------------------------
+def lora_leaves(n, experts, rank, n_in, n_out, T, seed):
+    gen = torch.Generator().manual_seed(seed)
+    of = torch.randint(-1, n, (T,), generator=gen, dtype=torch.int32).cuda()
+    return dict(a=normal(seed, n, experts, rank, n_in, std=n_in ** -0.5).requires_grad_(),
+                b=normal(seed + 1, n, experts, n_out, rank, std=0.5 * rank ** -0.5).requires_grad_(), of=of,
+                scale=(0.5 + torch.rand(n, generator=gen)).cuda())
+
+
+def dense_lora(x, w, l, refs, e):
+    """x @ (w[e] + scale b a)^T of every token's adapter, in 64 bits."""
+    out = x @ w[e].T
+    for k in range(refs["a"].shape[0]):
+        on = (l["of"].cpu() == k).double()[:, None]
+        out = out + on * l["scale"][k].double().cpu() * ((x @ refs["a"][k, e].T) @ refs["b"][k, e].T)
+    return out
+
+
+@pytest.mark.parametrize("shared", [0, 1])
+@pytest.mark.parametrize("rank", [0, 8])
+def test_layer_forward_and_backward(G, shared, rank):  # noqa: F811
+    """The layer with the gated block (and adapters beside both products) through
+    EpDispatcher against a dense form in 64 bits.  Forward the layer rounds to bf16
+    after three row operations, each at most 2^-8 of the value: results differ by at
+    most 3 * 2^-8 = 0.012 of their norm; gradients, up to six such roundings on the
+    way, by 6 * 2^-8 = 0.024."""
+    from combine_ep_dispatch_amd.autograd import EpDispatcher
+
+    T, H, E, K, inter = 65, 72, 8, 3, 40
+    x, logits, gy = normal(1, T, H).requires_grad_(), normal(2, T, E, dtype=torch.float32).requires_grad_(), normal(5, T, H)
+    w1 = normal(3, E + shared, 2 * inter, H, std=H ** -0.5).requires_grad_()
+    w2 = normal(4, E + shared, H, inter, std=inter ** -0.5).requires_grad_()
+    cfg = G.epx.EpConfig(num_tokens=T, hidden=H, num_experts=E, num_segments=2, top_k=K, align=16,
+                         shared_expert=shared, src_segment=1 if shared else 0)
+    leaves, l1, l2, ad1, ad2 = dict(x=x, logits=logits, w1=w1, w2=w2), None, None, None, None
+    if rank:
+        l1, l2 = (lora_leaves(3, E + shared, rank, *dims, T, seed) for dims, seed in (((H, 2 * inter), 60), ((inter, H), 70)))
+        l2["of"] = l1["of"]
+        ad1, ad2 = (G.epx.Adapters(l["of"], l["a"], l["b"], l["scale"]) for l in (l1, l2))
+        leaves |= dict(a1=l1["a"], b1=l1["b"], a2=l2["a"], b2=l2["b"])
+    d = EpDispatcher(cfg, "cuda:0")
+    ids, probs = d.gate(logits, G.epx.RouteConfig(score="sigmoid", scale=1.5))
+    act = d.gated(d.dispatch(x, ids), w1, probs, ad1)
+    y = d.combine(d.linear(act, w2, ad2), None)
+    y.backward(gy)
+
+    ref = {n: v.detach().double().cpu().requires_grad_() for n, v in leaves.items()}
+    s = torch.sigmoid(ref["logits"]).gather(1, ids.long().cpu())
+    p = torch.zeros(T, E + shared, dtype=torch.float64).scatter(1, ids.long().cpu(), 1.5 * s / s.sum(1, keepdim=True))
+    if shared:
+        p[:, E] = 1.0
+    want = 0
+    for e in range(E + shared):
+        if rank:
+            h = dense_lora(ref["x"], ref["w1"], l1, dict(a=ref["a1"], b=ref["b1"]), e)
+        else:
+            h = ref["x"] @ ref["w1"][e].T
+        g, u = h.split(inter, 1)
+        z = torch.nn.functional.silu(g) * u
+        o = dense_lora(z, ref["w2"], l2, dict(a=ref["a2"], b=ref["b2"]), e) if rank else z @ ref["w2"][e].T
+        want = want + p[:, e:e + 1] * o
+    want.backward(gy.double().cpu())
+    off = lambda g, v: ((g.double().cpu() - v).norm() / v.norm()).item()  # noqa: E731
+    assert off(y.detach(), want.detach()) < 0.012
+    for name, v in leaves.items():
+        assert off(v.grad, ref[name].grad) < 0.024, name
+
+
+def test_only_the_gradients_that_are_needed(G):  # noqa: F811
+    """Frozen weights get no gradient, and the adapters' are the same bits as beside
+    weights that do; a second derivative is refused."""
+    from combine_ep_dispatch_amd.autograd import EpDispatcher
+
+    T, H, E, inter = 33, 64, 4, 24
+    cfg = G.epx.EpConfig(num_tokens=T, hidden=H, num_experts=E, num_segments=1, top_k=2, align=8)
+    d = EpDispatcher(cfg, "cuda:0")
+    ids = torch.argsort(normal(9, T, E, dtype=torch.float32), dim=1)[:, :2].int().contiguous()
+    got = []
+    for frozen in (True, False):
+        l = lora_leaves(2, E, 8, H, 2 * inter, T, 30)
+        w = normal(3, E, 2 * inter, H, std=H ** -0.5).requires_grad_(not frozen)
+        act = d.gated(d.dispatch(normal(1, T, H), ids), w, None, G.epx.Adapters(l["of"], l["a"], l["b"], l["scale"]))
+        act.backward(normal(2, *act.shape))
+        assert (w.grad is None) == frozen
+        got.append((act.detach(), l["a"].grad, l["b"].grad))
+    for one, other in zip(*got):
+        assert torch.equal(one, other)
+    x = normal(1, T, H).requires_grad_()
+    l = lora_leaves(2, E, 8, H, 2 * inter, T, 30)
+    act = d.gated(d.dispatch(x, ids), normal(3, E, 2 * inter, H), None, G.epx.Adapters(l["of"], l["a"], l["b"]))
+    (gx,) = torch.autograd.grad(act.float().square().sum(), x, create_graph=True)
+    with pytest.raises(RuntimeError, match="differentiated twice"):
+        gx.float().sum().backward()
+
+
+def step_of(G, cfg, t, b):  # noqa: F811
+    """A training step of the layer by the calls themselves, into the buffers b."""
+    e, lay = G.epx, t["lay"]
+    e.ep_dispatch_with_layout(cfg, t["ids"].view(-1), t["ws"], lay, t["x"].view(-1), b["recv"].view(-1))
+    e.ep_lora_down(cfg, lay, b["recv"], t["lora"], b["u"])
+    e.ep_expert_gated(cfg, lay, b["recv"], t["w1"], t["probs"], b["act"], t["lora"], b["u"])
+    e.ep_expert_gated_nvfp4(cfg, lay, b["recv"], *t["q"], t["probs"], b["actq"], t["lora"], b["u"])
+    e.ep_expert_gemm(cfg, lay, b["act"], t["w2"], b["out"])
+    e.ep_combine(cfg, lay, b["out"].view(-1), None, b["y"].view(-1))
+    e.ep_expert_gemm_bwd_x(cfg, lay, b["out"], t["w2"], b["gact"])
+    e.ep_expert_gated_bwd(cfg, lay, b["recv"], t["w1"], t["probs"], b["gact"], b["gh"], grad_probs=b["gp"],
+                          workspace=b["parts"], adapters=t["lora"], u=b["u"])
+    e.ep_lora_bwd_u(cfg, lay, b["gh"], t["lora"], b["gu"])
+    e.ep_expert_gemm_bwd_x_lora(cfg, lay, b["gh"], t["w1"], b["gx"], t["lora"], b["gu"])
+    e.ep_lora_bwd_w(cfg, lay, b["recv"], b["gh"], t["lora"], b["u"], b["gu"], b["ga"], b["gb"])
+    e.ep_expert_gemm_bwd_w(cfg, lay, b["gh"], b["recv"], b["gw"])
+    e.ep_expert_gemm_nvfp4_lora(cfg, lay, b["recv"], *t["q"], b["yq"], t["lora"], b["u"])
+
+
+def step_inputs(G, T, H, E, inter, rank, seed):  # noqa: F811
+    K, n = 2, 3
+    cfg = G.epx.EpConfig(num_tokens=T, hidden=H, num_experts=E, num_segments=1, top_k=K, align=8)
+    R = cfg.recv_rows = G.epx.ep_query(cfg).min_recv_rows
+    q, _, _ = nvfp4_weights(seed, E, 2 * inter, H)
+    l = lora_leaves(n, E, rank, H, 2 * inter, T, seed)
+    t = dict(x=normal(seed, T, H), ids=torch.argsort(normal(seed + 1, T, E, dtype=torch.float32), dim=1)[:, :K].int().contiguous(),
+             w1=normal(seed + 2, E, 2 * inter, H, std=H ** -0.5), w2=normal(seed + 3, E, H, inter, std=inter ** -0.5), q=q,
+             probs=torch.rand(T, K, generator=torch.Generator().manual_seed(seed)).cuda(),
+             lora=G.epx.Adapters(l["of"], l["a"].detach(), l["b"].detach(), l["scale"]),
+             ws=G.epx.workspace_for(cfg, "cuda:0"), lay=G.epx.Layout.empty(cfg, "cuda:0"))
+    z = lambda *s, dtype=torch.bfloat16: torch.zeros(*s, dtype=dtype, device="cuda:0")  # noqa: E731
+    f = torch.float32
+    b = dict(recv=z(R, H), u=z(R, rank, dtype=f), act=z(R, inter), actq=z(R, inter), out=z(R, H), y=z(T, H),
+             gact=z(R, inter), gh=z(R, 2 * inter), gp=z(T, K, dtype=f), gu=z(R, rank, dtype=f), gx=z(R, H),
+             ga=z(n, E, rank, H), gb=z(n, E, 2 * inter, rank), gw=z(E, 2 * inter, H), yq=z(R, 2 * inter),
+             parts=G.epx.gated_workspace_for(cfg, inter, "cuda:0").zero_())
+    return cfg, t, b
+
+
+def test_captured_step_replays_like_the_eager_one(G):  # noqa: F811
+    """A step captured into a graph: every replay gives the eager call's bits, with
+    new inputs and other work in between."""
+    cfg, t, b = step_inputs(G, 20, 64, 8, 32, 16, 5)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step_of(G, cfg, t, b)
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step_of(G, cfg, t, b)
+    for i in range(4):
+        t["x"].copy_(normal(40 + i, *t["x"].shape))
+        t["ids"].copy_(torch.argsort(normal(50 + i, 20, 8, dtype=torch.float32), dim=1)[:, :2].int())
+        t["lora"].token_adapter.copy_(torch.randint(-1, 3, (20,), generator=torch.Generator().manual_seed(i)).int())
+        for v in b.values():
+            v.zero_()
+        step_of(G, cfg, t, b)
+        torch.cuda.synchronize()
+        want = {n: v.clone() for n, v in b.items()}
+        for v in b.values():
+            v.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        for n, v in b.items():
+            assert torch.equal(v.view(torch.uint8), want[n].view(torch.uint8)), (i, n)
+
+
+def test_steps_on_two_streams(G):  # noqa: F811
+    """Two different steps at once, each with buffers of its own on a stream of its own."""
+    steps = [step_inputs(G, 300, 144, 4, 72, 24, 5), step_inputs(G, 33, 64, 8, 40, 8, 9)]
+    want = []
+    for cfg, t, b in steps:
+        step_of(G, cfg, t, b)
+        torch.cuda.synchronize()
+        want.append({n: v.clone() for n, v in b.items()})
+        for v in b.values():
+            v.zero_()
+    streams = [torch.cuda.Stream() for _ in steps]
+    torch.cuda.synchronize()
+    for _ in range(3):
+        for (cfg, t, b), stream in zip(steps, streams):
+            with torch.cuda.stream(stream):
+                step_of(G, cfg, t, b)
+    torch.cuda.synchronize()
+    for (_, _, b), w in zip(steps, want):
+        for n, v in b.items():
+            assert torch.equal(v.view(torch.uint8), w[n].view(torch.uint8)), n
+
+
+def test_offsets_past_32_bits(G):  # noqa: F811
+    """Receive rows, weights and adapters of more than 2^32 bytes: the last ones are right."""
+    dev = "cuda:0"
+
+    def one_row(cfg, lay, e, x, w, gate, up, lo, u):
+        row = int(lay.token_row.view(-1)[cfg.num_tokens - 1])
+        act = torch.zeros(cfg.recv_rows, gate.shape[0], dtype=torch.bfloat16, device=dev)
+        G.epx.ep_lora_down(cfg, lay, x, lo, u)
+        G.epx.ep_expert_gated(cfg, lay, x, w, None, act, lo, u)
+        y = torch.zeros(cfg.recv_rows, 2 * gate.shape[0], dtype=torch.bfloat16, device=dev)
+        G.epx.ep_expert_gemm_lora(cfg, lay, x, w, y, lo, u)
+        k = int(lo.token_adapter[-1])
+        v = x[row].double().cpu()
+        m, a, b = torch.cat([gate, up]).double().cpu(), lo.a[k, e].double().cpu(), lo.b[k, e].double().cpu()
+        uu, eu = u_of(v[None], a, 1.0)
+        want = m @ v + (uu @ b.T)[0]
+        err = (m.abs() @ v.abs() * (len(v) + 2) + (uu.abs() @ b.abs().T)[0] * (2 * a.shape[0] + 4)) * U32 + (eu @ b.abs().T)[0]
+        check(y[row], want, rounded(want, err), "y")
+        (g, uv), (eg, ev) = want.split(len(want) // 2), err.split(len(want) // 2)
+        s, silu = silu_parts(g)
+        e_act = 1.1 * eg * (uv.abs() + ev) + silu.abs() * ev + (silu * uv).abs() * (24 + g.abs()) * U32 + TINY
+        check(act[row], silu * uv, rounded(silu * uv, e_act), "act")
+
+    # 330 000 rows of 7168 values (4.7 GB)
+    T, H, inter, rank = 330_000, 7168, 8, 8
+    cfg = G.epx.EpConfig(num_tokens=T, hidden=16, num_experts=2, num_segments=1, top_k=1)
+    cfg.recv_rows = T
+    lay = G.epx.Layout.empty(cfg, dev)
+    ids = torch.ones(T, dtype=torch.int32, device=dev)
+    G.epx.ep_dispatch_layout(cfg, ids, G.epx.workspace_for(cfg, dev), lay)
+    x = torch.empty(T, H, dtype=torch.bfloat16, device=dev).normal_()
+    w = normal(3, 2, 2 * inter, H, std=H ** -0.5)
+    of = torch.full((T,), -1, dtype=torch.int32, device=dev)
+    of[-1] = 1
+    lo = G.epx.Adapters(of, normal(4, 2, 2, rank, H, std=H ** -0.5), normal(5, 2, 2, 2 * inter, rank))
+    G.say("[gpu] far rows")
+    one_row(cfg, lay, 1, x, w, w[1, :inter], w[1, inter:], lo, torch.empty(T, rank, device=dev))
+    del x, w
+    # 160 experts of 4096 x 4096 (5.4 GB), 5 adapters of rank 128 beside them (1.7 GB)
+    E, H, inter, rank, n = 160, 4096, 2048, 128, 5
+    cfg = G.epx.EpConfig(num_tokens=3, hidden=16, num_experts=E, num_segments=1, top_k=1)
+    cfg.recv_rows = 3
+    lay = G.epx.Layout.empty(cfg, dev)
+    G.epx.ep_dispatch_layout(cfg, torch.tensor([0, 3, E - 1], dtype=torch.int32, device=dev), G.epx.workspace_for(cfg, dev), lay)
+    w = torch.empty(E, 2 * inter, H, dtype=torch.bfloat16, device=dev).normal_(0, H ** -0.5)
+    a = torch.empty(n, E, rank, H, dtype=torch.bfloat16, device=dev).normal_(0, H ** -0.5)
+    b = torch.empty(n, E, 2 * inter, rank, dtype=torch.bfloat16, device=dev).normal_(0, rank ** -0.5)
+    lo = G.epx.Adapters(torch.tensor([-1, 0, n - 1], dtype=torch.int32, device=dev), a, b)
+    G.say("[gpu] far weights and adapters")
+    one_row(cfg, lay, E - 1, normal(8, 3, H), w, w[E - 1, :inter], w[E - 1, inter:], lo, torch.empty(3, rank, device=dev))
