@@ -14,6 +14,19 @@ __device__ __forceinline__ int32_t row_adapter(const BlockArgs& a, int64_t r) {
     return ad < 0 || ad >= a.l.n ? -1 : ad;
 }
 
+// As row_adapter for COUNT rows of this lane, row(n) each (any row of the buffer), -1
+// where on(n) is false.  All loads go out together, twice.
+template <int COUNT, typename Row, typename On>
+__device__ __forceinline__ void row_adapters(const BlockArgs& a, Row row, On on, int32_t (&ad)[COUNT]) {
+    int32_t t[COUNT];
+#pragma unroll
+    for (int n = 0; n < COUNT; ++n) t[n] = a.src_info[2 * row(n)];
+#pragma unroll
+    for (int n = 0; n < COUNT; ++n) ad[n] = a.l.token_adapter[t[n] < 0 || t[n] >= a.T ? 0 : t[n]];
+#pragma unroll
+    for (int n = 0; n < COUNT; ++n) ad[n] = !on(n) || t[n] < 0 || t[n] >= a.T || ad[n] < 0 || ad[n] >= a.l.n ? -1 : ad[n];
+}
+
 // The smallest of the adapters `ad` (COUNT of each of the 16 lanes i; the
 // quarters of the wave hold the same) past `last`, kNoAdapter if there is none.
 constexpr int32_t kNoAdapter = INT32_MAX;
@@ -62,8 +75,8 @@ __device__ __forceinline__ void add_adapters(const BlockArgs& a, int64_t first, 
                                              f32x4 (&acc)[KF][KN]) {
     const int lane = threadIdx.x & (kWave - 1), i = lane % 16, q = lane / 16;
     int32_t ad[KN];
-#pragma unroll
-    for (int n = 0; n < KN; ++n) ad[n] = wn + n * 16 + i < rows ? row_adapter(a, first + wn + n * 16 + i) : -1;
+    row_adapters<KN>(
+        a, [&](int n) { return first + min(wn + n * 16 + i, rows - 1); }, [&](int n) { return wn + n * 16 + i < rows; }, ad);
     const int32_t chunks = uniform(a.l.rank / 4);  // of 8 halves: the rounded values', then the rests'
     const uint16_t* const u = reinterpret_cast<const uint16_t*>(a.u) + (first + wn + i) * 2 * a.l.rank;
     auto load_u = [&](bf16x8 (&v)[KN], int32_t cur, int32_t c) {
