@@ -231,7 +231,7 @@ hipError_t down_by_size(const BlockArgs& a, float* u, hipStream_t stream) {
 }
 
 constexpr int kGradThreads = 256, kGradRows = 64, kGradCols = 256;  // rows a step, columns of a tile
-constexpr int kList = 512;                                          // rows looked through at a time
+constexpr int kLook = 4, kList = kLook * kGradThreads;               // rows that a thread, and all, look through at a time
 
 // Gradients of one adapter's weights of one expert, columns c0 on: sum over the
 // rows r of the expert whose tokens have the adapter of v[r]^T d[r], d = x (of
@@ -253,44 +253,63 @@ __global__ __launch_bounds__(kGradThreads) void k_lora_bwd_w(BlockArgs a, const 
     const uint16_t* const vv = v + rows.first * 2 * rank;
     f32x4 acc[4][KP] = {};
     int32_t have = 0;  // rows in the list
+    constexpr int kX = kGradRows * kGradCols / 8 / kGradThreads;  // 16-byte pieces of d that a thread copies a step
     for (int32_t r0 = 0; r0 < rows.rows || have > 0; r0 += kList) {
         // append the next rows' matches
-        for (int32_t b = r0; b < min(r0 + kList, rows.rows); b += kGradThreads) {
-            const int32_t r = b + (int32_t)threadIdx.x;
-            const bool mine = r < rows.rows && row_adapter(a, rows.first + r) == ad;
+        int32_t of[kLook];
+        row_adapters<kLook>(
+            a, [&](int k) { return rows.first + min(r0 + k * kGradThreads + (int32_t)threadIdx.x, rows.rows - 1); },
+            [&](int k) { return r0 + k * kGradThreads + (int32_t)threadIdx.x < rows.rows; }, of);
+#pragma unroll
+        for (int k = 0; k < kLook; ++k) {
+            const bool mine = of[k] == ad;
             const uint64_t m = __builtin_amdgcn_ballot_w64(mine);
             if (lane == 0) counts[w] = __popcll(m);
             __syncthreads();
             int32_t at = have;
-            for (int k = 0; k < 4; ++k) {
-                if (k == w && mine) list[at + lanes_below(m)] = r;
-                at += counts[k];
+            for (int o = 0; o < 4; ++o) {
+                if (o == w && mine) list[at + lanes_below(m)] = r0 + k * kGradThreads + (int32_t)threadIdx.x;
+                at += counts[o];
             }
             have = at;
             __syncthreads();
         }
         const bool last = r0 + kList >= rows.rows;
-        int32_t done = 0;
-        for (; have - done >= kGradRows || (last && done < have); done += kGradRows) {
-            const int32_t n = min(kGradRows, have - done);
-            // d: 64 rows of 32 chunks of 8 values, one a thread and turn
+        const int32_t turns = last ? (have + kGradRows - 1) / kGradRows : have / kGradRows, done = turns * kGradRows;
+        // a step's rows on their way to LDS, while the step before is multiplied
+        v4u xr[kX], vr[KP];
+        auto fetch = [&](int32_t turn) {
+            const int32_t from = turn * kGradRows, n = min(kGradRows, have - from);
+            // d: 64 rows of 32 chunks of 8 values
 #pragma unroll
-            for (int k = 0; k < kGradRows * kGradCols / 8 / kGradThreads; ++k) {
+            for (int k = 0; k < kX; ++k) {
                 const int at = k * kGradThreads + threadIdx.x, r = at / 32, c = at % 32;
-                v4u o = {};
-                if (r < n && c0 + c * 8 < C) o = *reinterpret_cast<const v4u*>(d + (int64_t)list[done + r] * C + c * 8);
-                *reinterpret_cast<v4u*>(xs + r * kGradCols + (((c / 2) ^ XOp::swizzle(r)) * 2 + c % 2) * 8) = o;
+                xr[k] = v4u{};
+                if (r < n && c0 + c * 8 < C) xr[k] = *reinterpret_cast<const v4u*>(d + (int64_t)list[from + r] * C + c * 8);
             }
             // v: 64 rows of KP * 4 chunks
 #pragma unroll
             for (int k = 0; k < KP; ++k) {
                 const int at = k * kGradThreads + threadIdx.x, r = at / (KP * 4), c = at % (KP * 4);
                 const int half = c / (KP * 2), p = c % (KP * 2) * 8;
-                v4u o = {};
-                if (r < n && p < rank) o = *reinterpret_cast<const v4u*>(vv + (int64_t)list[done + r] * 2 * rank + half * rank + p);
-                *reinterpret_cast<v4u*>(vs + r * P * 2 + (((c / 2) ^ VOp::swizzle(r)) * 2 + c % 2) * 8) = o;
+                vr[k] = v4u{};
+                if (r < n && p < rank) vr[k] = *reinterpret_cast<const v4u*>(vv + (int64_t)list[from + r] * 2 * rank + half * rank + p);
             }
-            __syncthreads();
+        };
+        if (turns > 0) fetch(0);
+        for (int32_t turn = 0; turn < turns; ++turn) {
+#pragma unroll
+            for (int k = 0; k < kX; ++k) {
+                const int at = k * kGradThreads + threadIdx.x, r = at / 32, c = at % 32;
+                *reinterpret_cast<v4u*>(xs + r * kGradCols + (((c / 2) ^ XOp::swizzle(r)) * 2 + c % 2) * 8) = xr[k];
+            }
+#pragma unroll
+            for (int k = 0; k < KP; ++k) {
+                const int at = k * kGradThreads + threadIdx.x, r = at / (KP * 4), c = at % (KP * 4);
+                *reinterpret_cast<v4u*>(vs + r * P * 2 + (((c / 2) ^ VOp::swizzle(r)) * 2 + c % 2) * 8) = vr[k];
+            }
+            lds_barrier();
+            if (turn + 1 < turns) fetch(turn + 1);
 #pragma unroll
             for (int kk = 0; kk < 2; ++kk) {
                 bf16x8 xf[4];
@@ -307,7 +326,7 @@ __global__ __launch_bounds__(kGradThreads) void k_lora_bwd_w(BlockArgs a, const 
                     }
                 }
             }
-            __syncthreads();
+            lds_barrier();
         }
         // what is left of the list moves to its front
         const int32_t left = max(have - done, 0);
