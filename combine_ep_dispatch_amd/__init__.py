@@ -646,7 +646,7 @@ def _block_layout(layout: Layout, cfg: EpConfig, device, *names: str) -> EpLayou
 def ep_lora_down(cfg: EpConfig, layout: Layout, x: torch.Tensor, adapters: Adapters, u: torch.Tensor,
                  stream=None) -> None:
     """u[r] = scale * a[adapter, expert of r] @ x[r], for the products with adapters:
-    x bf16 [R, in], u float32 [R, rank] (words that hold two bf16 each, see include/epx.h)."""
+    x bf16 [R, in], u float32 [R, rank]."""
     dev = x.device
     n_in = _columns(x, "x", cfg.recv_rows)
     lora, pu = _lora(cfg, adapters, u, n_in, None, dev)

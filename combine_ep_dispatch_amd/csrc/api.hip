@@ -400,11 +400,11 @@ int check_block(const Shape& d, const ep_layout_t* L, int32_t in_dim, int32_t ou
 }
 
 BlockArgs block_args(const Shape& d, const ep_layout_t* L, const ep_lora_t* l, int32_t in_dim, int32_t out_dim,
-                     const void* u, void* out) {
+                     const float* u, void* out) {
     BlockArgs a = {};
     a.e = expert_args(d, L, in_dim, out_dim, out);
     if (l != nullptr) a.l = {l->token_adapter, l->a, l->b, l->scale, l->num_adapters, l->rank};
-    a.u = static_cast<const float*>(u);
+    a.u = u;
     a.src_info = L->src_info;
     a.token_row = L->token_row;
     a.T = d.T;
@@ -415,7 +415,7 @@ BlockArgs block_args(const Shape& d, const ep_layout_t* L, const ep_lora_t* l, i
 
 // Of the gated block: inter columns of act, optional adapters.
 int check_gated(const Shape& d, const ep_layout_t* L, const ep_lora_t* l, int32_t in_dim, int32_t inter,
-                int32_t in_multiple, const void* ulora, const float* probs) {
+                int32_t in_multiple, const float* ulora, const float* probs) {
     int rc;
     if ((rc = check_block(d, L, in_dim, inter, in_multiple)) != EP_OK) return rc;
     if (l != nullptr) {
@@ -428,7 +428,7 @@ int check_gated(const Shape& d, const ep_layout_t* L, const ep_lora_t* l, int32_
 }
 
 BlockArgs gated_args(const Shape& d, const ep_layout_t* L, const ep_lora_t* l, int32_t in_dim, int32_t inter,
-                     const void* ulora, const float* probs, void* act) {
+                     const float* ulora, const float* probs, void* act) {
     BlockArgs a = block_args(d, L, l, in_dim, 2 * inter, ulora, act);
     a.probs = probs;
     a.I = inter;
@@ -902,7 +902,7 @@ int ep_expert_gemm_nvfp4(const ep_cfg_t* cfg, const ep_layout_t* layout, int32_t
 }
 
 int ep_lora_down(const ep_cfg_t* cfg, const ep_layout_t* layout, const ep_lora_t* lora, int32_t in_dim,
-                 const uint16_t* x, void* u, void* stream) {
+                 const uint16_t* x, float* u, void* stream) {
     Shape d;
     int rc = derive(cfg, &d);
     if (rc != EP_OK) return rc;
@@ -913,12 +913,12 @@ int ep_lora_down(const ep_cfg_t* cfg, const ep_layout_t* layout, const ep_lora_t
     hipStream_t st = static_cast<hipStream_t>(stream);
     BlockArgs a = block_args(d, layout, lora, in_dim, 8, nullptr, nullptr);
     a.e.x = x;
-    if ((rc = expert_status(launch_lora_down(a, static_cast<float*>(u), st))) != EP_OK) return rc;
+    if ((rc = expert_status(launch_lora_down(a, u, st))) != EP_OK) return rc;
     return zero_pad(d, layout, u, (int64_t)lora->rank * 4, st);
 }
 
 int ep_lora_bwd_u(const ep_cfg_t* cfg, const ep_layout_t* layout, const ep_lora_t* lora, int32_t out_dim,
-                  const uint16_t* grad_y, void* grad_u, void* stream) {
+                  const uint16_t* grad_y, float* grad_u, void* stream) {
     Shape d;
     int rc = derive(cfg, &d);
     if (rc != EP_OK) return rc;
@@ -929,12 +929,12 @@ int ep_lora_bwd_u(const ep_cfg_t* cfg, const ep_layout_t* layout, const ep_lora_
     hipStream_t st = static_cast<hipStream_t>(stream);
     BlockArgs a = block_args(d, layout, lora, 8, out_dim, nullptr, nullptr);
     a.e.gy = grad_y;
-    if ((rc = expert_status(launch_lora_bwd_u(a, static_cast<float*>(grad_u), st))) != EP_OK) return rc;
+    if ((rc = expert_status(launch_lora_bwd_u(a, grad_u, st))) != EP_OK) return rc;
     return zero_pad(d, layout, grad_u, (int64_t)lora->rank * 4, st);
 }
 
 int ep_expert_gemm_lora(const ep_cfg_t* cfg, const ep_layout_t* layout, const ep_lora_t* lora, int32_t in_dim,
-                        int32_t out_dim, const uint16_t* x, const uint16_t* w, const void* u, uint16_t* y, void* stream) {
+                        int32_t out_dim, const uint16_t* x, const uint16_t* w, const float* u, uint16_t* y, void* stream) {
     Shape d;
     int rc = derive(cfg, &d);
     if (rc != EP_OK) return rc;
@@ -954,7 +954,7 @@ int ep_expert_gemm_lora(const ep_cfg_t* cfg, const ep_layout_t* layout, const ep
 
 int ep_expert_gemm_nvfp4_lora(const ep_cfg_t* cfg, const ep_layout_t* layout, const ep_lora_t* lora, int32_t in_dim,
                               int32_t out_dim, const uint16_t* x, const uint8_t* codes, const uint8_t* scales,
-                              const uint16_t* rowscale, const void* u, uint16_t* y, void* stream) {
+                              const uint16_t* rowscale, const float* u, uint16_t* y, void* stream) {
     Shape d;
     int rc = derive(cfg, &d);
     if (rc != EP_OK) return rc;
@@ -975,7 +975,7 @@ int ep_expert_gemm_nvfp4_lora(const ep_cfg_t* cfg, const ep_layout_t* layout, co
 }
 
 int ep_expert_gemm_bwd_x_lora(const ep_cfg_t* cfg, const ep_layout_t* layout, const ep_lora_t* lora, int32_t in_dim,
-                              int32_t out_dim, const uint16_t* grad_y, const uint16_t* w, const void* grad_u,
+                              int32_t out_dim, const uint16_t* grad_y, const uint16_t* w, const float* grad_u,
                               uint16_t* grad_x, void* stream) {
     Shape d;
     int rc = derive(cfg, &d);
@@ -995,7 +995,7 @@ int ep_expert_gemm_bwd_x_lora(const ep_cfg_t* cfg, const ep_layout_t* layout, co
 }
 
 int ep_lora_bwd_w(const ep_cfg_t* cfg, const ep_layout_t* layout, const ep_lora_t* lora, int32_t in_dim,
-                  int32_t out_dim, const uint16_t* x, const uint16_t* grad_y, const void* u, const void* grad_u,
+                  int32_t out_dim, const uint16_t* x, const uint16_t* grad_y, const float* u, const float* grad_u,
                   void* grad_a, void* grad_b, int32_t grad_type, void* stream) {
     Shape d;
     int rc = derive(cfg, &d);
@@ -1012,12 +1012,12 @@ int ep_lora_bwd_w(const ep_cfg_t* cfg, const ep_layout_t* layout, const ep_lora_
     a.e.x = x;
     a.e.gy = grad_y;
     a.e.grad_type = grad_type;
-    return expert_status(launch_lora_bwd_w(a, static_cast<const float*>(grad_u), grad_a, grad_b,
+    return expert_status(launch_lora_bwd_w(a, grad_u, grad_a, grad_b,
                                            static_cast<hipStream_t>(stream)));
 }
 
 int ep_expert_gated(const ep_cfg_t* cfg, const ep_layout_t* layout, const ep_lora_t* lora, int32_t in_dim, int32_t inter,
-                    const uint16_t* x, const uint16_t* w, const float* probs, const void* ulora, uint16_t* act,
+                    const uint16_t* x, const uint16_t* w, const float* probs, const float* ulora, uint16_t* act,
                     void* stream) {
     Shape d;
     int rc = derive(cfg, &d);
@@ -1036,7 +1036,7 @@ int ep_expert_gated(const ep_cfg_t* cfg, const ep_layout_t* layout, const ep_lor
 
 int ep_expert_gated_nvfp4(const ep_cfg_t* cfg, const ep_layout_t* layout, const ep_lora_t* lora, int32_t in_dim,
                           int32_t inter, const uint16_t* x, const uint8_t* codes, const uint8_t* scales,
-                          const uint16_t* rowscale, const float* probs, const void* ulora, uint16_t* act, void* stream) {
+                          const uint16_t* rowscale, const float* probs, const float* ulora, uint16_t* act, void* stream) {
     Shape d;
     int rc = derive(cfg, &d);
     if (rc != EP_OK) return rc;
@@ -1057,7 +1057,7 @@ int ep_expert_gated_nvfp4(const ep_cfg_t* cfg, const ep_layout_t* layout, const 
 }
 
 int ep_expert_gated_bwd(const ep_cfg_t* cfg, const ep_layout_t* layout, const ep_lora_t* lora, int32_t in_dim,
-                        int32_t inter, const uint16_t* x, const uint16_t* w, const float* probs, const void* ulora,
+                        int32_t inter, const uint16_t* x, const uint16_t* w, const float* probs, const float* ulora,
                         const uint16_t* grad_act, uint16_t* grad_h, uint16_t* act, float* grad_probs, void* workspace,
                         int64_t workspace_bytes, void* stream) {
     Shape d;

@@ -107,7 +107,7 @@ struct AdapterOperand : std::conditional<BWD, ColsOperand<P, 1>, RowsOperand<P, 
 // adapters: with few tiles, as in a decode step, each adapter's weights are read by
 // a workgroup of their own.  BWD: gu, from gy and B.
 template <bool BWD, int P, int NT>
-__global__ __launch_bounds__(kDownThreads) void k_lora_down(BlockArgs a, uint16_t* u) {
+__global__ __launch_bounds__(kDownThreads) void k_lora_down(BlockArgs a, float* u) {
     using Op = AdapterOperand<BWD, P>;
     constexpr int kStep = (NT + P) * kStepL;  // elements of a wave's step
     constexpr int kRing = NT + P <= 32 ? 4 : NT + P <= 96 ? 3 : 2;
@@ -191,10 +191,7 @@ __global__ __launch_bounds__(kDownThreads) void k_lora_down(BlockArgs a, uint16_
             float v = 0.0f;
 #pragma unroll
             for (int k = 0; k < kDownWaves; ++k) v += part[(k * NT + r) * (P + 1) + p];
-            const uint32_t two = split_bf16(s * v);
-            uint16_t* const to = u + (t.first + r) * 2 * rank + p;
-            to[0] = (uint16_t)two;
-            to[rank] = (uint16_t)(two >> 16);
+            u[(t.first + r) * rank + p] = s * v;
         }
         __syncthreads();
     }
@@ -202,9 +199,7 @@ __global__ __launch_bounds__(kDownThreads) void k_lora_down(BlockArgs a, uint16_
     // rows without an adapter: zeros
     for (int at = threadIdx.x; at < NT * P; at += kDownThreads) {
         const int r = at / P, p = at % P;
-        if (p >= rank || r >= t.rows || ads[r] >= 0) continue;
-        uint16_t* const to = u + (t.first + r) * 2 * rank + p;
-        to[0] = to[rank] = 0;
+        if (p < rank && r < t.rows && ads[r] < 0) u[(t.first + r) * rank + p] = 0.0f;
     }
 }
 
@@ -216,8 +211,7 @@ hipError_t down(const BlockArgs& a, float* u, hipStream_t stream) {
     if (blocks == 0) return hipSuccess;
     const int share = tiles <= 2 * kCus ? (a.l.n < NT ? a.l.n : NT) : 1;
     if (const hipError_t e = check_grid(blocks, kDownThreads)) return e;
-    hipLaunchKernelGGL((k_lora_down<BWD, P, NT>), dim3((unsigned)blocks, (unsigned)share), dim3(kDownThreads), 0, stream, a,
-                       reinterpret_cast<uint16_t*>(u));
+    hipLaunchKernelGGL((k_lora_down<BWD, P, NT>), dim3((unsigned)blocks, (unsigned)share), dim3(kDownThreads), 0, stream, a, u);
     return hipGetLastError();
 }
 
@@ -238,11 +232,13 @@ constexpr int kLook = 4, kList = kLook * kGradThreads;               // rows tha
 // width in; result [rank, in]) or gy (out; result [out, rank]), v = gu or u.  The
 // rows are picked out in order, 64 a step; d's go through registers to LDS.
 template <int KP, bool OUT>
-__global__ __launch_bounds__(kGradThreads) void k_lora_bwd_w(BlockArgs a, const uint16_t* v, void* out, int32_t ctiles) {
+__global__ __launch_bounds__(kGradThreads) void k_lora_bwd_w(BlockArgs a, const float* v, void* out, int32_t ctiles) {
     using XOp = ColsOperand<kGradCols, 4>;
-    using VOp = ColsOperand<KP * 32, 4>;  // the rounded values, then the rests
-    constexpr int P = KP * 16;
-    __shared__ __align__(1024) uint16_t xs[kGradRows * kGradCols], vs[kGradRows * P * 2];
+    // v as three bf16 whose sum it is (24 significant bits): the sums over the rows are
+    // as good as 32-bit products' would be
+    constexpr int P = KP * 16, kParts = 3;
+    using VOp = ColsOperand<P, 4>;
+    __shared__ __align__(1024) uint16_t xs[kGradRows * kGradCols], vs[kParts][kGradRows * P];
     __shared__ int32_t list[kList + kGradRows], counts[5];
     const int lane = threadIdx.x & (kWave - 1), w = uniform((int32_t)(threadIdx.x / kWave)), i = lane % 16, q = lane / 16;
     const int32_t EX = a.e.E + a.e.shared, rank = a.l.rank, C = OUT ? a.e.on : a.e.in;
@@ -250,7 +246,7 @@ __global__ __launch_bounds__(kGradThreads) void k_lora_bwd_w(BlockArgs a, const 
     const int32_t g = expert < a.e.E ? expert / a.e.E_loc * a.e.G + a.e.shared + expert % a.e.E_loc : a.e.src_seg * a.e.G;
     const GroupRows rows = group_rows(a.e, g);
     const uint16_t* const d = (OUT ? a.e.gy : a.e.x) + rows.first * C + c0;
-    const uint16_t* const vv = v + rows.first * 2 * rank;
+    const float* const vv = v + rows.first * rank;
     f32x4 acc[4][KP] = {};
     int32_t have = 0;  // rows in the list
     constexpr int kX = kGradRows * kGradCols / 8 / kGradThreads;  // 16-byte pieces of d that a thread copies a step
@@ -277,7 +273,8 @@ __global__ __launch_bounds__(kGradThreads) void k_lora_bwd_w(BlockArgs a, const 
         const bool last = r0 + kList >= rows.rows;
         const int32_t turns = last ? (have + kGradRows - 1) / kGradRows : have / kGradRows, done = turns * kGradRows;
         // a step's rows on their way to LDS, while the step before is multiplied
-        v4u xr[kX], vr[KP];
+        v4u xr[kX];
+        f32x4 vr[KP];
         auto fetch = [&](int32_t turn) {
             const int32_t from = turn * kGradRows, n = min(kGradRows, have - from);
             // d: 64 rows of 32 chunks of 8 values
@@ -287,13 +284,12 @@ __global__ __launch_bounds__(kGradThreads) void k_lora_bwd_w(BlockArgs a, const 
                 xr[k] = v4u{};
                 if (r < n && c0 + c * 8 < C) xr[k] = *reinterpret_cast<const v4u*>(d + (int64_t)list[from + r] * C + c * 8);
             }
-            // v: 64 rows of KP * 4 chunks
+            // v: 64 rows of KP * 4 chunks of 4 values
 #pragma unroll
             for (int k = 0; k < KP; ++k) {
-                const int at = k * kGradThreads + threadIdx.x, r = at / (KP * 4), c = at % (KP * 4);
-                const int half = c / (KP * 2), p = c % (KP * 2) * 8;
-                vr[k] = v4u{};
-                if (r < n && p < rank) vr[k] = *reinterpret_cast<const v4u*>(vv + (int64_t)list[from + r] * 2 * rank + half * rank + p);
+                const int at = k * kGradThreads + threadIdx.x, r = at / (KP * 4), p = at % (KP * 4) * 4;
+                vr[k] = f32x4{};
+                if (r < n && p < rank) vr[k] = *reinterpret_cast<const f32x4*>(vv + (int64_t)list[from + r] * rank + p);
             }
         };
         if (turns > 0) fetch(0);
@@ -306,7 +302,17 @@ __global__ __launch_bounds__(kGradThreads) void k_lora_bwd_w(BlockArgs a, const 
 #pragma unroll
             for (int k = 0; k < KP; ++k) {
                 const int at = k * kGradThreads + threadIdx.x, r = at / (KP * 4), c = at % (KP * 4);
-                *reinterpret_cast<v4u*>(vs + r * P * 2 + (((c / 2) ^ VOp::swizzle(r)) * 2 + c % 2) * 8) = vr[k];
+                f32x4 left = vr[k];
+#pragma unroll
+                for (int o = 0; o < kParts; ++o) {
+                    const v2u w = {pack_bf16x2(left[0], left[1]), pack_bf16x2(left[2], left[3])};
+                    *reinterpret_cast<v2u*>(vs[o] + r * P + ((c / 4) ^ VOp::swizzle(r)) * 16 + c % 4 * 4) = w;
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const float h = j % 2 ? bf16_hi(w[j / 2]) : bf16_lo(w[j / 2]);
+                        left[j] = __builtin_isinf(h) ? 0.0f : left[j] - h;  // an infinity leaves nothing
+                    }
+                }
             }
             lds_barrier();
             if (turn + 1 < turns) fetch(turn + 1);
@@ -316,8 +322,8 @@ __global__ __launch_bounds__(kGradThreads) void k_lora_bwd_w(BlockArgs a, const 
 #pragma unroll
                 for (int f = 0; f < 4; ++f) xf[f] = XOp::fragment(xs, w * 64 + f * 16, kk);
 #pragma unroll
-                for (int k = 0; k < 2 * KP; ++k) {
-                    const bf16x8 vf = VOp::fragment(vs, k * 16, kk);
+                for (int k = 0; k < kParts * KP; ++k) {
+                    const bf16x8 vf = VOp::fragment(vs[k / KP], k % KP * 16, kk);
 #pragma unroll
                     for (int f = 0; f < 4; ++f) {
                         f32x4& s = acc[f][k % KP];
@@ -361,8 +367,8 @@ hipError_t bwd_w(const BlockArgs& a, const float* v, void* out, hipStream_t stre
     const int32_t ctiles = ((OUT ? a.e.on : a.e.in) + kGradCols - 1) / kGradCols;
     const int64_t blocks = (int64_t)a.l.n * (a.e.E + a.e.shared) * ctiles;
     if (const hipError_t e = check_grid(blocks, kGradThreads)) return e;
-    hipLaunchKernelGGL((k_lora_bwd_w<KP, OUT>), dim3((unsigned)blocks), dim3(kGradThreads), 0, stream, a,
-                       reinterpret_cast<const uint16_t*>(v), out, ctiles);
+    hipLaunchKernelGGL((k_lora_bwd_w<KP, OUT>), dim3((unsigned)blocks), dim3(kGradThreads), 0, stream, a, v, out,
+                       ctiles);
     return hipGetLastError();
 }
 

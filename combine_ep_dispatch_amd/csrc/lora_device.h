@@ -40,15 +40,21 @@ __device__ __forceinline__ int32_t next_adapter(const int32_t (&ad)[COUNT], int3
     return uniform(v);
 }
 
-// u (and grad_u) travel as two bf16 a value: row r of [R, rank] words holds the
-// rank values rounded to bf16, then what the rounding left.  Their sum has 16
-// significant bits, so that the products with u are as good as 32-bit ones next to
-// the result's 8; one bf16 alone would add a rounding of its own where the
-// adapters make most of the result.  An infinity leaves nothing (not NaN).
-__device__ __forceinline__ uint32_t split_bf16(float v) {  // rounded value low, rest high
-    const uint32_t hi = f32_to_bf16(v);
-    const float rest = __builtin_isinf(bf16_lo(hi)) ? 0.0f : v - bf16_lo(hi);
-    return hi | f32_to_bf16(rest) << 16;
+// Eight values as bf16: rounded, or, with `rest`, what the rounding left.  Both
+// together have 16 significant bits, so that products with u are off by 2^-16 of
+// their terms, next to the result's 2^-8; one bf16 alone would add a rounding of its
+// own where the adapters make most of the result.  An infinity leaves nothing (not NaN).
+__device__ __forceinline__ bf16x8 split8(const f32x4 a, const f32x4 b, bool rest) {
+    v4u o;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const float x = j < 2 ? a[2 * j] : b[2 * j - 4], y = j < 2 ? a[2 * j + 1] : b[2 * j - 3];
+        const uint32_t w = pack_bf16x2(x, y);
+        const float rx = __builtin_isinf(bf16_lo(w)) ? 0.0f : x - bf16_lo(w);
+        const float ry = __builtin_isinf(bf16_hi(w)) ? 0.0f : y - bf16_hi(w);
+        o[j] = rest ? pack_bf16x2(rx, ry) : w;
+    }
+    return __builtin_bit_cast(bf16x8, o);
 }
 
 // Whether one of the values is an infinity or NaN: all exponent bits set.
@@ -77,14 +83,23 @@ __device__ __forceinline__ void add_adapters(const BlockArgs& a, int64_t first, 
     int32_t ad[KN];
     row_adapters<KN>(
         a, [&](int n) { return first + min(wn + n * 16 + i, rows - 1); }, [&](int n) { return wn + n * 16 + i < rows; }, ad);
-    const int32_t chunks = uniform(a.l.rank / 4);  // of 8 halves: the rounded values', then the rests'
-    const uint16_t* const u = reinterpret_cast<const uint16_t*>(a.u) + (first + wn + i) * 2 * a.l.rank;
+    const int32_t chunks = uniform(a.l.rank / 4);  // of 8 values: the rounded ones, then the rests
+    const float* const u = a.u + (first + wn + i) * a.l.rank;
     auto load_u = [&](bf16x8 (&v)[KN], int32_t cur, int32_t c) {
+        const bool rest = c >= chunks / 2;
+        const int32_t at = (rest ? c - chunks / 2 : c) * 8;
+        f32x4 lo[KN], hi[KN];
 #pragma unroll
         for (int n = 0; n < KN; ++n) {
-            v[n] = bf16x8{};
-            if (c < chunks && ad[n] == cur) v[n] = *reinterpret_cast<const bf16x8*>(u + n * 32 * a.l.rank + c * 8);
+            lo[n] = hi[n] = f32x4{};
+            if (c < chunks && ad[n] == cur) {
+                const f32x4* const p = reinterpret_cast<const f32x4*>(u + n * 16 * a.l.rank + at);
+                lo[n] = p[0];
+                hi[n] = p[1];
+            }
         }
+#pragma unroll
+        for (int n = 0; n < KN; ++n) v[n] = split8(lo[n], hi[n], rest);
     };
     auto load_w = [&](int f, int32_t cur, int32_t c) {
         bf16x8 w = {};

@@ -612,31 +612,31 @@ typedef struct ep_lora_t {
  * u[r] = scale[d] A[d, e(r)] x[r] for every kept row (fp32 accumulation), zeros
  * for those without an adapter.
  *   x  bf16 [R, in_dim]
- *   u  4-byte words [R, rank]; row r holds the rank values rounded to bf16, then
- *      rank bf16 of what the rounding left: their sum has 16 significant bits.
+ *   u  float [R, rank]; the products take it as two bf16 a value (16 significant
+ *      bits), the adapters' gradients as three (24).
  */
 int ep_lora_down(const ep_cfg_t* cfg, const ep_layout_t* layout, const ep_lora_t* lora, int32_t in_dim,
-                 const uint16_t* x, void* u, void* stream);
+                 const uint16_t* x, float* u, void* stream);
 
 /* ep_expert_gemm with the adapters' part:
  *   y[r, n] = bf16_rne( sum_h x[r, h] w[e(r), n, h] + sum_p B[d, e(r), n, p] u[r, p] ) */
 int ep_expert_gemm_lora(const ep_cfg_t* cfg, const ep_layout_t* layout, const ep_lora_t* lora, int32_t in_dim,
-                        int32_t out_dim, const uint16_t* x, const uint16_t* w, const void* u, uint16_t* y, void* stream);
+                        int32_t out_dim, const uint16_t* x, const uint16_t* w, const float* u, uint16_t* y, void* stream);
 
 /* ep_expert_gemm_nvfp4 with the adapters' part (in bf16 beside the 4-bit weights). */
 int ep_expert_gemm_nvfp4_lora(const ep_cfg_t* cfg, const ep_layout_t* layout, const ep_lora_t* lora, int32_t in_dim,
                               int32_t out_dim, const uint16_t* x, const uint8_t* codes, const uint8_t* scales,
-                              const uint16_t* rowscale, const void* u, uint16_t* y, void* stream);
+                              const uint16_t* rowscale, const float* u, uint16_t* y, void* stream);
 
 /* grad_u[r] = scale[d] B[d, e(r)]^T grad_y[r], held as u is; zeros for rows
  * without an adapter. */
 int ep_lora_bwd_u(const ep_cfg_t* cfg, const ep_layout_t* layout, const ep_lora_t* lora, int32_t out_dim,
-                  const uint16_t* grad_y, void* grad_u, void* stream);
+                  const uint16_t* grad_y, float* grad_u, void* stream);
 
 /* ep_expert_gemm_bwd_x with the adapters' part:
  *   grad_x[r, h] = bf16_rne( sum_n grad_y[r, n] w[e(r), n, h] + sum_p A[d, e(r), p, h] grad_u[r, p] ) */
 int ep_expert_gemm_bwd_x_lora(const ep_cfg_t* cfg, const ep_layout_t* layout, const ep_lora_t* lora, int32_t in_dim,
-                              int32_t out_dim, const uint16_t* grad_y, const uint16_t* w, const void* grad_u,
+                              int32_t out_dim, const uint16_t* grad_y, const uint16_t* w, const float* grad_u,
                               uint16_t* grad_x, void* stream);
 
 /*
@@ -649,7 +649,7 @@ int ep_expert_gemm_bwd_x_lora(const ep_cfg_t* cfg, const ep_layout_t* layout, co
  * work-items: 2^24 tiles of 256 columns over all adapters and experts.
  */
 int ep_lora_bwd_w(const ep_cfg_t* cfg, const ep_layout_t* layout, const ep_lora_t* lora, int32_t in_dim,
-                  int32_t out_dim, const uint16_t* x, const uint16_t* grad_y, const void* u, const void* grad_u,
+                  int32_t out_dim, const uint16_t* x, const uint16_t* grad_y, const float* u, const float* grad_u,
                   void* grad_a, void* grad_b, int32_t grad_type, void* stream);
 
 /*
@@ -666,14 +666,14 @@ int ep_lora_bwd_w(const ep_cfg_t* cfg, const ep_layout_t* layout, const ep_lora_
  * row_offsets, seg_base and src_info of the layout.
  */
 int ep_expert_gated(const ep_cfg_t* cfg, const ep_layout_t* layout, const ep_lora_t* lora, int32_t in_dim, int32_t inter,
-                    const uint16_t* x, const uint16_t* w, const float* probs, const void* ulora, uint16_t* act,
+                    const uint16_t* x, const uint16_t* w, const float* probs, const float* ulora, uint16_t* act,
                     void* stream);
 
 /* The same over 4-bit weights, as in ep_expert_gemm_nvfp4 with out_dim 2*inter
  * (in_dim a multiple of 16, inter * in_dim < 2^34). */
 int ep_expert_gated_nvfp4(const ep_cfg_t* cfg, const ep_layout_t* layout, const ep_lora_t* lora, int32_t in_dim,
                           int32_t inter, const uint16_t* x, const uint8_t* codes, const uint8_t* scales,
-                          const uint16_t* rowscale, const float* probs, const void* ulora, uint16_t* act, void* stream);
+                          const uint16_t* rowscale, const float* probs, const float* ulora, uint16_t* act, void* stream);
 
 /* Columns of act whose share of grad_probs is one part of the workspace. */
 #define EP_GATED_PART 32
@@ -694,7 +694,7 @@ int ep_expert_gated_nvfp4(const ep_cfg_t* cfg, const ep_layout_t* layout, const 
  *              run at the same time.  Else NULL.
  */
 int ep_expert_gated_bwd(const ep_cfg_t* cfg, const ep_layout_t* layout, const ep_lora_t* lora, int32_t in_dim,
-                        int32_t inter, const uint16_t* x, const uint16_t* w, const float* probs, const void* ulora,
+                        int32_t inter, const uint16_t* x, const uint16_t* w, const float* probs, const float* ulora,
                         const uint16_t* grad_act, uint16_t* grad_h, uint16_t* act, float* grad_probs, void* workspace,
                         int64_t workspace_bytes, void* stream);
 
