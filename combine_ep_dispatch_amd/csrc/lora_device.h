@@ -85,21 +85,17 @@ __device__ __forceinline__ void add_adapters(const BlockArgs& a, int64_t first, 
         a, [&](int n) { return first + min(wn + n * 16 + i, rows - 1); }, [&](int n) { return wn + n * 16 + i < rows; }, ad);
     const int32_t chunks = uniform(a.l.rank / 4);  // of 8 values: the rounded ones, then the rests
     const float* const u = a.u + (first + wn + i) * a.l.rank;
-    auto load_u = [&](bf16x8 (&v)[KN], int32_t cur, int32_t c) {
-        const bool rest = c >= chunks / 2;
-        const int32_t at = (rest ? c - chunks / 2 : c) * 8;
-        f32x4 lo[KN], hi[KN];
+    auto load_u = [&](f32x4 (&v)[KN][2], int32_t cur, int32_t c) {
+        const int32_t at = (c >= chunks / 2 ? c - chunks / 2 : c) * 8;
 #pragma unroll
         for (int n = 0; n < KN; ++n) {
-            lo[n] = hi[n] = f32x4{};
+            v[n][0] = v[n][1] = f32x4{};
             if (c < chunks && ad[n] == cur) {
                 const f32x4* const p = reinterpret_cast<const f32x4*>(u + n * 16 * a.l.rank + at);
-                lo[n] = p[0];
-                hi[n] = p[1];
+                v[n][0] = p[0];
+                v[n][1] = p[1];
             }
         }
-#pragma unroll
-        for (int n = 0; n < KN; ++n) v[n] = split8(lo[n], hi[n], rest);
     };
     auto load_w = [&](int f, int32_t cur, int32_t c) {
         bf16x8 w = {};
@@ -113,7 +109,8 @@ __device__ __forceinline__ void add_adapters(const BlockArgs& a, int64_t first, 
         for (int n = 0; n < KN; ++n) in_agprs(acc[f][n]);
     for (int32_t cur = next_adapter(ad, -1); cur != kNoAdapter; cur = next_adapter(ad, cur)) {
         for (int32_t c0 = 0; c0 < chunks; c0 += 4) {
-            bf16x8 wv[KF], uv[KN];
+            bf16x8 wv[KF];
+            f32x4 uv[KN][2];
 #pragma unroll
             for (int f = 0; f < KF; ++f) wv[f] = load_w(f, cur, c0 + q);
             load_u(uv, cur, c0 + q);
@@ -125,12 +122,15 @@ __device__ __forceinline__ void add_adapters(const BlockArgs& a, int64_t first, 
                 continue;
             }
 #pragma unroll
-            for (int f = 0; f < KF; ++f)
+            for (int n = 0; n < KN; ++n) {
+                if (__builtin_amdgcn_ballot_w64(ad[n] == cur) == 0) continue;
+                const bf16x8 v = split8(uv[n][0], uv[n][1], c0 + q >= chunks / 2);
 #pragma unroll
-                for (int n = 0; n < KN; ++n) {
-                    acc[f][n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wv[f], uv[n], acc[f][n], 0, 0, 0);
+                for (int f = 0; f < KF; ++f) {
+                    acc[f][n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wv[f], v, acc[f][n], 0, 0, 0);
                     in_agprs(acc[f][n]);
                 }
+            }
         }
     }
     if (uniform(any_bad) == 0) return;
@@ -145,17 +145,20 @@ __device__ __forceinline__ void add_adapters(const BlockArgs& a, int64_t first, 
 #pragma unroll
                 for (int f = 0; f < KF; ++f) bad |= not_finite(load_w(f, cur, c0 + q));
                 if (__builtin_amdgcn_ballot_w64(bad) == 0) continue;
-                bf16x8 uv[KN], wv[kBlock];
+                bf16x8 wv[kBlock];
+                f32x4 uv[KN][2];
                 load_u(uv, cur, c0 + q);
 #pragma unroll
                 for (int f = 0; f < kBlock; ++f) wv[f] = load_w(f0 + f, cur, c0 + q);
 #pragma unroll
-                for (int f = 0; f < kBlock; ++f)
+                for (int n = 0; n < KN; ++n) {
+                    const bf16x8 v = split8(uv[n][0], uv[n][1], c0 + q >= chunks / 2);
 #pragma unroll
-                    for (int n = 0; n < KN; ++n) {
-                        const f32x4 s = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wv[f], uv[n], acc[f0 + f][n], 0, 0, 0);
+                    for (int f = 0; f < kBlock; ++f) {
+                        const f32x4 s = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wv[f], v, acc[f0 + f][n], 0, 0, 0);
                         acc[f0 + f][n] = ad[n] == cur ? s : acc[f0 + f][n];
                     }
+                }
             }
         }
         // done with: into accumulation registers, out of the next block's way
