@@ -249,15 +249,15 @@ class _LinearLora(torch.autograd.Function):
         y = torch.zeros(cfg.recv_rows, w.shape[1], dtype=torch.bfloat16, device=x.device)
         ep_lora_down(cfg, layout, x, adapters, u)
         ep_expert_gemm_lora(cfg, layout, x, w, y, adapters, u)
-        ctx.cfg, ctx.layout, ctx.rest = cfg, layout, (token_adapter, scale)
-        ctx.save_for_backward(x, w, a, b, u)
+        ctx.cfg, ctx.layout = cfg, layout
+        ctx.save_for_backward(x, w, a, b, u, token_adapter, scale)
         return y
 
     @staticmethod
     @_first_only
     def backward(ctx, grad_y):
-        x, w, a, b, u = ctx.saved_tensors
-        adapters = Adapters(ctx.rest[0], a, b, ctx.rest[1])
+        x, w, a, b, u, token_adapter, scale = ctx.saved_tensors
+        adapters = Adapters(token_adapter, a, b, scale)
         grads = _product_grads(ctx, _rows(grad_y.to(torch.bfloat16)), x, w, adapters, u, ctx.needs_input_grad)
         return (*grads, None, None, None, None)
 
@@ -271,16 +271,16 @@ class _Gated(torch.autograd.Function):
             ep_lora_down(cfg, layout, x, adapters, u)
         act = torch.zeros(cfg.recv_rows, w.shape[1] // 2, dtype=torch.bfloat16, device=x.device)
         ep_expert_gated(cfg, layout, x, w, probs, act, adapters, u)
-        ctx.cfg, ctx.layout, ctx.rest = cfg, layout, (token_adapter, scale)
-        ctx.save_for_backward(x, w, a, b, probs, u)
+        ctx.cfg, ctx.layout = cfg, layout
+        ctx.save_for_backward(x, w, a, b, probs, u, token_adapter, scale)
         return act
 
     @staticmethod
     @_first_only
     def backward(ctx, grad_act):
-        x, w, a, b, probs, u = ctx.saved_tensors
+        x, w, a, b, probs, u, token_adapter, scale = ctx.saved_tensors
         cfg, layout = ctx.cfg, ctx.layout
-        adapters = None if a is None else Adapters(ctx.rest[0], a, b, ctx.rest[1])
+        adapters = None if a is None else Adapters(token_adapter, a, b, scale)
         ga = _rows(grad_act.to(torch.bfloat16))
         gh = torch.zeros(cfg.recv_rows, w.shape[1], dtype=torch.bfloat16, device=x.device)
         gp = ws = None

@@ -587,6 +587,25 @@ def test_only_the_gradients_that_are_needed(G):  # noqa: F811
         gx.float().sum().backward()
 
 
+@pytest.mark.parametrize("which", ["of", "scale"])
+@pytest.mark.parametrize("gated", [False, True])
+def test_adapters_changed_before_the_backward_pass_are_refused(G, gated, which):  # noqa: F811
+    """The tokens' adapters or their scales written over between the passes: the gradients would not be the results'."""
+    from combine_ep_dispatch_amd.autograd import EpDispatcher
+
+    T, H, E, inter = 17, 64, 4, 16
+    cfg = G.epx.EpConfig(num_tokens=T, hidden=H, num_experts=E, num_segments=1, top_k=2, align=8)
+    d = EpDispatcher(cfg, "cuda:0")
+    ids = torch.argsort(normal(9, T, E, dtype=torch.float32), dim=1)[:, :2].int().contiguous()
+    l = lora_leaves(2, E, 8, H, 2 * inter, T, 30)
+    rows, w = d.dispatch(normal(1, T, H), ids), normal(3, E, 2 * inter, H, std=H ** -0.5)
+    adapters = G.epx.Adapters(l["of"], l["a"], l["b"], l["scale"])
+    y = d.gated(rows, w, None, adapters) if gated else d.linear(rows, w, adapters)
+    l[which].zero_()
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        y.float().sum().backward()
+
+
 def step_of(G, cfg, t, b):  # noqa: F811
     """A training step of the layer by the calls themselves, into the buffers b."""
     e, lay = G.epx, t["lay"]
