@@ -6,6 +6,19 @@
 //   grad_probs[t, k] = sum_i ga silu(g) u
 // g and u are not rounded between the product and the activation.  Low-rank
 // adapters, if any, add to g and u before it.
+//
+// Against the product and the activation apart, the rows' 2 I values of h are neither
+// written nor read.  The backward pass makes g and u again, which costs a product more
+// but keeps nothing of 2 I values a row from one pass to the next.
+//
+// 32 experts of 4096 x 7168 (2 I x in): 128 rows 311 us, bound by reading 1.88 GB of
+// weights (6.0 TB/s); 32 768 rows 1490 to 1540 us, 1250 to 1290 TFLOP/s, where one
+// library product of as many operations reaches 1590.  Of a tile's time 89 % are its
+// 112 steps, each 2290 cycles of which 2048 are matrix instructions; 3400 cycles find
+// the tile, 2000 wait for its first step, 14 500 are the epilogue.  The backward
+// epilogue takes 33 700: 64 experts of 2048 x 1416, 49 152 rows, forward and gradients
+// 1560 us with the two products behind it.  There rows of 2832 bytes straddle the
+// 128-byte lines of memory: 22 steps take 88 000 cycles instead of 55 700.
 #include "expert_loop.h"
 #include "gated_device.h"
 

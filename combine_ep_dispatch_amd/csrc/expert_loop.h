@@ -1,6 +1,14 @@
 // Tiles of 256 features by up to 256 rows whose product ends in an epilogue of
 // its own: the gated block and the products with adapters.  A workgroup of 4 waves
 // a CU takes tile after tile; the loads run on from one to the next.
+//
+// Full tiles are as large as registers and LDS hold: 64 KiB come through L2 for
+// 2 x 256 x 256 x 64 operations a step and CU.  A wave's 128 x 128 results fill its 256
+// accumulation registers.  LDS reads, loads and what advances them go one by one
+// between the matrix instructions.  32 experts of 4096 x 7168, 32 768 rows, us: loads
+// and reads ahead of each step's products 1745, between them 1650, a workgroup a CU
+// whose loads run on into the next tile 1496.  A step then takes 2290 cycles, 2048 of
+// them matrix instructions.
 #pragma once
 
 #include <type_traits>
