@@ -30,8 +30,8 @@ The expert layer around the two, on the same layout:
 d.gated(recv, w1, probs) is d.swiglu(d.linear(recv, w1), probs) in one kernel that
 keeps neither h nor act's inputs: its backward pass makes h again.  linear and gated
 take Adapters (low-rank, a token's own each) beside the weights, differentiable in
-rows, w, adapters.a and adapters.b (scale gets no gradient); weights that need no
-gradient cost none.
+rows, w, adapters.a and adapters.b (a scale that asks for a gradient is refused);
+weights that need no gradient cost none.
 
 A step can be captured into a graph, backward pass included, on leaves that no
 eager autograd graph still holds (torch does not support capturing beside one).
@@ -295,6 +295,8 @@ def _parts(adapters: Optional[Adapters]):
     """a, b, token_adapter and scale of adapters as the calls take them."""
     if adapters is None:
         return None, None, None, None
+    if adapters.scale is not None and adapters.scale.requires_grad and torch.is_grad_enabled():
+        raise ValueError("adapters.scale gets no gradient: detach it")
     return (_rows(adapters.a), _rows(adapters.b), adapters.token_adapter.to(torch.int32).contiguous(),
             None if adapters.scale is None else adapters.scale.detach().float().contiguous())
 

@@ -121,3 +121,14 @@ def test_binding_refuses_host_tensors_and_wrong_shapes():
         epx._lora(c, None, u, 64, 64, None)
     with pytest.raises(ValueError, match="grad_a"):
         epx.ep_lora_bwd_w(c, None, rows, rows, epx.Adapters(ids, a, b), u, u, a.half(), b.half())
+
+
+def test_dispatcher_refuses_a_scale_that_asks_for_a_gradient():
+    from combine_ep_dispatch_amd.autograd import _parts
+
+    a, b = torch.zeros(4, 8, 16, 64, dtype=torch.bfloat16), torch.zeros(4, 8, 64, 16, dtype=torch.bfloat16)
+    adapters = epx.Adapters(torch.zeros(16, dtype=torch.int32), a, b, torch.ones(4, requires_grad=True))
+    with pytest.raises(ValueError, match="scale gets no gradient"):
+        _parts(adapters)
+    with torch.no_grad():
+        assert not _parts(adapters)[3].requires_grad
