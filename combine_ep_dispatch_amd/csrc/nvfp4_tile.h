@@ -81,6 +81,8 @@ struct Nvfp4Tile {
         const int64_t row0 = (int64_t)t.expert * a.on + f0;
         const int32_t frows = uniform(max(min(kPart, features - f0), 0));  // 0: this wave only helps with the rows
         const int32_t cpitch = in / 2, spitch = in / 16;
+        // gated: the scales of the wave's rows of both projections lie apart; of no rows, nothing may be read
+        const int32_t srows = uniform(GATED && frows > 0 ? features + frows : frows);
         const uint8_t* const codes = a.codes + row0 * cpitch;
         const uint8_t* const scales = a.scales + row0 * spitch;
         const uint16_t* const x = a.x + t.first * in;
@@ -121,7 +123,7 @@ struct Nvfp4Tile {
                 load_to_lds<16>(GATED && j == 1 ? codes + (int64_t)features * cpitch : codes, frows * cpitch,
                                 to + w * (FW * kCodeRow) + j * 1024, on ? off[j] + l0 / 2 : kOutside);
             else if (j < 2 + kScaleLoads)
-                load_to_lds<WORDS ? 4 : 1>(scales, (GATED ? features + frows : frows) * spitch,
+                load_to_lds<WORDS ? 4 : 1>(scales, srows * spitch,
                                            to + kCodes + w * kScaleBytes + (j - 2) * 256,
                                            on ? off[j] + l0 / 16 : kOutside);
             else
