@@ -462,8 +462,10 @@ __device__ __forceinline__ void run_kind(const ExpertArgs& a, const LoopTiles& t
         t = next;
         if (t.expert < 0) break;
     }
-    // No load may land in LDS that belongs to the next kind, or another workgroup, by then.
+    // No load of any wave may land in LDS that belongs to the next kind, or another workgroup,
+    // by then: those of the tile that is not there write zeros behind the last step's barrier.
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    lds_barrier();
 }
 
 // All tiles of this workgroup.

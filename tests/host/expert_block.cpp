@@ -130,6 +130,7 @@ const std::vector<std::vector<int32_t>> kLayouts = {
     {57, 0, 40, 33},            // up to 64
     {130, 20, 100},             // every kind of tile but the tallest
     {0, 300, 1, 200, 128, 33},  // all kinds
+    {1060, 20, 900, 100},       // full tiles and what is left over, tiles of one height
 };
 
 std::string name(const char* kernel, const std::vector<int32_t>& rows, int32_t in, int32_t out, int32_t rank) {

@@ -11,7 +11,7 @@ import pytest
 from combine_ep_dispatch_amd import build
 
 HERE = os.path.join(os.path.dirname(os.path.abspath(__file__)), "host")
-SOURCES = {"expert_nvfp4_block": 2}  # name, number in expert_block.cpp
+SOURCES = {"expert_gated": 0, "expert_lora": 1, "expert_nvfp4_block": 2}  # name, number in expert_block.cpp
 HEADERS = ("epx_device", "expert_device", "expert_tile", "expert_loop", "lora_device", "gated_device", "nvfp4_tile")
 
 # What the inline assembly does, in the host's words.
@@ -69,6 +69,12 @@ def run(program, ins, outs):
     said = [r.communicate()[0] for r in runs]
     for r, text in zip(runs, said):
         assert r.returncode == 0 and re.fullmatch(r"\d+ cases\n", text), text
+
+
+@pytest.mark.parametrize("name", ["expert_gated", "expert_lora"])
+def test_products(programs, name):
+    """Workgroups that go from tile to tile and from one kind of tiles to the next."""
+    run(programs[name], (8, 136, 264, 328), (8, 136))
 
 
 def test_four_bit_products(programs):
