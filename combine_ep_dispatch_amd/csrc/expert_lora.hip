@@ -244,7 +244,8 @@ constexpr int kLook = 4, kList = kLook * kGradThreads;               // rows tha
 // 32 experts, 4 adapters of rank 16, 32 768 rows of 2048: 44 to 46 us, bound by the
 // rows' reads (134 MB, 3.0 TB/s; 88 us with a step's loads behind the one before).
 template <int KP, bool OUT>
-__global__ __launch_bounds__(kGradThreads) void k_lora_bwd_w(BlockArgs a, const float* v, void* out, int32_t ctiles) {
+__global__ __launch_bounds__(kGradThreads, KP <= 2 ? 3 : KP == 4 ? 2 : 1)  // as many workgroups as LDS holds
+void k_lora_bwd_w(BlockArgs a, const float* v, void* out, int32_t ctiles) {
     using XOp = ColsOperand<kGradCols, 4>;
     // v as three bf16 whose sum it is (24 significant bits): the sums over the rows are
     // as good as 32-bit products' would be
@@ -259,102 +260,126 @@ __global__ __launch_bounds__(kGradThreads) void k_lora_bwd_w(BlockArgs a, const 
     const GroupRows rows = group_rows(a.e, g);
     const uint16_t* const d = (OUT ? a.e.gy : a.e.x) + rows.first * C + c0;
     const float* const vv = v + rows.first * rank;
-    f32x4 acc[4][KP] = {};
-    int32_t have = 0;  // rows in the list
+    f32x4 acc[4][KP];
     constexpr int kX = kGradRows * kGradCols / 8 / kGradThreads;  // 16-byte pieces of d that a thread copies a step
-    for (int32_t r0 = 0; r0 < rows.rows || have > 0; r0 += kList) {
-        // append the next rows' matches
-        int32_t of[kLook];
-        row_adapters<kLook>(
-            a, [&](int k) { return rows.first + min(r0 + k * kGradThreads + (int32_t)threadIdx.x, rows.rows - 1); },
-            [&](int k) { return r0 + k * kGradThreads + (int32_t)threadIdx.x < rows.rows; }, of);
+    auto sums = [&](auto again) {
+        constexpr bool kAgain = decltype(again)::value;
 #pragma unroll
-        for (int k = 0; k < kLook; ++k) {
-            const bool mine = of[k] == ad;
-            const uint64_t m = __builtin_amdgcn_ballot_w64(mine);
-            if (lane == 0) counts[w] = __popcll(m);
-            __syncthreads();
-            int32_t at = have;
-            for (int o = 0; o < 4; ++o) {
-                if (o == w && mine) list[at + lanes_below(m)] = r0 + k * kGradThreads + (int32_t)threadIdx.x;
-                at += counts[o];
+        for (int f = 0; f < 4; ++f)
+#pragma unroll
+            for (int k = 0; k < KP; ++k) acc[f][k] = f32x4{};
+        int32_t have = 0;  // rows in the list
+        for (int32_t r0 = 0; r0 < rows.rows || have > 0; r0 += kList) {
+            // append the next rows' matches
+            int32_t of[kLook];
+            row_adapters<kLook>(
+                a, [&](int k) { return rows.first + min(r0 + k * kGradThreads + (int32_t)threadIdx.x, rows.rows - 1); },
+                [&](int k) { return r0 + k * kGradThreads + (int32_t)threadIdx.x < rows.rows; }, of);
+#pragma unroll
+            for (int k = 0; k < kLook; ++k) {
+                const bool mine = of[k] == ad;
+                const uint64_t m = __builtin_amdgcn_ballot_w64(mine);
+                if (lane == 0) counts[w] = __popcll(m);
+                __syncthreads();
+                int32_t at = have;
+                for (int o = 0; o < 4; ++o) {
+                    if (o == w && mine) list[at + lanes_below(m)] = r0 + k * kGradThreads + (int32_t)threadIdx.x;
+                    at += counts[o];
+                }
+                have = at;
+                __syncthreads();
             }
-            have = at;
-            __syncthreads();
-        }
-        const bool last = r0 + kList >= rows.rows;
-        const int32_t turns = last ? (have + kGradRows - 1) / kGradRows : have / kGradRows, done = turns * kGradRows;
-        // a step's rows on their way to LDS, while the step before is multiplied
-        v4u xr[kX];
-        f32x4 vr[KP];
-        auto fetch = [&](int32_t turn) {
-            const int32_t from = turn * kGradRows, n = min(kGradRows, have - from);
-            // d: 64 rows of 32 chunks of 8 values
+            const bool last = r0 + kList >= rows.rows;
+            const int32_t turns = last ? (have + kGradRows - 1) / kGradRows : have / kGradRows, done = turns * kGradRows;
+            // a step's rows on their way to LDS, while the step before is multiplied
+            v4u xr[kX];
+            f32x4 vr[KP];
+            auto fetch = [&](int32_t turn) {
+                const int32_t from = turn * kGradRows, n = min(kGradRows, have - from);
+                // d: 64 rows of 32 chunks of 8 values
 #pragma unroll
-            for (int k = 0; k < kX; ++k) {
-                const int at = k * kGradThreads + threadIdx.x, r = at / 32, c = at % 32;
-                xr[k] = v4u{};
-                if (r < n && c0 + c * 8 < C) xr[k] = *reinterpret_cast<const v4u*>(d + (int64_t)list[from + r] * C + c * 8);
-            }
-            // v: 64 rows of KP * 4 chunks of 4 values
+                for (int k = 0; k < kX; ++k) {
+                    const int at = k * kGradThreads + threadIdx.x, r = at / 32, c = at % 32;
+                    xr[k] = v4u{};
+                    if (r < n && c0 + c * 8 < C) xr[k] = *reinterpret_cast<const v4u*>(d + (int64_t)list[from + r] * C + c * 8);
+                }
+                // v: 64 rows of KP * 4 chunks of 4 values
 #pragma unroll
-            for (int k = 0; k < KP; ++k) {
-                const int at = k * kGradThreads + threadIdx.x, r = at / (KP * 4), p = at % (KP * 4) * 4;
-                vr[k] = f32x4{};
-                if (r < n && p < rank) vr[k] = *reinterpret_cast<const f32x4*>(vv + (int64_t)list[from + r] * rank + p);
-            }
-        };
-        if (turns > 0) fetch(0);
-        for (int32_t turn = 0; turn < turns; ++turn) {
+                for (int k = 0; k < KP; ++k) {
+                    const int at = k * kGradThreads + threadIdx.x, r = at / (KP * 4), p = at % (KP * 4) * 4;
+                    vr[k] = f32x4{};
+                    if (r < n && p < rank) vr[k] = *reinterpret_cast<const f32x4*>(vv + (int64_t)list[from + r] * rank + p);
+                }
+            };
+            if (turns > 0) fetch(0);
+            for (int32_t turn = 0; turn < turns; ++turn) {
 #pragma unroll
-            for (int k = 0; k < kX; ++k) {
-                const int at = k * kGradThreads + threadIdx.x, r = at / 32, c = at % 32;
-                *reinterpret_cast<v4u*>(xs + r * kGradCols + (((c / 2) ^ XOp::swizzle(r)) * 2 + c % 2) * 8) = xr[k];
-            }
+                for (int k = 0; k < kX; ++k) {
+                    const int at = k * kGradThreads + threadIdx.x, r = at / 32, c = at % 32;
+                    *reinterpret_cast<v4u*>(xs + r * kGradCols + (((c / 2) ^ XOp::swizzle(r)) * 2 + c % 2) * 8) = xr[k];
+                }
 #pragma unroll
-            for (int k = 0; k < KP; ++k) {
-                const int at = k * kGradThreads + threadIdx.x, r = at / (KP * 4), c = at % (KP * 4);
-                f32x4 left = vr[k];
+                for (int k = 0; k < KP; ++k) {
+                    const int at = k * kGradThreads + threadIdx.x, r = at / (KP * 4), c = at % (KP * 4);
+                    f32x4 left = vr[k];
 #pragma unroll
-                for (int o = 0; o < kParts; ++o) {
-                    const v2u w = {pack_bf16x2(left[0], left[1]), pack_bf16x2(left[2], left[3])};
-                    *reinterpret_cast<v2u*>(vs[o] + r * P + ((c / 4) ^ VOp::swizzle(r)) * 16 + c % 4 * 4) = w;
+                    for (int o = 0; o < kParts; ++o) {
+                        const v2u w = {pack_bf16x2(left[0], left[1]), pack_bf16x2(left[2], left[3])};
+                        *reinterpret_cast<v2u*>(vs[o] + r * P + ((c / 4) ^ VOp::swizzle(r)) * 16 + c % 4 * 4) = w;
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const float h = j % 2 ? bf16_hi(w[j / 2]) : bf16_lo(w[j / 2]);
-                        left[j] = __builtin_isinf(h) ? 0.0f : left[j] - h;  // an infinity leaves nothing
+                        for (int j = 0; j < 4; ++j) {
+                            const float h = j % 2 ? bf16_hi(w[j / 2]) : bf16_lo(w[j / 2]);
+                            left[j] = __builtin_isinf(h) ? 0.0f : left[j] - h;  // an infinity leaves nothing
+                        }
                     }
                 }
-            }
-            lds_barrier();
-            if (turn + 1 < turns) fetch(turn + 1);
+                lds_barrier();
+                if (turn + 1 < turns) fetch(turn + 1);
 #pragma unroll
-            for (int kk = 0; kk < 2; ++kk) {
-                bf16x8 xf[4];
+                for (int kk = 0; kk < 2; ++kk) {
+                    bf16x8 xf[4];
 #pragma unroll
-                for (int f = 0; f < 4; ++f) xf[f] = XOp::fragment(xs, w * 64 + f * 16, kk);
+                    for (int f = 0; f < 4; ++f) xf[f] = XOp::fragment(xs, w * 64 + f * 16, kk);
 #pragma unroll
-                for (int k = 0; k < kParts * KP; ++k) {
-                    const bf16x8 vf = VOp::fragment(vs[k / KP], k % KP * 16, kk);
+                    for (int k = 0; k < kParts * KP; ++k) {
+                        const bf16x8 vf = VOp::fragment(vs[k / KP], k % KP * 16, kk);
 #pragma unroll
-                    for (int f = 0; f < 4; ++f) {
-                        f32x4& s = acc[f][k % KP];
-                        s = OUT ? __builtin_amdgcn_mfma_f32_16x16x32_bf16(vf, xf[f], s, 0, 0, 0)
-                                : __builtin_amdgcn_mfma_f32_16x16x32_bf16(xf[f], vf, s, 0, 0, 0);
+                        for (int f = 0; f < 4; ++f) {
+                            if (kAgain && k == KP) xf[f] = only_finite(xf[f]);
+                            f32x4& s = acc[f][k % KP];
+                            s = OUT ? __builtin_amdgcn_mfma_f32_16x16x32_bf16(vf, xf[f], s, 0, 0, 0)
+                                    : __builtin_amdgcn_mfma_f32_16x16x32_bf16(xf[f], vf, s, 0, 0, 0);
+                        }
                     }
                 }
+                lds_barrier();
             }
-            lds_barrier();
+            // what is left of the list moves to its front
+            const int32_t left = max(have - done, 0);
+            int32_t keep = 0;
+            if ((int32_t)threadIdx.x < left) keep = list[done + threadIdx.x];
+            __syncthreads();
+            if ((int32_t)threadIdx.x < left) list[threadIdx.x] = keep;
+            have = left;
+            __syncthreads();
         }
-        // what is left of the list moves to its front
-        const int32_t left = max(have - done, 0);
-        int32_t keep = 0;
-        if ((int32_t)threadIdx.x < left) keep = list[done + threadIdx.x];
-        __syncthreads();
-        if ((int32_t)threadIdx.x < left) list[threadIdx.x] = keep;
-        have = left;
-        __syncthreads();
-    }
+    };
+    sums(std::false_type{});
+    // Where a sum is NaN all are made once more, with the infinities of d times the first part
+    // of v alone: times the other two they may be NaN where the sum is infinite.
+    bool nan = false;
+#pragma unroll
+    for (int f = 0; f < 4; ++f)
+#pragma unroll
+        for (int k = 0; k < KP; ++k)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) nan |= acc[f][k][j] != acc[f][k][j];
+    const uint64_t any = __builtin_amdgcn_ballot_w64(nan);
+    if (lane == 0) counts[w] = any != 0;
+    __syncthreads();
+    const bool again = uniform(counts[0] | counts[1] | counts[2] | counts[3]) != 0;
+    __syncthreads();
+    if (again) sums(std::true_type{});
     // acc[f][k][j]: column c = c0 + 64 w + 16 f + .., value p = 16 k + .. of the rank;
     // the four of a lane lie along the result's rows
 #pragma unroll

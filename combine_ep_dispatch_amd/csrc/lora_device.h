@@ -66,6 +66,19 @@ __device__ __forceinline__ bool not_finite(const bf16x8 v) {
     return (carry & 0x80008000u) != 0;
 }
 
+// v with zeros in place of infinities and NaN.  Where a value goes into products in parts,
+// the others than the first meet only finite factors: an infinity times the first part
+// is infinite already, and times a rest of 0, or of the other sign, it would make that NaN.
+__device__ __forceinline__ bf16x8 only_finite(const bf16x8 v) {
+    v4u w = __builtin_bit_cast(v4u, v);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const uint32_t carry = (w[j] & 0x7F807F80u) + 0x00800080u;
+        w[j] &= ~((carry >> 15 & 0x00010001u) * 0xFFFFu);
+    }
+    return __builtin_bit_cast(bf16x8, w);
+}
+
 // acc[f][n] += the adapters' part of a wave's results: 16 features a fragment f
 // by 16 rows a fragment n, summed over u rounded to bf16 and then over what the
 // rounding left (2 rank values), 32 of them a step.  weights(f, ad, c): this lane's 8
@@ -73,7 +86,7 @@ __device__ __forceinline__ bool not_finite(const bf16x8 v) {
 // one of the rows has is multiplied with all of them, with u zero in the rows of
 // others.  Steps whose weights hold an infinity or NaN come afterwards, and are added
 // to the adapter's own rows alone: nothing that an adapter or another row holds
-// reaches a row that does not use it.  Bound by the loads' latency, some 0.8 us for each
+// reaches a row that does not use it.  There what the rounding left meets no infinity.  Bound by the loads' latency, some 0.8 us for each
 // adapter and step of a tile; loads a step ahead gained nothing.  (Selecting in every step moves all results
 // from accumulation to vector registers and back: 32 experts of 4096 x 7168, 4096
 // tokens of 8, rank 32, 2010 us.)
@@ -150,7 +163,10 @@ __device__ __forceinline__ void add_adapters(const BlockArgs& a, int64_t first, 
                 f32x4 uv[KN][2];
                 load_u(uv, cur, c0 + q);
 #pragma unroll
-                for (int f = 0; f < kBlock; ++f) wv[f] = load_w(f0 + f, cur, c0 + q);
+                for (int f = 0; f < kBlock; ++f) {
+                    wv[f] = load_w(f0 + f, cur, c0 + q);
+                    if (c0 + q >= chunks / 2) wv[f] = only_finite(wv[f]);
+                }
 #pragma unroll
                 for (int n = 0; n < KN; ++n) {
                     const bf16x8 v = split8(uv[n][0], uv[n][1], c0 + q >= chunks / 2);

@@ -613,7 +613,8 @@ typedef struct ep_lora_t {
  * for those without an adapter.
  *   x  bf16 [R, in_dim]
  *   u  float [R, rank]; the products take it as two bf16 a value (16 significant
- *      bits), the adapters' gradients as three (24).
+ *      bits), the adapters' gradients as three (24).  An infinity times u is one of
+ *      that sign all the same (NaN where u is 0, or below half of bf16's smallest).
  */
 int ep_lora_down(const ep_cfg_t* cfg, const ep_layout_t* layout, const ep_lora_t* lora, int32_t in_dim,
                  const uint16_t* x, float* u, void* stream);

@@ -35,6 +35,13 @@ uint16_t* values(size_t n) {
     return p;
 }
 
+// Values of which some are infinite.
+uint16_t* wild_values(size_t n) {
+    uint16_t* const p = values(n);
+    for (size_t k = random_bits() % 97; k < n; k += 97) p[k] = 0x7F80;
+    return p;
+}
+
 uint8_t* bytes(size_t n) {
     uint8_t* const p = array<uint8_t>(n);
     for (size_t k = 0; k < n; ++k) p[k] = (uint8_t)(random_bits() >> 3);
@@ -149,7 +156,7 @@ void one(const std::vector<int32_t>& rows, bool shared, int32_t in, int32_t out,
     a.e.x = values(l.R() * in);
     a.e.w = values(l.experts() * 2 * out * in);
     if (rank > 0) {
-        a.l.b = values(l.experts() * adapters * 2 * out * rank);
+        a.l.b = (rank == 40 ? wild_values : values)(l.experts() * adapters * 2 * out * rank);
         a.u = floats(l.R() * rank);
     }
     a.probs = floats(l.R());
@@ -171,8 +178,8 @@ void one(const std::vector<int32_t>& rows, bool shared, int32_t in, int32_t out,
     a.e.x = values(l.R() * in);
     a.e.gy = values(l.R() * out);
     a.e.w = values(l.experts() * out * in);
-    a.l.a = values(l.experts() * adapters * rank * in);
-    a.l.b = values(l.experts() * adapters * out * rank);
+    a.l.a = (rank == 40 ? wild_values : values)(l.experts() * adapters * rank * in);
+    a.l.b = (rank == 40 ? wild_values : values)(l.experts() * adapters * out * rank);
     float *const u = array<float>(l.R() * rank), *const gu = array<float>(l.R() * rank);
     const size_t u_bytes = (size_t)l.R() * rank * 4;
     host::what = name("lora_down", rows, in, out, rank);
@@ -214,7 +221,7 @@ void one(const std::vector<int32_t>& rows, bool shared, int32_t in, int32_t out,
         a.e.scales = bytes(l.experts() * on * in / 16);
         a.e.rowscale = values(l.experts() * on);
         if (rank > 0) {
-            a.l.b = values(l.experts() * adapters * on * rank);
+            a.l.b = (rank == 40 ? wild_values : values)(l.experts() * adapters * on * rank);
             a.u = floats(l.R() * rank);
         }
         a.probs = floats(l.R());

@@ -1,0 +1,117 @@
+"""The gated block and the products with adapters on the GPU where they are least
+ordinary: infinite adapters and rows."""
+
+import pytest
+import torch
+
+from test_gpu_expert_block import Lora, words
+from test_gpu_expert_layer import G, Rows, filled, normal, nvfp4_weights  # noqa: F401
+
+pytestmark = pytest.mark.gpu
+
+INF = float("inf")
+
+
+def half_rounded(seed, *shape):
+    """fp32 values of which every other one is a bf16 too: nothing is left of it by the rounding."""
+    t = normal(seed, *shape, dtype=torch.float32)
+    t.view(-1)[::2] = t.view(-1)[::2].to(torch.bfloat16).float()
+    assert (t != 0).all()
+    return t
+
+
+def same_kinds(got, want, what):
+    """The same infinities, signs included, and NaN in the same places."""
+    got, want = got.double().cpu(), want.cpu()
+    assert torch.isinf(want).any() and torch.isfinite(want).any()
+    for v in (INF, -INF):
+        assert torch.equal(got == v, want == v), what
+    assert torch.equal(got.isnan(), want.isnan()), what
+
+
+def with_adapters(d, lora, base, u, weights):
+    """base + the adapters' part of the kept rows, term by term (infinities as they are)."""
+    out = base.clone()
+    for e in range(d.experts):
+        on = (d.expert == e).nonzero().view(-1)
+        for k, some in lora.each(on):
+            rows = d.rows[on][some]
+            out[rows] += (weights(k, e)[None] * u[rows][:, None]).sum(2)
+    return out
+
+
+@pytest.mark.parametrize("name", ["odd", "tall"])
+@pytest.mark.parametrize("rank", [8, 40])
+def test_infinite_adapters_make_infinite_results(G, name, rank):  # noqa: F811
+    """An infinity in an adapter times u is an infinity of that sign, whatever the
+    rounding of u leaves of it, and two that cancel are NaN."""
+    d = Rows(G, name)
+    n_in, inter = 64, 72
+    x, gy = normal(1, d.R, n_in), normal(2, d.R, 2 * inter)
+    w = normal(3, d.experts, 2 * inter, n_in, std=n_in ** -0.5)
+    q, wq, rs = nvfp4_weights(5, d.experts, 2 * inter, n_in)
+    lora, u = Lora(G, d, rank, n_in, 2 * inter), half_rounded(9, d.R, rank)
+    lora.b[1, :, inter::3, 5] = INF  # of the up projection
+    lora.b[1, :, inter + 1::3, 2] = -INF
+    lora.b[0, :, inter + 2::9, 1:3] = INF
+    lora.a[1, :, 4, ::3] = -INF
+    lora.a[2, :, :2, 1::5] = INF
+    y, yq, gx, act, actq = (filled(d.R, n) for n in (2 * inter, 2 * inter, n_in, inter, inter))
+    G.epx.ep_expert_gemm_lora(d.cfg, d.lay, x, w, y, lora.c, u)
+    G.epx.ep_expert_gemm_nvfp4_lora(d.cfg, d.lay, x, *q, yq, lora.c, u)
+    G.epx.ep_expert_gemm_bwd_x_lora(d.cfg, d.lay, gy, w, gx, lora.c, u)
+    G.epx.ep_expert_gated(d.cfg, d.lay, x, w, None, act, lora.c, u)
+    G.epx.ep_expert_gated_nvfp4(d.cfg, d.lay, x, *q, None, actq, lora.c, u)
+    r, uc, xc, gc, wc = d.rows, u.double().cpu(), x.double().cpu(), gy.double().cpu(), w.double().cpu()
+
+    def product(t, m):
+        out = torch.zeros(d.R, m.shape[1], dtype=torch.float64)
+        for e in range(d.experts):
+            rows = r[d.expert == e]
+            out[rows] = t[rows] @ m[e].T
+        return out
+
+    b, a = (lambda k, e: lora.b[k, e].double().cpu()), (lambda k, e: lora.a[k, e].double().cpu().T)
+    h = with_adapters(d, lora, product(xc, wc), uc, b)
+    hq = with_adapters(d, lora, product(xc, wq * rs[:, :, None]), uc, b)
+    same_kinds(y.cpu()[r], h[r], "y")
+    same_kinds(yq.cpu()[r], hq[r], "y, 4-bit")
+    same_kinds(gx.cpu()[r], with_adapters(d, lora, product(gc, wc.transpose(1, 2)), uc, a)[r], "grad_x")
+    for got, v, what in ((act, h, "act"), (actq, hq, "act, 4-bit")):
+        # below g = -86 the sigmoid nears 2^-126 (exp(86) = 2^124.1; g itself is off by less than 1),
+        # where 32 bits have 0, and 0 times an infinity is NaN: those are not looked at
+        g, up = v[r].split(inter, 1)
+        seen = g >= -86
+        same_kinds(got.cpu()[r][seen], (torch.nn.functional.silu(g) * up)[seen], what)
+
+
+@pytest.mark.parametrize("name", ["odd", "tall"])
+@pytest.mark.parametrize("rank", [8, 24, 128])
+def test_infinite_rows_make_infinite_gradients(G, name, rank):  # noqa: F811
+    """The adapters' gradients over rows with infinities: those, of the sign of what
+    they are multiplied with, and NaN where both signs meet."""
+    d = Rows(G, name)
+    n_in, n_out = 264, 72
+    x, gy = normal(1, d.R, n_in), normal(2, d.R, n_out)
+    lora, u, gu = Lora(G, d, rank, n_in, n_out), half_rounded(8, d.R, rank), half_rounded(9, d.R, rank)
+    first = torch.cat([d.rows[on[some]][:1] for e in range(d.experts) for on in [(d.expert == e).nonzero().view(-1)]
+                       for _, some in lora.each(on)]).cuda()
+    x[first, 3], x[first, 260], gy[first, 7] = INF, -INF, -INF
+    x[d.rows.cuda()[::5], 100] = INF  # some of both signs meet
+    grads = []
+    for dtype in (torch.bfloat16, torch.float32):
+        ga, gb = (torch.full(t.shape, float("nan"), dtype=dtype, device="cuda:0") for t in (lora.a, lora.b))
+        G.epx.ep_lora_bwd_w(d.cfg, d.lay, x, gy, lora.c, u, gu, ga, gb)
+        grads.append((ga, gb))
+    xc, gc, uc, vc = x.double().cpu(), gy.double().cpu(), u.double().cpu(), gu.double().cpu()
+    wa, wb = (torch.zeros(t.shape, dtype=torch.float64) for t in (lora.a, lora.b))
+    for e in range(d.experts):
+        on = (d.expert == e).nonzero().view(-1)
+        for k, some in lora.each(on):
+            rows = d.rows[on[some]]
+            for row in rows:
+                wa[k, e] += vc[row][:, None] * xc[row][None]
+                wb[k, e] += gc[row][:, None] * uc[row][None]
+    for ga, gb in grads:
+        same_kinds(ga, wa, "grad_a")
+        same_kinds(gb, wb, "grad_b")
