@@ -1007,8 +1007,9 @@ int ep_lora_bwd_w(const ep_cfg_t* cfg, const ep_layout_t* layout, const ep_lora_
         bad_buffer(u, d.R * lora->rank * 4, 16) || bad_buffer(grad_u, d.R * lora->rank * 4, 16) ||
         bad_buffer(grad_a, 16, 16) || bad_buffer(grad_b, 16, 16))
         return EP_EINVAL;
-    if ((rc = check_device()) != EP_OK) return rc;
     BlockArgs a = block_args(d, layout, lora, in_dim, out_dim, u, nullptr);
+    if ((rc = expert_status(check_lora_bwd_w(a))) != EP_OK) return rc;
+    if ((rc = check_device()) != EP_OK) return rc;
     a.e.x = x;
     a.e.gy = grad_y;
     a.e.grad_type = grad_type;

@@ -452,7 +452,9 @@ hipError_t launch_gemm_bwd_x_lora(const BlockArgs& a, hipStream_t stream);
 // u [R, rank] = scale A x (ep_lora_down), or scale B^T grad_y (ep_lora_bwd_u; e.gy).
 hipError_t launch_lora_down(const BlockArgs& a, float* u, hipStream_t stream);
 hipError_t launch_lora_bwd_u(const BlockArgs& a, float* grad_u, hipStream_t stream);
-// The adapters' gradients, of e.grad_type, from e.x, e.gy, a.u and grad_u.
+// The adapters' gradients, of e.grad_type, from e.x, e.gy, a.u and grad_u: two launches,
+// whose grids are checked before the first.
+hipError_t check_lora_bwd_w(const BlockArgs& a);
 hipError_t launch_lora_bwd_w(const BlockArgs& a, const float* grad_u, void* grad_a, void* grad_b, hipStream_t stream);
 
 // Zero the payload bytes of every pad row ([count, align_up(count)) of each

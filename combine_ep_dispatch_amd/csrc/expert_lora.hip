@@ -399,11 +399,15 @@ void k_lora_bwd_w(BlockArgs a, const float* v, void* out, int32_t ctiles) {
         }
 }
 
+int32_t grad_tiles(int32_t columns) { return (columns + kGradCols - 1) / kGradCols; }
+int64_t grad_blocks(const BlockArgs& a, int32_t columns) {
+    return (int64_t)a.l.n * (a.e.E + a.e.shared) * grad_tiles(columns);
+}
+
 template <int KP, bool OUT>
 hipError_t bwd_w(const BlockArgs& a, const float* v, void* out, hipStream_t stream) {
-    const int32_t ctiles = ((OUT ? a.e.on : a.e.in) + kGradCols - 1) / kGradCols;
-    const int64_t blocks = (int64_t)a.l.n * (a.e.E + a.e.shared) * ctiles;
-    if (const hipError_t e = check_grid(blocks, kGradThreads)) return e;
+    const int32_t ctiles = grad_tiles(OUT ? a.e.on : a.e.in);
+    const int64_t blocks = grad_blocks(a, OUT ? a.e.on : a.e.in);
     hipLaunchKernelGGL((k_lora_bwd_w<KP, OUT>), dim3((unsigned)blocks), dim3(kGradThreads), 0, stream, a, v, out,
                        ctiles);
     return hipGetLastError();
@@ -423,6 +427,10 @@ hipError_t launch_gemm_lora(const BlockArgs& a, hipStream_t stream) { return pro
 hipError_t launch_gemm_bwd_x_lora(const BlockArgs& a, hipStream_t stream) { return product<kInputGrad>(a, stream); }
 hipError_t launch_lora_down(const BlockArgs& a, float* u, hipStream_t stream) { return down_by_size<false>(a, u, stream); }
 hipError_t launch_lora_bwd_u(const BlockArgs& a, float* u, hipStream_t stream) { return down_by_size<true>(a, u, stream); }
+hipError_t check_lora_bwd_w(const BlockArgs& a) {
+    const hipError_t e = check_grid(grad_blocks(a, a.e.in), kGradThreads);
+    return e != hipSuccess ? e : check_grid(grad_blocks(a, a.e.on), kGradThreads);
+}
 hipError_t launch_lora_bwd_w(const BlockArgs& a, const float* grad_u, void* grad_a, void* grad_b, hipStream_t stream) {
     if (const hipError_t e = bwd_w_by_rank<false>(a, grad_u, grad_a, stream)) return e;
     return bwd_w_by_rank<true>(a, a.u, grad_b, stream);

@@ -647,7 +647,8 @@ int ep_expert_gemm_bwd_x_lora(const ep_cfg_t* cfg, const ep_layout_t* layout, co
  * both of grad_type (EP_GRAD_*: bf16, float, float added to), zeros where no row
  * is.  Sums in row order: results repeat bit for bit.  (scale is part of u and
  * grad_u; a and b of lora are not read.)  Returns EP_EINVAL past one grid of 2^32
- * work-items: 2^24 tiles of 256 columns over all adapters and experts.
+ * work-items, 2^24 tiles of 256 columns of either over all adapters and experts; neither
+ * is written then.
  */
 int ep_lora_bwd_w(const ep_cfg_t* cfg, const ep_layout_t* layout, const ep_lora_t* lora, int32_t in_dim,
                   int32_t out_dim, const uint16_t* x, const uint16_t* grad_y, const float* u, const float* grad_u,

@@ -98,6 +98,15 @@ def test_lora_bwd_w_refuses_unknown_types(L):  # noqa: F811
         assert call(L, "ep_lora_bwd_w", extra=(kind,)) == INVALID
 
 
+@pytest.mark.parametrize("dims", [(8, 8192), (8192, 8)], ids=str)
+def test_lora_bwd_w_refuses_both_gradients_where_one_passes_a_grid(L, dims):  # noqa: F811
+    """65536 adapters of 8 experts: 2^19 tiles of one gradient, 2^24 of the other.  The call
+    launches twice and answers before the first launch (and before it asks for a device)."""
+    big = lora(num_adapters=65536, rank=8)
+    assert cfg().num_experts == 8
+    assert call(L, "ep_lora_bwd_w", lo=big, i=dims[0], o=dims[1]) == INVALID
+
+
 def test_gated_nvfp4_refuses_weights_past_32_bit_offsets(L):  # noqa: F811
     assert call(L, "ep_expert_gated_nvfp4", i=1 << 20, o=1 << 14) == INVALID
 
