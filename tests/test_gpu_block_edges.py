@@ -1,9 +1,11 @@
 """The gated block and the products with adapters on the GPU where they are least
-ordinary: infinite adapters and rows."""
+ordinary: infinite adapters and rows, workgroups that go through many tiles of every
+height, batches of many slots."""
 
 import pytest
 import torch
 
+import test_gpu_expert_block as block
 from test_gpu_expert_block import Lora, words
 from test_gpu_expert_layer import G, Rows, filled, normal, nvfp4_weights  # noqa: F401
 
@@ -115,3 +117,86 @@ def test_infinite_rows_make_infinite_gradients(G, name, rank):  # noqa: F811
     for ga, gb in grads:
         same_kinds(ga, wa, "grad_a")
         same_kinds(gb, wb, "grad_b")
+
+
+# ---------------------------------------------------------------------------
+# Workgroups of many tiles, and batches of many slots
+# ---------------------------------------------------------------------------
+GROUPS = {  # rows of each expert
+    # tiles of every height: full ones and what is left over, of one height, of at most 128 and 32 rows
+    "mixed": (1100, 0, 900, 300, 180, 100, 20, 1),
+    # 16384 slots and more: the adapters' first products take tiles of 64 rows
+    "slots": (9000, 5001, 2300, 0, 127, 3, 0, 1),
+}
+
+
+class Groups(Rows):
+    """A layout of GROUPS, a slot a token, tokens of all experts in turn."""
+
+    def __init__(self, G, name):  # noqa: F811
+        ids = torch.cat([torch.full((n,), e, dtype=torch.int32) for e, n in enumerate(GROUPS[name])])
+        ids = ids[torch.randperm(len(ids), generator=torch.Generator().manual_seed(3))]
+        self.cfg = cfg = G.epx.EpConfig(num_tokens=len(ids), hidden=16, num_experts=len(GROUPS[name]), num_segments=2,
+                                        top_k=1, align=16)
+        cfg.recv_rows = G.epx.ep_query(cfg).min_recv_rows + 5
+        self.ids, self.lay = ids.cuda(), G.sentinel_layout(cfg)
+        G.epx.ep_dispatch_layout(cfg, self.ids, G.epx.workspace_for(cfg, "cuda:0"), self.lay)
+        self.T, self.K, self.R, self.experts = len(ids), 1, cfg.recv_rows, cfg.num_experts
+        self.rows, self.slots = self.lay.token_row.cpu().long().view(-1), torch.arange(self.T)
+        self.kept = torch.zeros(self.R, dtype=torch.bool)
+        self.kept[self.rows] = True
+        self.expert = ids.long()
+        self.probs = torch.rand(self.T, 1, generator=torch.Generator().manual_seed(4)).cuda()
+        self.w = self.probs.double().cpu().view(-1)
+
+
+@pytest.fixture
+def grouped(monkeypatch):
+    """The block's tests on layouts of GROUPS."""
+    monkeypatch.setattr(block, "Rows", Groups)
+    return block
+
+
+# 15 row tiles of "mixed" by 40 or 41 feature tiles: two and more of a workgroup's 256
+@pytest.mark.parametrize("n_in", [8, 136, 256, 328])
+@pytest.mark.parametrize("rank", [0, 8, 24])
+def test_gated_block_of_many_tiles(G, grouped, n_in, rank):  # noqa: F811
+    grouped.test_gated_forward_and_backward(G, "mixed", (n_in, 5128 if n_in % 64 else 5120), rank)
+
+
+@pytest.mark.parametrize("dims", [(8, 10248, 8), (136, 10248, 24), (256, 10240, 64), (10248, 136, 24), (10240, 256, 64),
+                                  (10248, 8, 8)], ids=str)
+def test_products_of_many_tiles(G, grouped, dims):  # noqa: F811
+    grouped.test_adapters_and_gradients(G, "mixed", dims)
+
+
+@pytest.mark.parametrize("dims", [(136, 264, 8), (72, 136, 24), (264, 72, 64), (40, 200, 128)], ids=str)
+def test_adapters_of_many_slots(G, grouped, dims):  # noqa: F811
+    grouped.test_adapters_and_gradients(G, "slots", dims)
+
+
+@pytest.mark.parametrize("rank", [8, 24, 64, 128])
+def test_u_does_not_depend_on_the_slots(G, rank):  # noqa: F811
+    """u and grad_u of a row alone, and among 16384 and more slots (tiles of 64 rows), of
+    other adapters: the same bits."""
+    n_in, n_out, n = 456, 328, 5
+    a, b = normal(6, n, 1, rank, n_in, std=n_in ** -0.5), normal(7, n, 1, n_out, rank)
+    scale = (0.5 + torch.rand(n, generator=torch.Generator().manual_seed(1))).cuda()
+    x1, gy1, seen = normal(1, 1, n_in), normal(2, 1, n_out), []
+    for T in (1, 16383, 16384, 17001):
+        cfg = G.epx.EpConfig(num_tokens=T, hidden=16, num_experts=1, num_segments=1, top_k=1)
+        cfg.recv_rows = T
+        lay = G.epx.Layout.empty(cfg, "cuda:0")
+        G.epx.ep_dispatch_layout(cfg, torch.zeros(T, dtype=torch.int32, device="cuda:0"), G.epx.workspace_for(cfg, "cuda:0"), lay)
+        of = torch.randint(-1, n, (T,), generator=torch.Generator().manual_seed(T), dtype=torch.int32)
+        of[T // 2] = 3
+        lora, at = G.epx.Adapters(of.cuda(), a, b, scale), lay.token_row.view(-1)[T // 2].item()
+        x, gy = normal(T, T, n_in), normal(T + 1, T, n_out)
+        x[at], gy[at] = x1[0], gy1[0]
+        u, gu = words(T, rank), words(T, rank)
+        G.epx.ep_lora_down(cfg, lay, x, lora, u)
+        G.epx.ep_lora_bwd_u(cfg, lay, gy, lora, gu)
+        seen.append((u[at].cpu(), gu[at].cpu()))
+    for other in seen[1:]:
+        for one, same in zip(seen[0], other):
+            assert torch.equal(one, same)
