@@ -1,4 +1,4 @@
-// The launches of one of the expert block's sources (SOURCE, a number: which one) over
+// The launches of one of the experts' sources (SOURCE, a number: which one) over
 // layouts and sizes where operands and tiles end, on the host.  Every operand ends with
 // its allocation.  Each case runs with loads to LDS that land at once and as late as the
 // waits allow, each with either of a workgroup's ends ahead: the results have to be the
@@ -9,8 +9,12 @@
 #include "expert_gated.hip"
 #elif SOURCE == 1
 #include "expert_lora.hip"
-#else
+#elif SOURCE == 2
 #include "expert_nvfp4_block.hip"
+#elif SOURCE == 3
+#include "expert_gemm.hip"
+#else
+#include "expert_nvfp4.hip"
 #endif
 
 using namespace epx;
@@ -209,6 +213,38 @@ void one(const std::vector<int32_t>& rows, bool shared, int32_t in, int32_t out,
         host::what = name("lora_bwd_w", rows, in, out, rank);
         compare({{ga, na * each}, {gb, nb * each}}, [&] { return launch_lora_bwd_w(a, gu, ga, gb, nullptr); });
     }
+#elif SOURCE == 3
+    if (rank != 0) return;
+    Layout l(rows, shared, in, out, 0, 0);
+    ExpertArgs& a = l.a.e;
+    const size_t nx = l.R() * in, ny = l.R() * out, nw = l.experts() * out * in;
+    a.x = values(nx);
+    a.gy = values(ny);
+    a.w = values(nw);
+    a.out = array<uint16_t>(ny);
+    for (int64_t slots : {l.R(), int64_t(1) << 16}) {  // by which the tiles' sizes are chosen
+        a.slots = slots;
+        a.out = array<uint16_t>(ny);
+        host::what = name("gemm", rows, in, out, rank);
+        compare({{a.out, ny * 2}}, [&] { return launch_expert_gemm(a, nullptr); });
+        a.out = array<uint16_t>(nx);
+        host::what = name("gemm_bwd_x", rows, in, out, rank);
+        compare({{a.out, nx * 2}}, [&] { return launch_expert_gemm_bwd_x(a, nullptr); });
+        a.out = array<uint16_t>(nw);
+        host::what = name("gemm_bwd_w", rows, in, out, rank);
+        compare({{a.out, nw * 2}}, [&] { return launch_expert_gemm_bwd_w(a, nullptr); });
+    }
+#elif SOURCE == 4
+    if (rank != 0) return;
+    Layout l(rows, shared, in, out, 0, 0);
+    ExpertArgs& a = l.a.e;
+    a.x = values(l.R() * in);
+    a.codes = bytes(l.experts() * out * in / 2);
+    a.scales = bytes(l.experts() * out * in / 16);
+    a.rowscale = values(l.experts() * out);
+    a.out = array<uint16_t>(l.R() * out);
+    host::what = name("gemm_nvfp4", rows, in, out, rank);
+    compare({{a.out, (size_t)l.R() * out * 2}}, [&] { return launch_expert_gemm_nvfp4(a, nullptr); });
 #else
     for (bool gated : {true, false}) {
         if (!gated && rank == 0) continue;
@@ -234,7 +270,7 @@ void one(const std::vector<int32_t>& rows, bool shared, int32_t in, int32_t out,
 
 }  // namespace
 
-// Arguments: the smallest of in_dim's multiples, then the in_dims, then "x", then the widths.
+// Arguments: the in_dims, "x", the widths.
 int main(int argc, char** argv) {
     host::start();
     std::vector<int32_t> ins, outs;

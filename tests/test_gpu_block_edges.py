@@ -1,13 +1,13 @@
 """The gated block and the products with adapters on the GPU where they are least
-ordinary: infinite adapters and rows, workgroups that go through many tiles of every
+ordinary: infinite adapters and rows, beside the calls that it replaces, workgroups that go through many tiles of every
 height, batches of many slots."""
 
 import pytest
 import torch
 
 import test_gpu_expert_block as block
-from test_gpu_expert_block import Lora, words
-from test_gpu_expert_layer import G, Rows, filled, normal, nvfp4_weights  # noqa: F401
+from test_gpu_expert_block import TINY, Lora, silu_parts, words
+from test_gpu_expert_layer import HALF_BF16, U32, G, Rows, check, filled, normal, nvfp4_weights  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -117,6 +117,61 @@ def test_infinite_rows_make_infinite_gradients(G, name, rank):  # noqa: F811
     for ga, gb in grads:
         same_kinds(ga, wa, "grad_a")
         same_kinds(gb, wb, "grad_b")
+
+
+# ---------------------------------------------------------------------------
+# Against the calls that the block replaces
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("name", ["one-top8", "odd", "aligned", "capacity", "tall"])
+@pytest.mark.parametrize("dims", [(8, 8), (136, 72), (264, 264)], ids=str)
+@pytest.mark.parametrize("rank", [0, 16])
+def test_the_block_is_the_product_and_the_activation(G, name, dims, rank):  # noqa: F811
+    """Forward and backward against ep_expert_gemm (or its form with adapters) and
+    ep_swiglu.  Those round h to bf16 in between, each of g and u by at most 2^-8 of its
+    value; how far that and the sums' own roundings carry is counted as for the block
+    itself, on both sides, and each result's rounding twice."""
+    n_in, inter = dims
+    d, e = Rows(G, name), G.epx
+    x, ga = normal(1, d.R, n_in), normal(2, d.R, inter)
+    w = normal(3, d.experts, 2 * inter, n_in, std=n_in ** -0.5)
+    h, act, act2, gh, gh2 = (filled(d.R, n) for n in (2 * inter, inter, inter, 2 * inter, 2 * inter))
+    gp, gp2 = (torch.full((d.T, d.K), float("nan"), device="cuda:0") for _ in range(2))
+    kw, u_size = {}, 0
+    if rank:
+        lora = Lora(G, d, rank, n_in, 2 * inter)
+        kw = dict(adapters=lora.c, u=words(d.R, rank))
+        e.ep_lora_down(d.cfg, d.lay, x, lora.c, kw["u"])
+        e.ep_expert_gemm_lora(d.cfg, d.lay, x, w, h, **kw)
+        u_size = kw["u"].cpu()[d.rows].double().abs().sum(1, keepdim=True) * lora.b.double().abs().max().item()
+    else:
+        e.ep_expert_gemm(d.cfg, d.lay, x, w, h)
+    e.ep_swiglu(d.cfg, d.lay, h, d.probs, act)
+    e.ep_swiglu_bwd(d.cfg, d.lay, h, d.probs, ga, gh, gp)
+    e.ep_expert_gated(d.cfg, d.lay, x, w, d.probs, act2, **kw)
+    e.ep_expert_gated_bwd(d.cfg, d.lay, x, w, d.probs, ga, gh2, grad_probs=gp2,
+                          workspace=e.gated_workspace_for(d.cfg, inter, "cuda:0"), **kw)
+    r, p = d.rows, d.w[:, None]
+    hr, gar = h.cpu()[r].double(), ga.cpu()[r].double()
+    # the same sums in another order on each side: (terms + 2) roundings of their size, as
+    # sum |x| |w|, at most the largest weight times sum |x|; u's as two bf16, 2^-16
+    size = x.cpu()[r].double().abs().sum(1, keepdim=True) * w.double().abs().max().item()
+    eh = hr.abs() * HALF_BF16 * 1.01 + 2 * size * (n_in + 4) * U32 + 2 * u_size * (2.0 ** -16 + (2 * rank + 4) * U32)
+    (g, v), (eg, ev) = hr.split(inter, 1), eh.split(inter, 1)
+    s, silu = silu_parts(g)
+    own = 2 * (32 + g.abs()) * U32
+    want = p * silu * v
+    e_act = p * (1.1 * eg * (v.abs() + ev) + silu.abs() * ev) + want.abs() * own + TINY
+    check(act2.cpu()[r], act.cpu()[r].double(), e_act + 2 * (want.abs() + e_act) * HALF_BF16 * 1.01, "act")
+    gabs = (p * gar).abs()
+    slope = s * (1 + g * torch.sigmoid(-g))
+    want = torch.cat([gabs * (v * slope).abs(), gabs * silu.abs()], 1)
+    e_h = torch.cat([gabs * (1.1 * ev + (v.abs() + ev) * 0.5 * eg), gabs * 1.1 * eg], 1)
+    e_h = e_h + torch.cat([gabs * v.abs() * (1 + g.abs()), gabs * g.abs()], 1) * torch.cat([own, own], 1) + TINY
+    check(gh2.cpu()[r], gh.cpu()[r].double(), e_h + 2 * (want + e_h) * HALF_BF16 * 1.01, "grad_h")
+    terms = gar.abs() * (1.1 * eg * (v.abs() + ev) + silu.abs() * ev + (silu * v).abs() * (own + 2 * inter * U32))
+    err = torch.zeros(d.T * d.cfg.kp, dtype=torch.float64)
+    err[d.slots] = terms.sum(1) + TINY
+    check(gp2, gp.cpu().double(), err.view(d.T, -1)[:, : d.K], "grad_probs")
 
 
 # ---------------------------------------------------------------------------

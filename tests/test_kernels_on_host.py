@@ -11,7 +11,7 @@ import pytest
 from combine_ep_dispatch_amd import build
 
 HERE = os.path.join(os.path.dirname(os.path.abspath(__file__)), "host")
-SOURCES = {"expert_gated": 0, "expert_lora": 1, "expert_nvfp4_block": 2}  # name, number in expert_block.cpp
+SOURCES = {"expert_gated": 0, "expert_lora": 1, "expert_nvfp4_block": 2, "expert_gemm": 3, "expert_nvfp4": 4}  # name, number in expert_block.cpp
 HEADERS = ("epx_device", "expert_device", "expert_tile", "expert_loop", "lora_device", "gated_device", "nvfp4_tile")
 
 # What the inline assembly does, in the host's words.
@@ -80,3 +80,9 @@ def test_products(programs, name):
 def test_four_bit_products(programs):
     """Widths of which a tile's last waves have nothing, and those that fill one."""
     run(programs["expert_nvfp4_block"], (16, 64, 272, 320), (8, 40, 56, 136))
+    run(programs["expert_nvfp4"], (16, 64, 272, 320), (8, 40, 136, 264))
+
+
+def test_products_without_an_end_of_their_own(programs):
+    """The products and both gradients, in small and in wide tiles."""
+    run(programs["expert_gemm"], (8, 136, 264), (8, 136))
