@@ -28,7 +28,9 @@ The expert layer around the two, on the same layout:
     y = d.combine(d.linear(act, w2), None)
 
 d.gated(recv, w1, probs) is d.swiglu(d.linear(recv, w1), probs) in one kernel that
-keeps neither h nor act's inputs: its backward pass makes h again.  linear and gated
+keeps neither h nor act's inputs: its backward pass makes h again, which saves h's
+memory and costs more time than keeping it (a step of 64 experts of 2048 x 1416, 49 152
+rows: 1.57 ms, by the two 1.28 ms and 201 MB).  linear and gated
 take Adapters (low-rank, a token's own each) beside the weights, differentiable in
 rows, w, adapters.a and adapters.b (a scale that asks for a gradient is refused);
 weights that need no gradient cost none.
@@ -355,7 +357,8 @@ class EpDispatcher:
     def gated(self, rows: torch.Tensor, w: torch.Tensor, probs: Optional[torch.Tensor],
               adapters: Optional[Adapters] = None) -> torch.Tensor:
         """swiglu(linear(rows, w, adapters), probs) in one kernel: rows [R, in], w bf16
-        [E (+1 shared), 2*inter, in] (gate rows, then up rows) -> [R, inter]."""
+        [E (+1 shared), 2*inter, in] (gate rows, then up rows) -> [R, inter].  Faster
+        forward; with gradients the two calls are, where h fits beside the rest."""
         a, b, of, scale = _parts(adapters)
         return _Gated.apply(_rows(rows), _rows(w), a, b, _weights(probs), of, scale, self.cfg, self.layout)
 

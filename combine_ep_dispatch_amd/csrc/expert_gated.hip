@@ -9,10 +9,13 @@
 //
 // Against the product and the activation apart, the rows' 2 I values of h are neither
 // written nor read.  The backward pass makes g and u again, which costs a product more
-// but keeps nothing of 2 I values a row from one pass to the next.
+// but keeps nothing of 2 I values a row from one pass to the next: forward and backward
+// the two calls take 1280 us where this takes 1570 (64 experts of 2048 x 1416, 49 152 rows).
+// grad_h is rounded to bf16, the type that the products behind it multiply: their
+// gradients are then off by 0.0023 of their norm, 0.0017 with grad_h in 32 bits.
 //
 // 32 experts of 4096 x 7168 (2 I x in): 128 rows 311 us, bound by reading 1.88 GB of
-// weights (6.0 TB/s); 32 768 rows 1490 to 1540 us, 1250 to 1290 TFLOP/s, where one
+// weights (6.0 TB/s); 32 768 rows 1490 to 1610 us, 1190 to 1290 TFLOP/s, where one
 // library product of as many operations reaches 1590.  Of a tile's time 89 % are its
 // 112 steps, each 2290 cycles of which 2048 are matrix instructions; 3400 cycles find
 // the tile, 2000 wait for its first step, 14 500 are the epilogue.  The backward

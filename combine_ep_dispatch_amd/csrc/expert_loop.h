@@ -40,14 +40,14 @@ constexpr int kKindRows[kKinds] = {kTileN, 128, 32};  // at most
 // as few tiles as can be, of one height: 896 rows are 4 of 224.  From five tiles on
 // they are full ones and what is left over, if that is at most half of one, which
 // then reads the weights once more.  32 experts of 4096 x 7168, us for one height and
-// for full tiles and the rest: 896 rows 1290 and 1450, 1040 rows 1645 and 1645, 996
+// for full tiles and the rest: 300 rows 605 and 750, 384 632 and 772, 520 918 and 1018,
+// 600 1053 and 1060, 776 1335 and 1381, 896 1328 and 1446, 1040 1645 and 1645, 996
 // to 1060 rows (a training step's) 1605 and 1510, where one height is 9 tiles a CU and
-// the other 8 and a rest.  Every wave
-// keeps, for the run of groups that each lane looks after, how many row tiles of
-// each kind come before and up to it; no memory but the layout's is used.  Of each
-// kind each XCD takes an eighth, in blocks of 4 row tiles by all feature tiles, whose
-// operands the workgroups that run together share in its L2, and hands them out in
-// turn.
+// the other 8 and a rest.  Every wave keeps, for the run of groups that each lane looks
+// after, how many row tiles of each kind come before and up to it; no memory but the
+// layout's is used.  Of each kind each XCD takes an eighth, in blocks of 4 row tiles by
+// all feature tiles, whose operands the workgroups that run together share in its L2,
+// and hands them out in turn.
 struct LoopTiles {
     int32_t before[kKinds], upto[kKinds];  // of this lane's groups
     int32_t total[kKinds], ftiles, per;

@@ -9,11 +9,11 @@
 // The second product of an adapter is added to the experts' own in the registers that
 // hold it, before anything is rounded; the adapters' rows need not be sorted.
 //
-// 32 experts of 4096 x 7168: 128 rows of 16 adapters of rank 16 331 us for u and the
+// 32 experts of 4096 x 7168: 128 rows of 16 adapters of rank 16 328 to 345 us for u and the
 // product, bound by reading 1.92 GB of weights; 16 experts of 2048 x 1416, 4092 rows,
-// every token another of 5 adapters, rank 64: 150 to 168 us.  A training step of 4
-// adapters of rank 16 over 32 experts of 2048 x 2048, 32 768 rows: 734 us, of which the
-// two products take 291 and 321 (940 and 860 TFLOP/s).
+// every token another of 5 adapters, rank 64: 145 to 170 us, of 16 290, of 256 850.  A
+// training step of 4 adapters of rank 16 over 32 experts of 2048 x 2048, 32 768 rows: 734
+// to 775 us, of which the two products take 278 and 310 (990 and 890 TFLOP/s); of 256 2660.
 #include "expert_loop.h"
 
 namespace epx {
@@ -241,8 +241,9 @@ constexpr int kLook = 4, kList = kLook * kGradThreads;               // rows tha
 // width in; result [rank, in]) or gy (out; result [out, rank]), v = gu or u.  The
 // rows are picked out in order, 64 a step; d's go through registers to LDS.  No
 // workgroup shares a result with another: the order of the sums is the rows'.
-// 32 experts, 4 adapters of rank 16, 32 768 rows of 2048: 44 to 46 us, bound by the
+// 32 experts, 4 adapters of rank 16, 32 768 rows of 2048: 41 to 46 us, bound by the
 // rows' reads (134 MB, 3.0 TB/s; 88 us with a step's loads behind the one before).
+// Every adapter's workgroups look through all rows of their expert.
 template <int KP, bool OUT>
 __global__ __launch_bounds__(kGradThreads, KP <= 2 ? 3 : KP == 4 ? 2 : 1)  // as many workgroups as LDS holds
 void k_lora_bwd_w(BlockArgs a, const float* v, void* out, int32_t ctiles) {

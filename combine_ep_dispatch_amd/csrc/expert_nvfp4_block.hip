@@ -1,7 +1,7 @@
 // The gated block over 4-bit weights, and the 4-bit product with adapters: the
 // tiles of the 4-bit product with other ends, and bound by what bounds that: 8 rows of 8
-// experts of 4096 x 7168 31 us, 576 rows of 65 249 us (4.4 TB/s), 3890 rows of 32 328 us
-// (700 TFLOP/s; conversions, LDS reads and matrix instructions overlap little).  With
+// experts of 4096 x 7168 31 us, 576 rows of 65 250 us (4.3 TB/s), 3890 rows of 32 328 to
+// 339 us (670 to 700 TFLOP/s; conversions, LDS reads and matrix instructions overlap little).  With
 // 8 adapters of rank 16 576 rows take 266 to 282: each (adapter, 32 values of rank) is a round
 // trip to memory behind the tile's last step.
 //   act[r, i] = w_r silu(g) u,  g = rowscale[e, i] sum_h x[r, h] e2m1 e4m3 (+ adapters),  u: row I + i

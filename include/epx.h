@@ -664,7 +664,8 @@ int ep_lora_bwd_w(const ep_cfg_t* cfg, const ep_layout_t* layout, const ep_lora_
  *   probs float [T, K] or NULL (w_r = 1; 1 in the shared slot as well);  act  bf16 [R, inter]
  *   lora  NULL, or adapters beside the stacked weights (B [.., 2*inter, rank]), added to g
  *         and u before the activation; ulora: ep_lora_down's of x (NULL without)
- * in_dim and inter: multiples of 8 in [8, EP_MAX_EXPERT_DIM].  Reads counts,
+ * in_dim and inter: multiples of 8 in [8, EP_MAX_EXPERT_DIM] (2*inter at most that where
+ * gradients of x and w are to follow).  Reads counts,
  * row_offsets, seg_base and src_info of the layout.
  */
 int ep_expert_gated(const ep_cfg_t* cfg, const ep_layout_t* layout, const ep_lora_t* lora, int32_t in_dim, int32_t inter,
@@ -688,7 +689,8 @@ int ep_expert_gated_nvfp4(const ep_cfg_t* cfg, const ep_layout_t* layout, const 
  *   grad_probs[t, k]     = sum_i ga silu(g) u   (k < K; 0 for masked, invalid and dropped
  *                          slots; float [T, K], or NULL to leave it out)
  *   act                  as the forward pass, or NULL to leave it out
- * and, from grad_h, the gradients of x and w by ep_expert_gemm_bwd_x and
+ * (ep_expert_gemm and ep_swiglu with their backward calls keep h instead and take less
+ * time in a training step) and, from grad_h, the gradients of x and w by ep_expert_gemm_bwd_x and
  * ep_expert_gemm_bwd_w (of the adapters by ep_lora_bwd_u and ep_lora_bwd_w).
  *   grad_act bf16 [R, inter];  grad_h bf16 [R, 2*inter]
  *   workspace: with grad_probs, at least T * K * ceil(inter / EP_GATED_PART) * 4
