@@ -689,9 +689,9 @@ int ep_expert_gated_nvfp4(const ep_cfg_t* cfg, const ep_layout_t* layout, const 
  *   grad_probs[t, k]     = sum_i ga silu(g) u   (k < K; 0 for masked, invalid and dropped
  *                          slots; float [T, K], or NULL to leave it out)
  *   act                  as the forward pass, or NULL to leave it out
- * (ep_expert_gemm and ep_swiglu with their backward calls keep h instead and take less
- * time in a training step) and, from grad_h, the gradients of x and w by ep_expert_gemm_bwd_x and
- * ep_expert_gemm_bwd_w (of the adapters by ep_lora_bwd_u and ep_lora_bwd_w).
+ * and, from grad_h, the gradients of x and w by ep_expert_gemm_bwd_x and
+ * ep_expert_gemm_bwd_w (of the adapters by ep_lora_bwd_u and ep_lora_bwd_w).  A training
+ * step of ep_expert_gemm and ep_swiglu with their backward calls keeps h and takes less time.
  *   grad_act bf16 [R, inter];  grad_h bf16 [R, 2*inter]
  *   workspace: with grad_probs, at least T * K * ceil(inter / EP_GATED_PART) * 4
  *              bytes, 16-byte aligned, of any content; not shared by calls that may
