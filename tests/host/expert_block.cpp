@@ -281,7 +281,7 @@ int main(int argc, char** argv) {
     for (int32_t in : ins)
         for (int32_t out : outs)
             for (size_t n = 0; n < kLayouts.size(); ++n)
-                for (int32_t rank : {0, 8, 40}) {
+                for (int32_t rank : {0, 40}) {
                     one(kLayouts[n], n % 2 == 1, in, out, rank);
                     host::free_all();
                     ++cases;
